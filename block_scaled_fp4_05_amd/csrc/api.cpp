@@ -48,6 +48,50 @@ int check_gemm_shape(int32_t num_experts, int64_t m_total, int64_t n, int64_t k)
   return MOE_FP4_OK;
 }
 
+// Byte sizes the few-token products address with 32-bit buffer offsets.
+constexpr int64_t kFewLimit = (int64_t)INT32_MAX - 4096;
+
+// Rows of a few-token linear call: 16 of them per workgroup row of the grid.
+constexpr int64_t kFewMaxRows = 16 * 65535;
+
+bool few_dtypes_ok(int x_dtype, int out_dtype) {
+  return (x_dtype == MOE_FP4_IN_BF16 || x_dtype == MOE_FP4_IN_FP16) &&
+         (out_dtype == MOE_FP4_OUT_BF16 || out_dtype == MOE_FP4_OUT_FP32 ||
+          out_dtype == MOE_FP4_OUT_FP16);
+}
+
+int64_t out_size(int out_dtype) { return out_dtype == MOE_FP4_OUT_FP32 ? 4 : 2; }
+
+bool few_k_ok(int64_t k) { return k % 16 == 0 && k >= 64; }
+
+bool few_rows_aligned(const void* x, int64_t ld_x, const void* residual, const void* out,
+                      int out_dtype) {
+  return aligned(x, 16) && ld_x % 8 == 0 && aligned(residual, 2) && aligned(out, out_size(out_dtype));
+}
+
+// x within 32-bit offsets, and the extents of residual and out representable.
+bool few_rows_fit(int64_t m, int64_t ld_x, int64_t ld_res, int64_t ldo) {
+  return ld_x <= kFewLimit / 2 / m && ld_res <= INT64_MAX / 8 / m && ldo <= INT64_MAX / 8 / m;
+}
+
+// The residual and the output are the same rows (each element is read by the thread
+// that writes it) or share no byte.
+bool residual_ok(const void* residual, int64_t ld_res, int x_dtype, const void* out, int out_dtype,
+                 int64_t ldo, int64_t m, int64_t cols) {
+  if (!residual) return true;
+  const bool same_type = (x_dtype == MOE_FP4_IN_BF16 && out_dtype == MOE_FP4_OUT_BF16) ||
+                         (x_dtype == MOE_FP4_IN_FP16 && out_dtype == MOE_FP4_OUT_FP16);
+  if (residual == out && same_type && (m == 1 || ld_res == ldo)) return true;
+  return !overlap(out, ((m - 1) * ldo + cols) * out_size(out_dtype), residual,
+                  ((m - 1) * ld_res + cols) * 2);
+}
+
+// End of the records in the layer's workspace: the count and one record per expert
+// that `pairs` slots can name.
+size_t ffn_records_end(int64_t pairs, int32_t experts) {
+  return 16 + 16 * (size_t)(pairs < experts ? pairs : experts);
+}
+
 }  // namespace
 
 extern "C" {
@@ -410,6 +454,133 @@ int moe_fp4_combine(const uint16_t* rows, int64_t ld_rows, int64_t m_total,
   a.ldo = ldo;
   a.f32_out = out_dtype == MOE_FP4_OUT_FP32 ? 1 : 0;
   hipError_t err = moe_fp4::launch_combine(a, reinterpret_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_FP4_OK : MOE_FP4_ERR_HIP;
+}
+
+int moe_fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ld_x, const uint8_t* w_q,
+                   const uint8_t* w_sf, const float* w_scale, int64_t n, int64_t k, int swiglu,
+                   const void* residual, int64_t ld_res, void* out, int out_dtype, int64_t ldo,
+                   void* stream) {
+  if (!few_dtypes_ok(x_dtype, out_dtype) || (swiglu != 0 && swiglu != 1)) return MOE_FP4_ERR_ARG;
+  if (!w_q || !w_sf || !w_scale || (m > 0 && (!x || !out))) return MOE_FP4_ERR_NULL;
+  const int64_t cols = swiglu ? n / 2 : n;
+  if (m < 0 || n < 1 || k < 1 || (swiglu && (n % 2 != 0 || residual))) return MOE_FP4_ERR_SHAPE;
+  if (m > 0 && (ld_x < k || ldo < cols || (residual && ld_res < n))) return MOE_FP4_ERR_SHAPE;
+  if (!aligned(w_q, 16) || !aligned(w_sf, 4) || !aligned(w_scale, 4)) return MOE_FP4_ERR_ALIGN;
+  if (m > 0 && !few_rows_aligned(x, ld_x, residual, out, out_dtype)) return MOE_FP4_ERR_ALIGN;
+  if (!few_k_ok(k) || k / 2 > kFewLimit / n || m > kFewMaxRows) return MOE_FP4_ERR_UNSUPPORTED;
+  if (m == 0) return MOE_FP4_OK;
+  if (!few_rows_fit(m, ld_x, residual ? ld_res : 0, ldo)) return MOE_FP4_ERR_UNSUPPORTED;
+  const int64_t ob = ((m - 1) * ldo + cols) * out_size(out_dtype);
+  if (overlap(out, ob, x, ((m - 1) * ld_x + k) * 2) || overlap(out, ob, w_q, n * (k / 2)) ||
+      overlap(out, ob, w_sf, n * (k / 16)) || overlap(out, ob, w_scale, 4) ||
+      !residual_ok(residual, ld_res, x_dtype, out, out_dtype, ldo, m, cols))
+    return MOE_FP4_ERR_ARG;
+  moe_fp4::LinearArgs a;
+  a.x = x;
+  a.ld_x = ld_x;
+  a.w_q = w_q;
+  a.w_sf = w_sf;
+  a.w_scale = w_scale;
+  a.residual = residual;
+  a.ld_res = ld_res;
+  a.out = out;
+  a.ldo = ldo;
+  a.m = (int32_t)m;
+  a.n = (int32_t)n;
+  a.k = (int32_t)k;
+  a.x_f16 = x_dtype == MOE_FP4_IN_FP16 ? 1 : 0;
+  a.swiglu = swiglu;
+  a.out_dtype = out_dtype;
+  hipError_t err = moe_fp4::launch_linear(a, reinterpret_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_FP4_OK : MOE_FP4_ERR_HIP;
+}
+
+size_t moe_fp4_ffn_workspace_size(int64_t tokens, int32_t topk, int32_t num_experts, int64_t inter) {
+  if (tokens < 1 || topk < 1 || num_experts < 1 || inter < 1) return 0;
+  if (tokens > moe_fp4::kFfnMaxTokens || topk > moe_fp4::kFfnMaxPairs / tokens ||
+      inter > kFewLimit / 4 / (tokens * topk))
+    return 0;
+  return ffn_records_end(tokens * topk, num_experts) + (size_t)(tokens * topk * inter * 4);
+}
+
+int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const int32_t* ids,
+                const float* weights, int32_t topk, const uint8_t* w13_q, const uint8_t* w13_sf,
+                const float* w13_scale, const uint8_t* w2_q, const uint8_t* w2_sf,
+                const float* w2_scale, int32_t num_experts, int64_t hidden, int64_t inter,
+                const void* residual, int64_t ld_res, void* out, int out_dtype, int64_t ldo,
+                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!few_dtypes_ok(x_dtype, out_dtype)) return MOE_FP4_ERR_ARG;
+  if (!w13_q || !w13_sf || !w13_scale || !w2_q || !w2_sf || !w2_scale) return MOE_FP4_ERR_NULL;
+  if (tokens > 0 && (!x || !ids || !weights || !out || !workspace)) return MOE_FP4_ERR_NULL;
+  if (tokens < 0 || topk < 1 || num_experts < 1 || hidden < 1 || inter < 1) return MOE_FP4_ERR_SHAPE;
+  if (tokens > 0 && (ld_x < hidden || ldo < hidden || (residual && ld_res < hidden)))
+    return MOE_FP4_ERR_SHAPE;
+  if (!aligned(w13_q, 16) || !aligned(w13_sf, 4) || !aligned(w13_scale, 4) || !aligned(w2_q, 16) ||
+      !aligned(w2_sf, 4) || !aligned(w2_scale, 4))
+    return MOE_FP4_ERR_ALIGN;
+  if (tokens > 0 && (!few_rows_aligned(x, ld_x, residual, out, out_dtype) || !aligned(ids, 4) ||
+                     !aligned(weights, 4) || !aligned(workspace, 16)))
+    return MOE_FP4_ERR_ALIGN;
+  if (!few_k_ok(hidden) || !few_k_ok(inter) || num_experts > kMaxExperts ||
+      inter > kFewLimit / hidden)
+    return MOE_FP4_ERR_UNSUPPORTED;
+  // Code bytes of one expert, multiples of 128: every expert's codes are aligned.
+  const int64_t w13_b = hidden * inter, w2_b = hidden * inter / 2;
+  if (tokens == 0) return MOE_FP4_OK;
+  if (!few_rows_fit(tokens, ld_x, residual ? ld_res : 0, ldo)) return MOE_FP4_ERR_UNSUPPORTED;
+  const size_t need = moe_fp4_ffn_workspace_size(tokens, topk, num_experts, inter);
+  if (need == 0) return MOE_FP4_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return MOE_FP4_ERR_SHAPE;
+  const int64_t ob = ((tokens - 1) * ldo + hidden) * out_size(out_dtype);
+  const int64_t pb = tokens * topk * 4, xb = ((tokens - 1) * ld_x + hidden) * 2;
+  struct {
+    const void* p;
+    int64_t bytes;
+  } const in[] = {{x, xb},
+                  {ids, pb},
+                  {weights, pb},
+                  {w13_q, num_experts * w13_b},
+                  {w13_sf, num_experts * (w13_b / 8)},
+                  {w13_scale, num_experts * (int64_t)4},
+                  {w2_q, num_experts * w2_b},
+                  {w2_sf, num_experts * (w2_b / 8)},
+                  {w2_scale, num_experts * (int64_t)4},
+                  {residual, residual ? ((tokens - 1) * ld_res + hidden) * 2 : 0}};
+  for (const auto& b : in) {
+    if (overlap(workspace, (int64_t)need, b.p, b.bytes)) return MOE_FP4_ERR_ARG;
+    if (b.p != residual && overlap(out, ob, b.p, b.bytes)) return MOE_FP4_ERR_ARG;
+  }
+  if (overlap(workspace, (int64_t)need, out, ob) ||
+      !residual_ok(residual, ld_res, x_dtype, out, out_dtype, ldo, tokens, hidden))
+    return MOE_FP4_ERR_ARG;
+  moe_fp4::FfnArgs a;
+  a.x = x;
+  a.ld_x = ld_x;
+  a.ids = ids;
+  a.weights = weights;
+  a.w13_q = w13_q;
+  a.w13_sf = w13_sf;
+  a.w13_scale = w13_scale;
+  a.w2_q = w2_q;
+  a.w2_sf = w2_sf;
+  a.w2_scale = w2_scale;
+  a.residual = residual;
+  a.ld_res = ld_res;
+  a.out = out;
+  a.ldo = ldo;
+  a.tokens = (int32_t)tokens;
+  a.topk = topk;
+  a.experts = num_experts;
+  a.hidden = (int32_t)hidden;
+  a.inter = (int32_t)inter;
+  a.x_f16 = x_dtype == MOE_FP4_IN_FP16 ? 1 : 0;
+  a.out_dtype = out_dtype;
+  char* ws = static_cast<char*>(workspace);
+  a.ranks = reinterpret_cast<int32_t*>(ws);
+  a.records = reinterpret_cast<int4*>(ws + 16);
+  a.h = ws + ffn_records_end(tokens * topk, num_experts);
+  hipError_t err = moe_fp4::launch_ffn(a, reinterpret_cast<hipStream_t>(stream));
   return err == hipSuccess ? MOE_FP4_OK : MOE_FP4_ERR_HIP;
 }
 

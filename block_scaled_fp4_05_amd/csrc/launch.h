@@ -150,6 +150,55 @@ size_t big_lds(int32_t num_experts);
 hipError_t launch_grouped_gemm_mid(const GemmArgs& args, hipStream_t stream);
 size_t mid_lds(int32_t num_experts);
 
+// Output types of the few-token products (the values of MOE_FP4_OUT_*).
+constexpr int32_t kFewOutF32 = 1;
+constexpr int32_t kFewOutF16 = 2;
+
+// Few-token linear layer (linear.hip); sizes checked so that every byte offset
+// into x and the weights is below 2^31.
+struct LinearArgs {
+  const void* x;  // BF16 or FP16 [m][ld_x]
+  int64_t ld_x;
+  const uint8_t* w_q;
+  const uint8_t* w_sf;
+  const float* w_scale;  // one float
+  const void* residual;  // x's type [m][ld_res] or NULL
+  int64_t ld_res;
+  void* out;
+  int64_t ldo;
+  int32_t m, n, k;
+  int32_t x_f16, swiglu, out_dtype;
+};
+hipError_t launch_linear(const LinearArgs& args, hipStream_t stream);
+
+// Few-token Mixture-of-Experts layer (ffn.hip).
+constexpr int32_t kFfnMaxTokens = 64;  // a wavefront's lanes stand for the tokens
+constexpr int32_t kFfnMaxPairs = 2048;  // ids and weights of every pair in LDS
+struct FfnArgs {
+  const void* x;  // BF16 or FP16 [tokens][ld_x]
+  int64_t ld_x;
+  const int32_t* ids;    // [tokens][topk]
+  const float* weights;  // [tokens][topk]
+  const uint8_t* w13_q;
+  const uint8_t* w13_sf;
+  const float* w13_scale;
+  const uint8_t* w2_q;
+  const uint8_t* w2_sf;
+  const float* w2_scale;
+  const void* residual;  // x's type [tokens][ld_res] or NULL
+  int64_t ld_res;
+  void* out;
+  int64_t ldo;
+  int32_t tokens, topk, experts, hidden, inter;
+  int32_t x_f16, out_dtype;
+  // Workspace: the number of experts in use, a 16-byte record for each, and the
+  // intermediate rows, 4 bytes a value.
+  int32_t* ranks;
+  int4* records;
+  char* h;
+};
+hipError_t launch_ffn(const FfnArgs& args, hipStream_t stream);
+
 // LDS a workgroup may use on gfx950.
 constexpr size_t kLdsBytes = 160 * 1024;
 

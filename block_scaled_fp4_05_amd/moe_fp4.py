@@ -17,13 +17,14 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_FP4_LIB") or os.path.join(_PKG, "libmoe_fp4.so")
 
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_HIP, ERR_ARG = range(7)
-OUT_BF16, OUT_FP32 = 0, 1
-IN_BF16, IN_FP32 = 0, 1
+OUT_BF16, OUT_FP32, OUT_FP16 = 0, 1, 2
+IN_BF16, IN_FP32, IN_FP16 = 0, 1, 2
 SCALE_STATIC, SCALE_DYNAMIC = 0, 1
 
 # Every symbol include/moe_fp4.h declares.
 EXPORTED = ("moe_fp4_quantize", "moe_grouped_gemm_fp4", "moe_grouped_gemm_fp4_packed",
             "moe_grouped_gemm_fp4_finalize", "moe_grouped_gemm_fp4_swiglu", "moe_fp4_combine",
+            "moe_fp4_linear", "moe_fp4_ffn", "moe_fp4_ffn_workspace_size",
             "moe_fp4_pack_weights", "moe_fp4_unpack_weights", "moe_grouped_gemm_fp4_plan",
             "moe_grouped_gemm_fp4_workspace_size", "moe_fp4_stage_bytes",
             "moe_fp4_status_string", "moe_fp4_abi_version")
@@ -68,6 +69,13 @@ def lib() -> ctypes.CDLL:
     L.moe_grouped_gemm_fp4_swiglu.restype = i
     L.moe_fp4_combine.argtypes = [vp, i64, i64, vp, vp, i32, i64, i64, vp, i64, vp, i, i64, vp]
     L.moe_fp4_combine.restype = i
+    L.moe_fp4_linear.argtypes = [vp, i, i64, i64, vp, vp, vp, i64, i64, i, vp, i64, vp, i, i64, vp]
+    L.moe_fp4_linear.restype = i
+    L.moe_fp4_ffn_workspace_size.argtypes = [i64, i32, i32, i64]
+    L.moe_fp4_ffn_workspace_size.restype = ctypes.c_size_t
+    L.moe_fp4_ffn.argtypes = [vp, i, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, i64, i64,
+                              vp, i64, vp, i, i64, vp, ctypes.c_size_t, vp]
+    L.moe_fp4_ffn.restype = i
     for f in (L.moe_fp4_pack_weights, L.moe_fp4_unpack_weights):
         f.argtypes = [vp, vp, i32, i64, i64, vp]
         f.restype = i
@@ -393,4 +401,113 @@ def combine(rows, token_rows, token_weights, out=None, residual=None, out_dtype=
                                out.stride(0), _stream(stream, dev))
     if st != OK:
         raise MoeFp4Error(st, "moe_fp4_combine")
+    return out
+
+
+_IN_TYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32, torch.float16: IN_FP16}
+_OUT_TYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32, torch.float16: OUT_FP16}
+
+
+def _few_rows(x, residual, out, out_dtype, cols):
+    """Check the activations, residual and output of a few-token call; returns
+    (x type, out, out type)."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("x: expected a bfloat16 or float16 tensor")
+    _need(x, "x", x.dtype, (None, None), rows=True)
+    m = x.shape[0]
+    if residual is not None:
+        _need(residual, "residual", x.dtype, (m, cols), rows=True)
+    if out is None:
+        out = torch.empty((m, cols), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: dtype {out.dtype}, expected {out_dtype}")
+    if out.dtype not in _OUT_TYPES:
+        raise ValueError(f"out: dtype {out.dtype}, expected bfloat16, float16 or float32")
+    _need(out, "out", out.dtype, (m, cols), rows=True)
+    return _IN_TYPES[x.dtype], out, _OUT_TYPES[out.dtype]
+
+
+def linear_raw(*args):
+    """moe_fp4_linear with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_linear(*args)
+
+
+def linear(x, w_q, w_sf, w_scale, swiglu: bool = False, residual=None, out=None, out_dtype=None,
+           stream=None):
+    """Few-token linear layer: x (bfloat16 or float16 CUDA tensor [m][k], unit column
+    stride) times NVFP4 weights w_q uint8 [n][k/2], w_sf uint8 [n][k/16], w_scale
+    float32 [1].  Returns out [m][n] = x W^T (+ residual, x's type [m][n]), or with swiglu
+    [m][n/2] = silu(first half) * second half; of out_dtype (default: x's type)."""
+    _need(w_q, "w_q", torch.uint8, (None, None))
+    n, kb = w_q.shape
+    if swiglu and (n % 2 or residual is not None):
+        raise ValueError("swiglu: needs an even number of weight rows and no residual")
+    dt, out, odt = _few_rows(x, residual, out, out_dtype, n // 2 if swiglu else n)
+    m, k = x.shape
+    if k != 2 * kb:
+        raise ValueError(f"w_q: shape {tuple(w_q.shape)}, expected (n, {k // 2})")
+    _need(w_sf, "w_sf", torch.uint8, (n, k // 16))
+    _need(w_scale, "w_scale", torch.float32, (_AtLeast(1),))
+    dev = _same_cuda("x w_q w_sf w_scale residual out", x, w_q, w_sf, w_scale, residual, out)
+    st = lib().moe_fp4_linear(_ptr(x), dt, m, x.stride(0) if m > 1 else k, _ptr(w_q), _ptr(w_sf),
+                              _ptr(w_scale), n, k, 1 if swiglu else 0, _ptr(residual),
+                              0 if residual is None else residual.stride(0) if m > 1 else n,
+                              _ptr(out), odt, out.stride(0) if m > 1 else out.shape[1],
+                              _stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_linear")
+    return out
+
+
+def ffn_raw(*args):
+    """moe_fp4_ffn with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_ffn(*args)
+
+
+def ffn_workspace_size(tokens: int, topk: int, num_experts: int, inter: int) -> int:
+    """Device workspace bytes of moe_ffn for these sizes (0 where it does not run)."""
+    return lib().moe_fp4_ffn_workspace_size(tokens, topk, num_experts, inter)
+
+
+def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, residual=None,
+            out=None, out_dtype=None, workspace=None, stream=None):
+    """A whole Mixture-of-Experts layer for up to 64 tokens: x (bfloat16 or float16 CUDA
+    tensor [tokens][hidden]), ids int32 / weights float32 [tokens][topk] (an id outside
+    [0, E) is skipped), NVFP4 weights w13 [E][2I][hidden] (gate rows, then up rows) and
+    w2 [E][hidden][I] with scales float32 [E].  Returns out [tokens][hidden] = (residual +)
+    the routing-weighted sum of the experts, of out_dtype (default: x's type).
+    workspace: uint8 CUDA tensor of ffn_workspace_size bytes (default: a new one)."""
+    _need(w13_q, "w13_q", torch.uint8, (None, None, None))
+    E, rows, hb = w13_q.shape
+    H, I = 2 * hb, rows // 2
+    dt, out, odt = _few_rows(x, residual, out, out_dtype, H)
+    T = x.shape[0]
+    _need(x, "x", x.dtype, (T, H), rows=True)
+    _need(w13_q, "w13_q", torch.uint8, (E, 2 * I, hb))
+    _need(ids, "ids", torch.int32, (T, None))
+    K = ids.shape[1]
+    _need(weights, "weights", torch.float32, (T, K))
+    _need(w13_sf, "w13_sf", torch.uint8, (E, 2 * I, H // 16))
+    _need(w13_scale, "w13_scale", torch.float32, (E,))
+    _need(w2_q, "w2_q", torch.uint8, (E, H, I // 2))
+    _need(w2_sf, "w2_sf", torch.uint8, (E, H, I // 16))
+    _need(w2_scale, "w2_scale", torch.float32, (E,))
+    need = ffn_workspace_size(T, K, E, I)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if stream is not None and workspace.is_cuda:
+            # Freed on return: not to be handed out again before this stream is done with it.
+            workspace.record_stream(stream)
+    _need(workspace, "workspace", torch.uint8, (_AtLeast(need),))
+    dev = _same_cuda("x ids weights w13_q w13_sf w13_scale w2_q w2_sf w2_scale residual out workspace",
+                     x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, residual, out,
+                     workspace)
+    st = lib().moe_fp4_ffn(_ptr(x), dt, T, x.stride(0) if T > 1 else H, _ptr(ids), _ptr(weights), K,
+                           _ptr(w13_q), _ptr(w13_sf), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_sf),
+                           _ptr(w2_scale), E, H, I, _ptr(residual),
+                           0 if residual is None else residual.stride(0) if T > 1 else H, _ptr(out),
+                           odt, out.stride(0) if T > 1 else H, _ptr(workspace), workspace.numel(),
+                           _stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_ffn")
     return out

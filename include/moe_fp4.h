@@ -56,8 +56,9 @@ enum {
                                /* buffers that must be distinct overlap              */
 };
 
-/* Input element types of moe_fp4_quantize. */
-enum { MOE_FP4_IN_BF16 = 0, MOE_FP4_IN_FP32 = 1 };
+/* Input element types of moe_fp4_quantize (BF16, FP32), of the few-token entry points
+ * (BF16, FP16) and of the router (all three). */
+enum { MOE_FP4_IN_BF16 = 0, MOE_FP4_IN_FP32 = 1, MOE_FP4_IN_FP16 = 2 };
 
 /* Tensor-scale modes of moe_fp4_quantize. */
 enum {
@@ -320,8 +321,9 @@ int moe_grouped_gemm_fp4_swiglu(const uint8_t* a_q, const uint8_t* a_sf, const f
                                 int64_t m_total, int64_t n, int64_t k, const float* h_scale,
                                 uint8_t* h_q, uint8_t* h_sf, void* stream);
 
-/* Output element types of moe_fp4_combine. */
-enum { MOE_FP4_OUT_BF16 = 0, MOE_FP4_OUT_FP32 = 1 };
+/* Output element types of moe_fp4_combine (BF16, FP32) and of the few-token entry
+ * points (all three). */
+enum { MOE_FP4_OUT_BF16 = 0, MOE_FP4_OUT_FP32 = 1, MOE_FP4_OUT_FP16 = 2 };
 
 /*
  * moe_fp4_combine -- the Mixture-of-Experts finalize step as a pass of its own:
@@ -358,6 +360,78 @@ int moe_fp4_combine(const uint16_t* rows, int64_t ld_rows, int64_t m_total,
                     const int32_t* token_rows, const float* token_weights, int32_t topk,
                     int64_t num_tokens, int64_t n, const float* residual, int64_t ld_res,
                     void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * moe_fp4_linear -- a linear layer of a few tokens with NVFP4 weights and 16-bit
+ * activations (no activation quantisation): projections, the dense or shared expert,
+ * the vocabulary head of a decode step.  With
+ *
+ *     y[t][j] = *w_scale * sum_k x[t][k] * E2M1(w_q code) * E4M3(w_sf[j][k/16])
+ *
+ * (weights exact in x's type, sums in FP32):
+ *   swiglu = 0:  out[t][j] = y[t][j] + (residual ? residual[t][j] : 0),  j < n
+ *   swiglu = 1:  out[t][i] = silu(y[t][i]) * y[t][n/2 + i],              i < n/2
+ * rounded once, to out_dtype, nearest even.  Deterministic.  The weights are read
+ * once for every 16 tokens (32 from 17 tokens on), so the call is meant for a few dozen
+ * tokens.
+ *   x         device, [m][ld_x] of x_dtype (MOE_FP4_IN_BF16 or _FP16), 16-byte
+ *             aligned, ld_x >= k and a multiple of 8.
+ *   m         0 .. 16 * 65535 (0 is a no-op).
+ *   w_q       device, [n][k/2] row-major codes, 16-byte aligned; w_sf [n][k/16],
+ *             4-byte aligned; w_scale one float.
+ *   n         >= 1 (no other condition), even with swiglu.
+ *   k         a multiple of 16, at least 64.
+ *   residual  device, [m][ld_res] of x_dtype, 2-byte aligned, ld_res >= n, or NULL;
+ *             not with swiglu.  out may be the same buffer (same type and pitch).
+ *   out       device, [m][ldo] of out_dtype, aligned to its element, ldo >= n (n/2
+ *             with swiglu); columns past that are not touched.
+ * Errors: NULL, SHAPE (m < 0, n < 1, k < 1, a pitch below its row, n odd or residual given with
+ * swiglu), ALIGN, ARG (x_dtype, out_dtype, swiglu not 0 or 1; out overlapping x or the
+ * weights), UNSUPPORTED (k % 16, k < 64, m > 16 * 65535, n * k/2 or m * ld_x * 2 >=
+ * 2^31 - 4096), HIP.
+ */
+int moe_fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ld_x, const uint8_t* w_q,
+                   const uint8_t* w_sf, const float* w_scale, int64_t n, int64_t k, int swiglu,
+                   const void* residual, int64_t ld_res, void* out, int out_dtype, int64_t ldo,
+                   void* stream);
+
+/*
+ * moe_fp4_ffn -- a whole Mixture-of-Experts feed-forward layer of a few tokens, in
+ * two kernels, with NVFP4 weights and 16-bit activations:
+ *
+ *     (g, u)  = the two halves of w13_scale[e] * W13[e] x[t]      (I values each)
+ *     out[t]  = (residual[t] +) sum_s weights[t][s] * w2_scale[e] * W2[e] (silu(g) * u),
+ *               e = ids[t][s], over the slots with 0 <= e < num_experts
+ *
+ * Sums in FP32; the intermediate silu(g) * u, times its weight, is carried in two BF16
+ * parts (2^-17 relative); one rounding, to out_dtype, at the end.  A token may name an
+ * expert more than once (the weights add).  A token without a valid slot leaves its
+ * residual, or 0.  Experts are summed in ascending order: deterministic.  Weights
+ * of experts that no token names are not read, and whatever they hold touches no
+ * output.
+ *   x, residual, out, x_dtype, out_dtype as moe_fp4_linear, with rows of `hidden`.
+ *   tokens     0 .. 64 (0 is a no-op); for more, the grouped GEMM chain.
+ *   ids        device, [tokens][topk] int32; weights device, [tokens][topk] float.
+ *   w13_q      device, [num_experts][2I][hidden/2], rows 0 .. I-1 the gate, I .. 2I-1
+ *              the up projection; w13_sf [num_experts][2I][hidden/16]; w13_scale
+ *              [num_experts] floats.
+ *   w2_q       device, [num_experts][hidden][I/2]; w2_sf [num_experts][hidden][I/16];
+ *              w2_scale [num_experts].  Codes 16-byte aligned, scales 4-byte.
+ *   hidden, inter (= I): multiples of 16, at least 64.
+ *   workspace  device, moe_fp4_ffn_workspace_size bytes, 16-byte aligned; written
+ *              before it is read, holds nothing between calls.  Calls that may run
+ *              at once need one each.
+ * Errors: as moe_fp4_linear, plus SHAPE (num_experts < 1, topk < 1, tokens < 0, workspace
+ * too small), UNSUPPORTED (tokens > 64, tokens * topk > 2048, num_experts > 8192, one
+ * expert's weights or the intermediate 2^31 - 4096 bytes or larger).
+ */
+size_t moe_fp4_ffn_workspace_size(int64_t tokens, int32_t topk, int32_t num_experts, int64_t inter);
+int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const int32_t* ids,
+                const float* weights, int32_t topk, const uint8_t* w13_q, const uint8_t* w13_sf,
+                const float* w13_scale, const uint8_t* w2_q, const uint8_t* w2_sf,
+                const float* w2_scale, int32_t num_experts, int64_t hidden, int64_t inter,
+                const void* residual, int64_t ld_res, void* out, int out_dtype, int64_t ldo,
+                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * moe_grouped_gemm_fp4_workspace_size -- device workspace bytes the grouped GEMM
