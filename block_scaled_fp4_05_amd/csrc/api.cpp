@@ -92,6 +92,16 @@ size_t ffn_records_end(int64_t pairs, int32_t experts) {
   return 16 + 16 * (size_t)(pairs < experts ? pairs : experts);
 }
 
+// Tokens of a router block: one per wavefront for a few thousand tokens, more for more,
+// so that the blocks whose counts every block reads stay near 256.
+int64_t route_block(int64_t tokens) {
+  int64_t b = 16;
+  while (b < moe_fp4::kRouteMaxBlock && b * 256 < tokens) b *= 2;
+  return b;
+}
+
+int32_t route_pitch(int32_t experts) { return (experts + 7) / 8 * 8; }
+
 }  // namespace
 
 extern "C" {
@@ -581,6 +591,86 @@ int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const 
   a.records = reinterpret_cast<int4*>(ws + 16);
   a.h = ws + ffn_records_end(tokens * topk, num_experts);
   hipError_t err = moe_fp4::launch_ffn(a, reinterpret_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_FP4_OK : MOE_FP4_ERR_HIP;
+}
+
+size_t moe_fp4_route_workspace_size(int64_t tokens, int32_t num_experts) {
+  if (tokens <= moe_fp4::kRouteOneBlock || num_experts < 1 || num_experts > 1024 ||
+      tokens > kFewLimit)
+    return 0;
+  const int64_t block = route_block(tokens);
+  return (size_t)((tokens + block - 1) / block) * route_pitch(num_experts) * 2;
+}
+
+int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_experts, int64_t ld,
+                  int score, const float* bias, int renormalize, int32_t topk, int32_t num_groups,
+                  int32_t topk_groups, int32_t* ids, float* weights, int32_t* offsets,
+                  int32_t* row_token, int32_t* token_rows, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (dtype != MOE_FP4_IN_BF16 && dtype != MOE_FP4_IN_FP32 && dtype != MOE_FP4_IN_FP16)
+    return MOE_FP4_ERR_ARG;
+  if ((score != MOE_FP4_SCORE_SOFTMAX && score != MOE_FP4_SCORE_SIGMOID) ||
+      (renormalize != 0 && renormalize != 1) || (bias && score != MOE_FP4_SCORE_SIGMOID))
+    return MOE_FP4_ERR_ARG;
+  if (!offsets || (tokens > 0 && (!logits || !ids || !weights || !row_token || !token_rows)))
+    return MOE_FP4_ERR_NULL;
+  if (tokens < 0 || num_experts < 1 || num_groups < 1 || num_experts % num_groups != 0 ||
+      topk_groups < 1 || topk_groups > num_groups || topk < 1 ||
+      topk > (int64_t)(num_experts / num_groups) * topk_groups || (tokens > 0 && ld < num_experts))
+    return MOE_FP4_ERR_SHAPE;
+  const int64_t esize = dtype == MOE_FP4_IN_FP32 ? 4 : 2;
+  if (!aligned(logits, esize) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(token_rows, 4) ||
+      !aligned(workspace, 16))
+    return MOE_FP4_ERR_ALIGN;
+  if (num_experts > 1024 || topk > 32 || num_groups > 64) return MOE_FP4_ERR_UNSUPPORTED;
+  int32_t group_lanes = 64;
+  while (group_lanes * num_groups > 64) group_lanes /= 2;
+  const int32_t per_lane = (num_experts / num_groups + group_lanes - 1) / group_lanes;
+  if (per_lane > moe_fp4::kRouteMaxPerLane) return MOE_FP4_ERR_UNSUPPORTED;
+  if (tokens > 0 && (tokens > kFewLimit / topk || ld > kFewLimit / tokens))
+    return MOE_FP4_ERR_UNSUPPORTED;
+  const size_t need = moe_fp4_route_workspace_size(tokens, num_experts);
+  if (need > 0 && !workspace) return MOE_FP4_ERR_NULL;
+  if (workspace_bytes < need) return MOE_FP4_ERR_SHAPE;
+  const int64_t pb = tokens * topk * 4;
+  struct {
+    const void* p;
+    int64_t bytes;
+  } const bufs[] = {{logits, tokens > 0 ? ((tokens - 1) * ld + num_experts) * esize : 0},
+                    {bias, bias ? num_experts * (int64_t)4 : 0},
+                    {ids, pb},
+                    {weights, pb},
+                    {row_token, pb},
+                    {token_rows, pb},
+                    {offsets, (num_experts + 1) * (int64_t)4},
+                    {workspace, (int64_t)need}};
+  for (int i = 2; i < 8; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes)) return MOE_FP4_ERR_ARG;
+  moe_fp4::RouteArgs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  a.offsets = offsets;
+  a.row_token = row_token;
+  a.token_rows = token_rows;
+  a.counts = static_cast<uint16_t*>(workspace);
+  a.dtype = dtype;
+  a.tokens = (int32_t)tokens;
+  a.experts = num_experts;
+  a.topk = topk;
+  a.num_groups = num_groups;
+  a.topk_groups = topk_groups;
+  a.sigmoid = score == MOE_FP4_SCORE_SIGMOID ? 1 : 0;
+  a.renormalize = renormalize;
+  a.group_lanes = group_lanes;
+  a.per_lane = per_lane;
+  a.block_tokens = (int32_t)route_block(tokens);
+  a.counts_pitch = route_pitch(num_experts);
+  hipError_t err = moe_fp4::launch_route(a, reinterpret_cast<hipStream_t>(stream));
   return err == hipSuccess ? MOE_FP4_OK : MOE_FP4_ERR_HIP;
 }
 

@@ -199,6 +199,30 @@ struct FfnArgs {
 };
 hipError_t launch_ffn(const FfnArgs& args, hipStream_t stream);
 
+// Router (route.hip).
+constexpr int32_t kRouteF32 = 1, kRouteF16 = 2;  // the values of MOE_FP4_IN_*
+constexpr int32_t kRouteMaxPerLane = 16;   // experts a lane holds
+constexpr int32_t kRouteOneBlock = 32;     // tokens of the single-launch form
+constexpr int32_t kRouteMaxBlock = 512;    // tokens of a block: 16 words of marks an expert
+struct RouteArgs {
+  const void* logits;  // [tokens][ld] of dtype
+  int64_t ld;
+  const float* bias;  // [experts] or NULL
+  int32_t* ids;       // [tokens][topk]
+  float* weights;     // [tokens][topk]
+  int32_t* offsets;   // [experts + 1]
+  int32_t* row_token;   // [tokens * topk]
+  int32_t* token_rows;  // [tokens][topk]
+  uint16_t* counts;     // workspace: [blocks][counts_pitch]
+  int32_t dtype, tokens, experts, topk, num_groups, topk_groups;
+  int32_t sigmoid, renormalize;
+  int32_t group_lanes;   // lanes of one group, a power of two
+  int32_t per_lane;      // consecutive experts of one lane
+  int32_t block_tokens;  // tokens of a block
+  int32_t counts_pitch;  // experts rounded up to 8
+};
+hipError_t launch_route(const RouteArgs& args, hipStream_t stream);
+
 // LDS a workgroup may use on gfx950.
 constexpr size_t kLdsBytes = 160 * 1024;
 

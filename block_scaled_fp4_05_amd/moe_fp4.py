@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -20,11 +21,13 @@ OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_HIP, ERR_ARG = range(7)
 OUT_BF16, OUT_FP32, OUT_FP16 = 0, 1, 2
 IN_BF16, IN_FP32, IN_FP16 = 0, 1, 2
 SCALE_STATIC, SCALE_DYNAMIC = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 # Every symbol include/moe_fp4.h declares.
 EXPORTED = ("moe_fp4_quantize", "moe_grouped_gemm_fp4", "moe_grouped_gemm_fp4_packed",
             "moe_grouped_gemm_fp4_finalize", "moe_grouped_gemm_fp4_swiglu", "moe_fp4_combine",
-            "moe_fp4_linear", "moe_fp4_ffn", "moe_fp4_ffn_workspace_size",
+            "moe_fp4_linear", "moe_fp4_ffn", "moe_fp4_ffn_workspace_size", "moe_fp4_route",
+            "moe_fp4_route_workspace_size",
             "moe_fp4_pack_weights", "moe_fp4_unpack_weights", "moe_grouped_gemm_fp4_plan",
             "moe_grouped_gemm_fp4_workspace_size", "moe_fp4_stage_bytes",
             "moe_fp4_status_string", "moe_fp4_abi_version")
@@ -76,6 +79,11 @@ def lib() -> ctypes.CDLL:
     L.moe_fp4_ffn.argtypes = [vp, i, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, i64, i64,
                               vp, i64, vp, i, i64, vp, ctypes.c_size_t, vp]
     L.moe_fp4_ffn.restype = i
+    L.moe_fp4_route_workspace_size.argtypes = [i64, i32]
+    L.moe_fp4_route_workspace_size.restype = ctypes.c_size_t
+    L.moe_fp4_route.argtypes = [vp, i, i64, i32, i64, i, vp, i, i32, i32, i32, vp, vp, vp, vp, vp,
+                                vp, ctypes.c_size_t, vp]
+    L.moe_fp4_route.restype = i
     for f in (L.moe_fp4_pack_weights, L.moe_fp4_unpack_weights):
         f.argtypes = [vp, vp, i32, i64, i64, vp]
         f.restype = i
@@ -510,4 +518,75 @@ def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, re
                            _stream(stream, dev))
     if st != OK:
         raise MoeFp4Error(st, "moe_fp4_ffn")
+    return out
+
+
+class Routing(NamedTuple):
+    """What the router leaves on the GPU: ids / weights / token_rows [tokens][topk],
+    offsets [E + 1], row_token [tokens * topk] (moe_fp4_route)."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    row_token: torch.Tensor
+    token_rows: torch.Tensor
+
+
+def route_raw(*args):
+    """moe_fp4_route with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_route(*args)
+
+
+def route_workspace_size(tokens: int, num_experts: int) -> int:
+    """Device workspace bytes of route for these sizes."""
+    return lib().moe_fp4_route_workspace_size(tokens, num_experts)
+
+
+def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: bool = True,
+          num_groups: int = 1, topk_groups: int | None = None, out: Routing | None = None,
+          workspace=None, stream=None) -> Routing:
+    """The router: gate logits (float32, bfloat16 or float16 CUDA tensor [tokens][E], unit
+    column stride) to each token's topk experts, their weights and the routed rows
+    grouped by expert.  score "softmax" or "sigmoid" (ranked by score + bias, float32
+    [E]); num_groups / topk_groups limit the choice to the best groups of experts.
+    Routing.offsets and .row_token are grouped_gemm's offsets and a_row_index,
+    .token_rows and .weights combine's; .ids and .weights moe_ffn's."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _IN_TYPES:
+        raise ValueError("logits: expected a float32, bfloat16 or float16 tensor")
+    _need(logits, "logits", logits.dtype, (None, None), rows=True)
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score: {score!r}, expected 'softmax' or 'sigmoid'")
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    if topk < 1:
+        raise ValueError(f"topk: {topk}, expected at least 1")
+    if out is None:
+        i32, d = torch.int32, logits.device
+        out = Routing(torch.empty((T, topk), dtype=i32, device=d),
+                      torch.empty((T, topk), dtype=torch.float32, device=d),
+                      torch.empty(E + 1, dtype=i32, device=d),
+                      torch.empty(T * topk, dtype=i32, device=d),
+                      torch.empty((T, topk), dtype=i32, device=d))
+    _need(out.ids, "ids", torch.int32, (T, topk))
+    _need(out.weights, "weights", torch.float32, (T, topk))
+    _need(out.offsets, "offsets", torch.int32, (E + 1,))
+    _need(out.row_token, "row_token", torch.int32, (T * topk,))
+    _need(out.token_rows, "token_rows", torch.int32, (T, topk))
+    need = route_workspace_size(T, E)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+        if stream is not None and workspace.is_cuda:
+            workspace.record_stream(stream)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, (_AtLeast(need),))
+    dev = _same_cuda("logits bias ids weights offsets row_token token_rows workspace", logits, bias,
+                     *out, workspace)
+    st = lib().moe_fp4_route(
+        _ptr(logits), _IN_TYPES[logits.dtype], T, E, logits.stride(0) if T > 1 else E,
+        SCORE_SIGMOID if score == "sigmoid" else SCORE_SOFTMAX, _ptr(bias), 1 if renormalize else 0,
+        topk, num_groups, num_groups if topk_groups is None else topk_groups, _ptr(out.ids),
+        _ptr(out.weights), _ptr(out.offsets), _ptr(out.row_token), _ptr(out.token_rows),
+        _ptr(workspace), need, _stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_route")
     return out

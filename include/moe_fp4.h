@@ -433,6 +433,50 @@ int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const 
                 const void* residual, int64_t ld_res, void* out, int out_dtype, int64_t ldo,
                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* Scores of moe_fp4_route. */
+enum { MOE_FP4_SCORE_SOFTMAX = 0, MOE_FP4_SCORE_SIGMOID = 1 };
+
+/*
+ * moe_fp4_route -- the Mixture-of-Experts router: from gate logits to each token's
+ * topk experts and weights, and the routed rows grouped by expert as the grouped GEMM
+ * (expert_offsets, a_row_index = row_token) and moe_fp4_combine (token_rows) take them.
+ *
+ *   SOFTMAX   p[e] = e^x[e] / sum e^x over all experts; experts are ranked by x.
+ *   SIGMOID   p[e] = 1 / (1 + e^-x[e]); ranked by p[e] + bias[e] (or p[e]), in binary64.
+ *   groups    num_groups > 1 splits the experts into equal consecutive groups; only the best
+ *             topk_groups groups are eligible.  A group's score is its largest
+ *             ranking value (SOFTMAX) or the sum of its two largest (SIGMOID).
+ *   ties      go to the lower index, in both choices.  A NaN ranks below every number.
+ *   weights   p of the chosen experts (the bias plays no part); renormalize: divided by
+ *             their sum (with SOFTMAX, the softmax over the chosen experts).
+ *   slots     in descending order of the ranking value.
+ *   rows      all (token, slot) pairs ordered by expert, then token: expert e owns rows
+ *             [offsets[e], offsets[e + 1]); row r is of token row_token[r]; slot s of
+ *             token t has row token_rows[t][s].
+ * Deterministic.  One launch up to 32 tokens, two above.
+ *   logits     device, [tokens][ld] of dtype (MOE_FP4_IN_BF16, _FP32 or _FP16), aligned to
+ *              its element, ld >= num_experts.
+ *   tokens     >= 0 (0 writes the offsets, all 0).
+ *   bias       device, [num_experts] float, or NULL; SIGMOID only.
+ *   topk       1 .. 32, at most num_experts / num_groups * topk_groups.
+ *   ids, weights, token_rows  device, [tokens][topk] int32 / float / int32;
+ *   row_token  device, [tokens * topk] int32; offsets device, [num_experts + 1] int32.
+ *   workspace  device, moe_fp4_route_workspace_size bytes (0 up to 32 tokens, NULL then
+ *              allowed), 16-byte aligned; holds nothing between calls.
+ * Errors: NULL, SHAPE (tokens < 0, num_experts < 1, ld < num_experts, num_groups < 1 or not a
+ * divisor of num_experts, topk_groups outside 1 .. num_groups, topk < 1 or more than
+ * the eligible experts, workspace too small), ALIGN, ARG (dtype, score, renormalize not 0 or
+ * 1, a bias with SOFTMAX, an output overlapping another buffer), UNSUPPORTED (num_experts > 1024, topk > 32,
+ * num_groups > 64 or groups of more experts than 16 for each of the group's lanes (64 /
+ * num_groups rounded down to a power of two), tokens * topk or tokens * ld >= 2^31 - 4096), HIP.
+ */
+size_t moe_fp4_route_workspace_size(int64_t tokens, int32_t num_experts);
+int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_experts, int64_t ld,
+                  int score, const float* bias, int renormalize, int32_t topk, int32_t num_groups,
+                  int32_t topk_groups, int32_t* ids, float* weights, int32_t* offsets,
+                  int32_t* row_token, int32_t* token_rows, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /*
  * moe_grouped_gemm_fp4_workspace_size -- device workspace bytes the grouped GEMM
  * entry points need for these sizes.  Always 0: every kernel builds its work
