@@ -7,12 +7,18 @@
 // consecutive weight rows of one token.  The order of K inside a product is free
 // as long as both operands agree: a wavefront takes 256 elements of K per step
 // and lane group g the 64 consecutive ones at 64 g, so that a lane's codes are two
-// 16-byte loads, its four block scales one dword and its activations eight
-// 16-byte loads, and the four lanes of a row read 128 consecutive bytes.
+// 16-byte loads and its four block scales one dword.
 //
-// Any K that is a multiple of 16 and at least 64 runs without a narrow path: a
-// lane whose 64 elements would pass the end of the row reads the row's last 64
-// instead and drops the blocks that other lanes own (scale and activations 0).
+// What reaches a lane through LDS, private to its wavefront (no barriers):
+//   - activations: loaded in whole 512-byte pieces of a token's row and read back as
+//     operands.  Loading operands straight from memory costs eight instructions a step
+//     whatever the token count, each touching 64 places.
+//   - block scales: one load covers four steps (64 bytes of each row); a dword a
+//     step and lane touches as many lines as the codes do for an eighth of the bytes.
+//
+// Any K that is a multiple of 16 and at least 64 runs: a lane whose 64 elements pass
+// the end of the row reads the row's last 64 and moves them down; scales and
+// activations past the end are zeros.
 #pragma once
 
 #include "fp4_device.h"
@@ -23,7 +29,6 @@ namespace moe_fp4 {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kFewStep = 256;  // elements of K per wavefront step
-constexpr int kFewRows = 16;   // weight rows, and tokens, of one matrix product
 
 // Eight codes (one dword) times one block scale as eight exact 16-bit values: the
 // product has at most 6 significant bits and lies in [2^-10, 2688], inside both
@@ -62,67 +67,68 @@ __device__ __forceinline__ float4_t mfma16(u32x4_t a, u32x4_t b, float4_t c) {
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// Where a lane's 64 elements of a step start, and how many of their four blocks
-// (the first ones) belong to other lanes.
-struct LaneK {
-  int32_t k;
-  int32_t skip;  // 0..4
-};
-
-__device__ __forceinline__ LaneK lane_k(int32_t step, int32_t g, int32_t k) {
-  const int32_t k0 = step * kFewStep + 64 * g;
-  const int32_t last = k - 64;
-  LaneK r;
-  r.k = k0 < last ? k0 : last;
-  const int32_t over = (k0 - r.k) >> 4;
-  r.skip = over < 4 ? over : 4;
-  return r;
+// Blocks (0..4) of a row that lie in a lane's 64 elements from k0.
+__device__ __forceinline__ int32_t blocks_left(int32_t k0, int32_t k) {
+  const int32_t b = (k - k0) >> 4;
+  return b < 0 ? 0 : b < 4 ? b : 4;
 }
 
-// One step of NT x 16 weight rows in registers.
+// The codes of a step for NT x 16 weight rows.
 template <int NT>
-struct WeightStep {
+struct Codes {
   u32x4_t q[NT][2];
-  uint32_t s[NT];
 };
 
+// Byte offset, in a row of codes, of a lane's 32 bytes of a step: the row's last 32
+// where they would pass its end.
+__device__ __forceinline__ uint32_t code_offset(int32_t step, int32_t g, int32_t k) {
+  const uint32_t o = (uint32_t)(step * (kFewStep / 2) + 32 * g), last = (uint32_t)(k / 2 - 32);
+  return o < last ? o : last;
+}
+
 template <int NT>
-__device__ __forceinline__ void load_weights(WeightStep<NT>& w, rsrc_t q_rs, rsrc_t s_rs,
-                                             const uint32_t (&row)[NT], int32_t k, int32_t kk) {
+__device__ __forceinline__ void load_codes(Codes<NT>& c, rsrc_t q_rs, const uint32_t (&row_off)[NT],
+                                           uint32_t off) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const uint32_t off = row[t] * (uint32_t)(k / 2) + (uint32_t)(kk / 2);
-    w.q[t][0] = __builtin_amdgcn_raw_buffer_load_b128(q_rs, off, 0, kLoadStreamOnce);
-    w.q[t][1] = __builtin_amdgcn_raw_buffer_load_b128(q_rs, off + 16u, 0, kLoadStreamOnce);
-    w.s[t] = __builtin_amdgcn_raw_buffer_load_b32(
-        s_rs, row[t] * (uint32_t)(k / 16) + (uint32_t)(kk / 16), 0, 0);
+    c.q[t][0] = __builtin_amdgcn_raw_buffer_load_b128(q_rs, row_off[t] + off, 0, 0);
+    c.q[t][1] = __builtin_amdgcn_raw_buffer_load_b128(q_rs, row_off[t] + off + 16u, 0, 0);
   }
 }
 
+// Move the last `left` (1..3) blocks of a lane's window down to its start; 0 and 4 stay.
 template <int NT>
-__device__ __forceinline__ void drop_scales(WeightStep<NT>& w, int32_t skip) {
-  const uint32_t keep = skip >= 4 ? 0u : 0xFFFFFFFFu << (8 * skip);
+__device__ __forceinline__ void move_codes(Codes<NT>& c, int32_t left) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) w.s[t] &= keep;
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t w[8] = {c.q[t][0][0], c.q[t][0][1], c.q[t][0][2], c.q[t][0][3],
+                           c.q[t][1][0], c.q[t][1][1], c.q[t][1][2], c.q[t][1][3]};
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t v = w[i];
+      if (left == 3) v = i + 2 < 8 ? w[i + 2 < 8 ? i + 2 : 0] : 0u;
+      if (left == 2) v = i + 4 < 8 ? w[i + 4 < 8 ? i + 4 : 0] : 0u;
+      if (left == 1) v = i + 6 < 8 ? w[i + 6 < 8 ? i + 6 : 0] : 0u;
+      m[i] = v;
+    }
+    c.q[t][0] = u32x4_t{m[0], m[1], m[2], m[3]};
+    c.q[t][1] = u32x4_t{m[4], m[5], m[6], m[7]};
+  }
 }
 
-// Block scale J (0..3) of a lane's dword.
-template <int J>
-__device__ __forceinline__ float block_scale(uint32_t s) {
-  return __builtin_amdgcn_cvt_f32_fp8((int)s, J);
-}
-
-// Eight matrix products of a step: operand j covers elements 8j .. 8j+7 of each
-// lane's 64.  f(j, t, a): consume weight operand a of tile t.
-template <bool F16, int NT, int J, typename F>
-__device__ __forceinline__ void for_operands(const WeightStep<NT>& w, F&& f) {
+// The eight matrix products of a step: operand J covers elements 8J .. 8J+7 of each
+// lane's 64.  x(J): the token operands; f(t, a, x): multiply tile t.
+template <bool F16, int NT, int J, typename X, typename F>
+__device__ __forceinline__ void for_operands(const Codes<NT>& c, const uint32_t (&s)[NT], X&& x, F&& f) {
   if constexpr (J < 8) {
+    const auto xv = x(J);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const uint32_t codes = w.q[t][J / 4][J % 4];
-      f(J, t, dequant8_16bit<F16>(codes, block_scale<J / 2>(w.s[t])));
+      const uint32_t codes = c.q[t][J / 4][J % 4];
+      f(t, dequant8_16bit<F16>(codes, __builtin_amdgcn_cvt_f32_fp8((int)s[t], J / 2)), xv);
     }
-    for_operands<F16, NT, J + 1>(w, f);
+    for_operands<F16, NT, J + 1>(c, s, x, f);
   }
 }
 
@@ -149,85 +155,156 @@ __device__ __forceinline__ void store_as(void* out, int64_t i, float v, int32_t 
 // x / (1 + e^-x): exactly 0 or the identity where e^-x overflows or vanishes.
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
 
-// The running sums of NT x 16 weight rows times MT x 16 tokens over a wavefront's
-// steps [s0, s1), s0 < s1.  Token t's row starts at byte xoff[t] of x (kOutOfRange:
-// no token, reads as zeros); groups (<= MT) of 16 tokens hold any.
-// The loads of the next step are in flight while a step is computed; the loop is
-// unrolled by two so that both steps keep their registers.
-template <bool F16, int NT, int MT>
+template <int MT>
+struct TokenOperands {
+  u32x4_t v[MT];
+};
+
+// The sums of NT x 16 weight rows times up to MT x 16 tokens over a wavefront's steps
+// [s0, s1).  XR = loads of two tokens each that a step takes at most (8 MT), PF of
+// them kept in flight, the rest (where there are as many tokens) loaded when needed.
+// Two steps are in flight; a load that has nothing to fetch is sent out of range
+// instead of being branched around, so that the compiler's counts of outstanding
+// loads stay exact.
+template <bool F16, int NT, int MT, int XR, int PF>
 struct FewLoop {
-  struct Regs {
-    WeightStep<NT> w;
-    u32x4_t x[MT][8];
+  struct Stage {
+    Codes<NT> c;
+    u32x4_t x[PF];
   };
+  static constexpr int kChunk = 8;  // steps whose scales are in LDS at once
+  static constexpr int kXBytes = XR * 1024, kSBytes = NT * 2048;
+  static constexpr int kLdsBytes = kXBytes + kSBytes;  // of a wavefront; its sums take the place of both
 
   rsrc_t q_rs, s_rs, x_rs;
-  int32_t k, g;
+  uint32_t q_off[NT], s_off[NT];  // row starts, bytes
+  uint32_t x_off[XR];             // start of this lane's 16 bytes of token 2i + lane / 32
+  char* lds;                      // kLdsBytes of this wavefront
+  int32_t k, tokens, lane;
 
-  __device__ __forceinline__ void load(Regs& r, const uint32_t (&row)[NT],
-                                       const uint32_t (&xoff)[MT], int32_t step) const {
-    const LaneK lk = lane_k(step, g, k);
-    load_weights<NT>(r.w, q_rs, s_rs, row, k, lk.k);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        r.x[m][j] = __builtin_amdgcn_raw_buffer_load_b128(
-            x_rs, xoff[m] + (uint32_t)(2 * lk.k + 16 * j), 0, 0);
+  // Steps from `end` on are not fetched (in all that follows).
+  __device__ __forceinline__ uint32_t x_offset(int i, int32_t step, int32_t end) const {
+    return step * kFewStep + 8 * (lane & 31) < k && step < end
+               ? x_off[i] + (uint32_t)(2 * kFewStep * step) : kOutOfRange;
   }
 
-  __device__ __forceinline__ void compute(Regs& r, float4_t (&acc)[NT][MT], int32_t step) const {
-    if ((step + 1) * kFewStep > k) {  // uniform: only a row's last step
-      const LaneK lk = lane_k(step, g, k);
-      drop_scales<NT>(r.w, lk.skip);
+  __device__ __forceinline__ void load(Stage& r, int32_t step, int32_t end) const {
+    load_codes<NT>(r.c, q_rs, q_off, step < end ? code_offset(step, lane >> 4, k) : kOutOfRange);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < 2 * lk.skip) r.x[m][j] = u32x4_t{0, 0, 0, 0};
-    }
-    for_operands<F16, NT, 0>(r.w, [&](int j, int t, u32x4_t a) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[t][m] = mfma16<F16>(a, r.x[m][j], acc[t][m]);
-    });
+    for (int i = 0; i < PF; ++i)
+      r.x[i] = __builtin_amdgcn_raw_buffer_load_b128(x_rs, x_offset(i, step, end), 0, 0);
   }
 
-  __device__ __forceinline__ void run(const uint32_t (&row)[NT], const uint32_t (&xoff)[MT],
-                                      float4_t (&acc)[NT][MT], int32_t s0, int32_t s1) const {
-    Regs a, b;
-    load(a, row, xoff, s0);
-    int32_t s = s0;
-    for (; s + 2 < s1; s += 2) {
-      load(b, row, xoff, s + 1);
-      compute(a, acc, s);
-      load(a, row, xoff, s + 2);
-      compute(b, acc, s + 1);
+  // Scales of steps base .. base + 3: lane (row, i) takes the 16 bytes of step base + i.
+  __device__ __forceinline__ void load_scales(u32x4_t (&s)[NT], int32_t base, int32_t end) const {
+    const int32_t step = base + (lane >> 4);
+    const int32_t last = base + 4 < end ? base + 4 : end;
+    if (last * kFewStep <= k) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        s[t] = __builtin_amdgcn_raw_buffer_load_b128(
+            s_rs, step < end ? s_off[t] + (uint32_t)(16 * step) : kOutOfRange, 0, 0);
+    } else {  // a row ends inside: a dword reads the row's last four where it would pass the end
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t left = blocks_left(step * kFewStep + 64 * i, k);
+          const uint32_t d = __builtin_amdgcn_raw_buffer_load_b32(
+              s_rs, step < end && left > 0 ? s_off[t] + (uint32_t)(16 * step + 4 * i - (4 - left))
+                                          : kOutOfRange, 0, 0);
+          s[t][i] = left > 0 ? d >> (8 * (4 - left)) : 0u;
+        }
     }
-    if (s + 1 < s1) {
-      load(b, row, xoff, s + 1);
-      compute(a, acc, s);
-      compute(b, acc, s + 1);
-    } else {
-      compute(a, acc, s);
+  }
+
+  __device__ __forceinline__ void put_scales(const u32x4_t (&s)[NT], int h) const {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      *reinterpret_cast<u32x4_t*>(lds + kXBytes + (t * 2 + h) * 1024 + lane * 16) = s[t];
+  }
+
+  // 16-byte piece c (0..31) of token t is kept at piece c ^ (t % 16): sixteen tokens'
+  // equal pieces lie in different banks.
+  __device__ __forceinline__ void put_x(int i, u32x4_t v) const {
+    const int32_t t = 2 * i + (lane >> 5);
+    *reinterpret_cast<u32x4_t*>(lds + t * 512 + (((lane & 31) ^ (t & 15)) << 4)) = v;
+  }
+
+  // Step `step`, the i-th of those whose scales are in LDS.
+  __device__ __forceinline__ void compute(Stage& r, float4_t (&acc)[NT][MT], int32_t step, int i) const {
+#pragma unroll
+    for (int j = 0; j < PF; ++j) put_x(j, r.x[j]);
+#pragma unroll
+    for (int j = PF; j < XR; ++j)
+      if (2 * j < tokens)
+        put_x(j, __builtin_amdgcn_raw_buffer_load_b128(x_rs, x_offset(j, step, step + 1), 0, 0));
+    const int32_t g = lane >> 4, col = lane & 15;
+    if ((step + 1) * kFewStep > k) move_codes<NT>(r.c, blocks_left(step * kFewStep + 64 * g, k));
+    uint32_t s[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      s[t] = *reinterpret_cast<const uint32_t*>(lds + kXBytes + t * 2048 + (col + 16 * i) * 16 + 4 * g);
+    uint32_t at[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int32_t t = 16 * m + col < tokens ? 16 * m + col : tokens - 1;
+      at[m] = (uint32_t)(t * 512 + (((8 * g) ^ (t & 15)) << 4));
+    }
+    for_operands<F16, NT, 0>(
+        r.c, s,
+        [&](int j) {
+          TokenOperands<MT> x;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            x.v[m] = *reinterpret_cast<const u32x4_t*>(lds + (at[m] ^ (uint32_t)(j << 4)));
+          return x;
+        },
+        [&](int t, u32x4_t a, const TokenOperands<MT>& x) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[t][m] = mfma16<F16>(a, x.v[m], acc[t][m]);
+        });
+  }
+
+  // kChunk steps at a time: their scales first, then two steps in flight.
+  __device__ __forceinline__ void run(float4_t (&acc)[NT][MT], int32_t s0, int32_t s1) const {
+    for (int32_t c0 = s0; c0 < s1; c0 += kChunk) {
+      const int32_t c1 = c0 + kChunk < s1 ? c0 + kChunk : s1;
+      u32x4_t sc[2][NT];
+      Stage a, b;
+      load_scales(sc[0], c0, c1);
+      load(a, c0, c1);
+      load_scales(sc[1], c0 + 4, c1);
+      load(b, c0 + 1, c1);
+      put_scales(sc[0], 0);
+      put_scales(sc[1], 1);
+      int32_t s = c0;
+      for (; s + 2 < c1; s += 2) {
+        compute(a, acc, s, s - c0);
+        load(a, s + 2, c1);
+        compute(b, acc, s + 1, s + 1 - c0);
+        load(b, s + 3, c1);
+      }
+      compute(a, acc, s, s - c0);
+      if (s + 1 < c1) compute(b, acc, s + 1, s + 1 - c0);
     }
   }
 };
 
-// Leave a wavefront's sums in LDS: red[wave][tile][lane], four values each.
+// Leave a wavefront's sums in its own LDS: [tile][lane], four values each.
 template <int NT, int MT>
-__device__ __forceinline__ void put_sums(float4_t* red, const float4_t (&acc)[NT][MT], int wave,
-                                         int lane) {
+__device__ __forceinline__ void put_sums(char* lds, const float4_t (&acc)[NT][MT], int lane) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) red[((wave * NT + t) * MT + m) * 64 + lane] = acc[t][m];
+    for (int m = 0; m < MT; ++m) reinterpret_cast<float4_t*>(lds)[(t * MT + m) * 64 + lane] = acc[t][m];
 }
 
 // The sum over the wavefronts, in wavefront order, of one lane's values of a tile.
-__device__ __forceinline__ float4_t take_sum(const float4_t* red, int tiles, int tile, int lane,
-                                             int waves) {
-  float4_t v = red[tile * 64 + lane];
-  for (int w = 1; w < waves; ++w) v += red[(w * tiles + tile) * 64 + lane];
+__device__ __forceinline__ float4_t take_sum(const char* lds, int pitch, int tile, int lane, int waves) {
+  const int at = (tile * 64 + lane) * 16;
+  float4_t v = *reinterpret_cast<const float4_t*>(lds + at);
+  for (int w = 1; w < waves; ++w) v += *reinterpret_cast<const float4_t*>(lds + w * pitch + at);
   return v;
 }
 

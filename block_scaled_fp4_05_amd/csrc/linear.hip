@@ -20,99 +20,117 @@ namespace moe_fp4 {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kWaves = 8;
 
-template <bool F16, int NT, int MT, bool SWIGLU>
+// XR: loads of two tokens (see FewLoop); at most eight of them are kept in flight.
+template <bool F16, int NT, int MT, int XR>
+using LinearLoop = FewLoop<F16, NT, MT, XR, (XR < 8 ? XR : 8)>;
+
+template <bool F16, int NT, int MT, int XR>
 __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
   extern __shared__ __align__(16) char smem[];
-  float4_t* red = reinterpret_cast<float4_t*>(smem);
+  typedef LinearLoop<F16, NT, MT, XR> Loop;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
-  const int32_t half = a.n / 2;
-  const int32_t n0 = blockIdx.x * (SWIGLU ? 8 : 16) * NT;
+  const int waves = blockDim.x >> 6, r = lane & 15;
+  const bool swiglu = a.swiglu != 0;
+  const int32_t half = a.n / 2, cols = swiglu ? half : a.n;
+  const int32_t n0 = blockIdx.x * (swiglu ? 8 : 16) * NT;
   const int32_t m0 = blockIdx.y * 16 * MT;
   const float scale = ((sconst_f32)a.w_scale)[0];
-
-  // Item of the epilogue: four consecutive weight rows of one token.
-  const int tile = threadIdx.x >> 6;  // (nt, mt)
-  const int32_t tok = m0 + (tile % MT) * 16 + (lane & 15);
-  const int32_t j0 = SWIGLU ? n0 + (tile / MT) * 8 + 4 * ((lane >> 4) & 1)
-                            : n0 + (tile / MT) * 16 + 4 * (lane >> 4);
-  const int32_t cols = SWIGLU ? half : a.n;
-  const bool mine = tile < NT * MT && tok < a.m && (!SWIGLU || lane < 32);
-  float res[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (!SWIGLU && a.residual && mine) {
-    const uint16_t* rp = static_cast<const uint16_t*>(a.residual) + tok * a.ld_res;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (j0 + i < cols) res[i] = value16<F16>(rp[j0 + i]);
-  }
-
-  uint32_t row[NT], xoff[MT];
-  const int r = lane & 15;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (SWIGLU) {  // rows 0-7 of a tile: gate; 8-15: the same columns of up
-      const int32_t c = n0 + 8 * t + (r & 7);
-      row[t] = (uint32_t)((r >> 3) * half + (c < half ? c : half - 1));
-    } else {
-      const int32_t c = n0 + 16 * t + r;
-      row[t] = (uint32_t)(c < a.n ? c : a.n - 1);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int32_t t = m0 + 16 * m + r;
-    xoff[m] = t < a.m ? (uint32_t)(t * a.ld_x * 2) : kOutOfRange;
-  }
-  FewLoop<F16, NT, MT> loop;
+  Loop loop;
   loop.q_rs = make_rsrc(a.w_q, (uint32_t)((int64_t)a.n * (a.k / 2)));
   loop.s_rs = make_rsrc(a.w_sf, (uint32_t)((int64_t)a.n * (a.k / 16)));
   loop.x_rs = make_rsrc(a.x, (uint32_t)(((a.m - 1) * a.ld_x + a.k) * 2));
+  loop.lds = smem + wave * Loop::kLdsBytes;
   loop.k = a.k;
-  loop.g = lane >> 4;
+  loop.tokens = a.m - m0 < 16 * MT ? a.m - m0 : 16 * MT;
+  loop.lane = lane;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    int32_t row;
+    if (swiglu) {  // rows 0-7 of a tile: gate; 8-15: the same columns of up
+      const int32_t c = n0 + 8 * t + (r & 7);
+      row = (r >> 3) * half + (c < half ? c : half - 1);
+    } else {
+      const int32_t c = n0 + 16 * t + r;
+      row = c < a.n ? c : a.n - 1;
+    }
+    loop.q_off[t] = (uint32_t)row * (uint32_t)(a.k / 2);
+    loop.s_off[t] = (uint32_t)row * (uint32_t)(a.k / 16);
+  }
+#pragma unroll
+  for (int i = 0; i < XR; ++i) {
+    const int32_t t = 2 * i + (lane >> 5);
+    loop.x_off[i] = t < loop.tokens ? (uint32_t)((m0 + t) * a.ld_x * 2 + 16 * (lane & 31)) : kOutOfRange;
+  }
   float4_t acc[NT][MT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[t][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int32_t steps = (a.k + kFewStep - 1) / kFewStep;
-  const int32_t s0 = uniform(wave * steps / waves), s1 = uniform((wave + 1) * steps / waves);
-  if (s0 < s1) loop.run(row, xoff, acc, s0, s1);
-  put_sums<NT, MT>(red, acc, wave, lane);
+  loop.run(acc, uniform(wave * steps / waves), uniform((wave + 1) * steps / waves));
+
+  // A thread's share of the result: four consecutive weight rows of one token.
+  const int tile = threadIdx.x >> 6;  // (nt, mt)
+  const int32_t tok = m0 + (tile % MT) * 16 + r;
+  const int32_t j0 = swiglu ? n0 + (tile / MT) * 8 + 4 * ((lane >> 4) & 1)
+                            : n0 + (tile / MT) * 16 + 4 * (lane >> 4);
+  const bool mine = tile < NT * MT && tok < a.m && j0 < cols && (!swiglu || lane < 32);
+  float res[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.residual && mine) {  // its latency passes under the barrier
+    const uint16_t* rp = static_cast<const uint16_t*>(a.residual) + tok * a.ld_res + j0;
+    uint16_t raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = rp[j0 + i < cols ? i : 0];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) res[i] = value16<F16>(raw[i]);
+  }
+  put_sums<NT, MT>(loop.lds, acc, lane);
   __syncthreads();
   if (!mine) return;
-
-  const float4_t v = take_sum(red, NT * MT, tile, lane, waves);
-  const int64_t o = tok * a.ldo + j0;
-  if (SWIGLU) {
-    const float4_t u = take_sum(red, NT * MT, tile, lane + 32, waves);
+  float4_t v = take_sum(smem, Loop::kLdsBytes, tile, lane, waves) * scale;
+  if (swiglu) {
+    const float4_t u = take_sum(smem, Loop::kLdsBytes, tile, lane + 32, waves) * scale;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (j0 + i < cols) store_as(a.out, o + i, silu(v[i] * scale) * (u[i] * scale), a.out_dtype);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (j0 + i < cols) store_as(a.out, o + i, v[i] * scale + res[i], a.out_dtype);
+    for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
   }
+  const int64_t o = tok * a.ldo + j0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j0 + i < cols) store_as(a.out, o + i, a.residual ? v[i] + res[i] : v[i], a.out_dtype);
 }
 
-template <bool F16, int NT, int MT>
-hipError_t launch(const LinearArgs& a, int waves, hipStream_t stream) {
-  const int cols = a.swiglu ? a.n / 2 : a.n, width = (a.swiglu ? 8 : 16) * NT;
-  const dim3 grid((cols + width - 1) / width, (a.m + 16 * MT - 1) / (16 * MT));
-  const size_t lds = (size_t)waves * NT * MT * 64 * 16;
-  if (a.swiglu)
-    hipLaunchKernelGGL((k_linear<F16, NT, MT, true>), grid, dim3(waves * 64), lds, stream, a);
-  else
-    hipLaunchKernelGGL((k_linear<F16, NT, MT, false>), grid, dim3(waves * 64), lds, stream, a);
+template <bool F16, int NT, int MT, int XR>
+hipError_t launch(const LinearArgs& a, int items, int waves, hipStream_t stream) {
+  if (waves < NT * MT) waves = NT * MT;  // a wavefront finishes one tile of the result
+  const dim3 grid(items, (a.m + 16 * MT - 1) / (16 * MT));
+  const size_t lds = (size_t)waves * LinearLoop<F16, NT, MT, XR>::kLdsBytes;
+  hipLaunchKernelGGL((k_linear<F16, NT, MT, XR>), grid, dim3(waves * 64), lds, stream, a);
   return hipGetLastError();
 }
 
+template <bool F16, int NT>
+hipError_t launch_rows(const LinearArgs& a, int items, int waves, hipStream_t stream) {
+  if (a.m <= 2) return launch<F16, NT, 1, 1>(a, items, waves, stream);
+  if (a.m <= 4) return launch<F16, NT, 1, 2>(a, items, waves, stream);
+  if (a.m <= 16) return launch<F16, NT, 1, 8>(a, items, waves, stream);
+  return launch<F16, NT, 2, 16>(a, items, waves < 4 ? waves : 4, stream);
+}
+
+// Two tiles an item (half the activation reads and half the wavefronts) once that
+// leaves an item for every CU: 8192 x 6144, 16 tokens 13.6 us against 14.8; 65536 x 6144,
+// 4 tokens 54 against 56; but 6144 x 6144, one token 9.8 against 9.7.  Four wavefronts an
+// item, eight where there are few items to fill the CUs (one or two wavefronts
+// on 6144 x 6144: 17.9 and 13.1 us; eight on 65536 x 6144: 63 us).
 template <bool F16>
 hipError_t launch_typed(const LinearArgs& a, hipStream_t stream) {
-  const int mt = a.m > 16 ? 2 : 1;
-  return mt == 1 ? launch<F16, 1, 1>(a, kWaves, stream) : launch<F16, 1, 2>(a, kWaves, stream);
+  const int steps = (a.k + kFewStep - 1) / kFewStep;
+  const int tiles = a.swiglu ? (a.n / 2 + 7) / 8 : (a.n + 15) / 16;
+  const bool pair = tiles >= 512;
+  const int items = pair ? (tiles + 1) / 2 : tiles;
+  int waves = tiles <= 256 ? 8 : 4;
+  if (waves > steps) waves = steps;
+  return pair ? launch_rows<F16, 2>(a, items, waves, stream) : launch_rows<F16, 1>(a, items, waves, stream);
 }
 
 }  // namespace
