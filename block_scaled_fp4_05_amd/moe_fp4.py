@@ -416,23 +416,58 @@ _IN_TYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32, torch.float16: IN_
 _OUT_TYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32, torch.float16: OUT_FP16}
 
 
-def _few_rows(x, residual, out, out_dtype, cols):
+# The calls below are short on the GPU (a few microseconds), so their host time counts:
+# tensors are checked with the three plain comparisons that almost always hold, and
+# _need, which names what is wrong, runs only where one of them fails.
+
+def _exact(t, name, dtype, shape):
+    """A contiguous tensor of this dtype and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+
+
+def _pitch(t, name, dtype, shape):
+    """A matrix of this dtype and shape with unit column stride; returns its row pitch."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape):
+        _need(t, name, dtype, shape)
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: rows must have unit column stride")
+    return row if shape[0] > 1 else shape[1]
+
+
+def _launch_stream(stream, dev):
+    """_stream, without a stream object for the default."""
+    if stream is not None:
+        return _stream(stream, dev)
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"stream on cuda:{torch._C._cuda_getDevice()}, tensors on cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _few_rows(x, residual, out, out_dtype, m, k, cols):
     """Check the activations, residual and output of a few-token call; returns
-    (x type, out, out type)."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("x: expected a bfloat16 or float16 tensor")
-    _need(x, "x", x.dtype, (None, None), rows=True)
-    m = x.shape[0]
-    if residual is not None:
-        _need(residual, "residual", x.dtype, (m, cols), rows=True)
+    (x type, x pitch, residual pitch, out, out type, out pitch)."""
+    dt = x.dtype
+    ld = _pitch(x, "x", dt, (m, k))
+    ld_res = 0 if residual is None else _pitch(residual, "residual", dt, (m, cols))
     if out is None:
-        out = torch.empty((m, cols), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out: dtype {out.dtype}, expected {out_dtype}")
-    if out.dtype not in _OUT_TYPES:
-        raise ValueError(f"out: dtype {out.dtype}, expected bfloat16, float16 or float32")
-    _need(out, "out", out.dtype, (m, cols), rows=True)
-    return _IN_TYPES[x.dtype], out, _OUT_TYPES[out.dtype]
+        out = x.new_empty((m, cols)) if out_dtype is None else x.new_empty((m, cols), dtype=out_dtype)
+        if out.dtype not in _OUT_TYPES:
+            raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16, float16 or float32")
+        return _IN_TYPES[dt], ld, ld_res, out, _OUT_TYPES[out.dtype], cols
+    if not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPES or \
+            (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out: expected a " + ("bfloat16, float16 or float32" if out_dtype is None
+                                               else str(out_dtype)) + " tensor")
+    ldo = _pitch(out, "out", out.dtype, (m, cols))
+    return _IN_TYPES[dt], ld, ld_res, out, _OUT_TYPES[out.dtype], ldo
+
+
+def _x_ok(x):
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float16) or x.dim() != 2:
+        raise ValueError("x: expected a 2-D bfloat16 or float16 tensor")
+    return x.shape
 
 
 def linear_raw(*args):
@@ -446,22 +481,19 @@ def linear(x, w_q, w_sf, w_scale, swiglu: bool = False, residual=None, out=None,
     stride) times NVFP4 weights w_q uint8 [n][k/2], w_sf uint8 [n][k/16], w_scale
     float32 [1].  Returns out [m][n] = x W^T (+ residual, x's type [m][n]), or with swiglu
     [m][n/2] = silu(first half) * second half; of out_dtype (default: x's type)."""
-    _need(w_q, "w_q", torch.uint8, (None, None))
-    n, kb = w_q.shape
+    m, k = _x_ok(x)
+    _need(w_q, "w_q", torch.uint8, (None, k // 2))
+    n = w_q.shape[0]
     if swiglu and (n % 2 or residual is not None):
         raise ValueError("swiglu: needs an even number of weight rows and no residual")
-    dt, out, odt = _few_rows(x, residual, out, out_dtype, n // 2 if swiglu else n)
-    m, k = x.shape
-    if k != 2 * kb:
-        raise ValueError(f"w_q: shape {tuple(w_q.shape)}, expected (n, {k // 2})")
-    _need(w_sf, "w_sf", torch.uint8, (n, k // 16))
-    _need(w_scale, "w_scale", torch.float32, (_AtLeast(1),))
+    _exact(w_sf, "w_sf", torch.uint8, (n, k // 16))
+    _exact(w_scale, "w_scale", torch.float32, (1,))
+    dt, ld, ld_res, out, odt, ldo = _few_rows(x, residual, out, out_dtype, m, k, n // 2 if swiglu else n)
     dev = _same_cuda("x w_q w_sf w_scale residual out", x, w_q, w_sf, w_scale, residual, out)
-    st = lib().moe_fp4_linear(_ptr(x), dt, m, x.stride(0) if m > 1 else k, _ptr(w_q), _ptr(w_sf),
-                              _ptr(w_scale), n, k, 1 if swiglu else 0, _ptr(residual),
-                              0 if residual is None else residual.stride(0) if m > 1 else n,
-                              _ptr(out), odt, out.stride(0) if m > 1 else out.shape[1],
-                              _stream(stream, dev))
+    st = (_lib or lib()).moe_fp4_linear(
+        x.data_ptr(), dt, m, ld, w_q.data_ptr(), w_sf.data_ptr(), w_scale.data_ptr(), n, k,
+        1 if swiglu else 0, None if residual is None else residual.data_ptr(), ld_res, out.data_ptr(),
+        odt, ldo, _launch_stream(stream, dev))
     if st != OK:
         raise MoeFp4Error(st, "moe_fp4_linear")
     return out
@@ -474,7 +506,7 @@ def ffn_raw(*args):
 
 def ffn_workspace_size(tokens: int, topk: int, num_experts: int, inter: int) -> int:
     """Device workspace bytes of moe_ffn for these sizes (0 where it does not run)."""
-    return lib().moe_fp4_ffn_workspace_size(tokens, topk, num_experts, inter)
+    return (_lib or lib()).moe_fp4_ffn_workspace_size(tokens, topk, num_experts, inter)
 
 
 def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, residual=None,
@@ -485,37 +517,37 @@ def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, re
     w2 [E][hidden][I] with scales float32 [E].  Returns out [tokens][hidden] = (residual +)
     the routing-weighted sum of the experts, of out_dtype (default: x's type).
     workspace: uint8 CUDA tensor of ffn_workspace_size bytes (default: a new one)."""
-    _need(w13_q, "w13_q", torch.uint8, (None, None, None))
-    E, rows, hb = w13_q.shape
-    H, I = 2 * hb, rows // 2
-    dt, out, odt = _few_rows(x, residual, out, out_dtype, H)
-    T = x.shape[0]
-    _need(x, "x", x.dtype, (T, H), rows=True)
-    _need(w13_q, "w13_q", torch.uint8, (E, 2 * I, hb))
+    u8, f32 = torch.uint8, torch.float32
+    T, H = _x_ok(x)
+    _need(w13_q, "w13_q", u8, (None, None, H // 2))
+    E, rows, _ = w13_q.shape
+    I = rows // 2
+    if rows % 2:
+        raise ValueError(f"w13_q: shape {tuple(w13_q.shape)}, expected an even number of rows")
     _need(ids, "ids", torch.int32, (T, None))
     K = ids.shape[1]
-    _need(weights, "weights", torch.float32, (T, K))
-    _need(w13_sf, "w13_sf", torch.uint8, (E, 2 * I, H // 16))
-    _need(w13_scale, "w13_scale", torch.float32, (E,))
-    _need(w2_q, "w2_q", torch.uint8, (E, H, I // 2))
-    _need(w2_sf, "w2_sf", torch.uint8, (E, H, I // 16))
-    _need(w2_scale, "w2_scale", torch.float32, (E,))
-    need = ffn_workspace_size(T, K, E, I)
+    _exact(weights, "weights", f32, (T, K))
+    _exact(w13_sf, "w13_sf", u8, (E, rows, H // 16))
+    _exact(w13_scale, "w13_scale", f32, (E,))
+    _exact(w2_q, "w2_q", u8, (E, H, I // 2))
+    _exact(w2_sf, "w2_sf", u8, (E, H, I // 16))
+    _exact(w2_scale, "w2_scale", f32, (E,))
+    dt, ld, ld_res, out, odt, ldo = _few_rows(x, residual, out, out_dtype, T, H, H)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = w13_q.new_empty(ffn_workspace_size(T, K, E, I))
         if stream is not None and workspace.is_cuda:
             # Freed on return: not to be handed out again before this stream is done with it.
             workspace.record_stream(stream)
-    _need(workspace, "workspace", torch.uint8, (_AtLeast(need),))
+    else:
+        _need(workspace, "workspace", u8, (_AtLeast(ffn_workspace_size(T, K, E, I)),))
     dev = _same_cuda("x ids weights w13_q w13_sf w13_scale w2_q w2_sf w2_scale residual out workspace",
                      x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, residual, out,
                      workspace)
-    st = lib().moe_fp4_ffn(_ptr(x), dt, T, x.stride(0) if T > 1 else H, _ptr(ids), _ptr(weights), K,
-                           _ptr(w13_q), _ptr(w13_sf), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_sf),
-                           _ptr(w2_scale), E, H, I, _ptr(residual),
-                           0 if residual is None else residual.stride(0) if T > 1 else H, _ptr(out),
-                           odt, out.stride(0) if T > 1 else H, _ptr(workspace), workspace.numel(),
-                           _stream(stream, dev))
+    st = (_lib or lib()).moe_fp4_ffn(
+        x.data_ptr(), dt, T, ld, ids.data_ptr(), weights.data_ptr(), K, w13_q.data_ptr(),
+        w13_sf.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(), w2_sf.data_ptr(), w2_scale.data_ptr(),
+        E, H, I, None if residual is None else residual.data_ptr(), ld_res, out.data_ptr(), odt, ldo,
+        workspace.data_ptr(), workspace.numel(), _launch_stream(stream, dev))
     if st != OK:
         raise MoeFp4Error(st, "moe_fp4_ffn")
     return out
@@ -538,7 +570,10 @@ def route_raw(*args):
 
 def route_workspace_size(tokens: int, num_experts: int) -> int:
     """Device workspace bytes of route for these sizes."""
-    return lib().moe_fp4_route_workspace_size(tokens, num_experts)
+    return (_lib or lib()).moe_fp4_route_workspace_size(tokens, num_experts)
+
+
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 
 def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: bool = True,
@@ -550,43 +585,43 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
     [E]); num_groups / topk_groups limit the choice to the best groups of experts.
     Routing.offsets and .row_token are grouped_gemm's offsets and a_row_index,
     .token_rows and .weights combine's; .ids and .weights moe_ffn's."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in _IN_TYPES:
-        raise ValueError("logits: expected a float32, bfloat16 or float16 tensor")
-    _need(logits, "logits", logits.dtype, (None, None), rows=True)
-    if score not in ("softmax", "sigmoid"):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _IN_TYPES or logits.dim() != 2:
+        raise ValueError("logits: expected a 2-D float32, bfloat16 or float16 tensor")
+    if score not in _SCORES:
         raise ValueError(f"score: {score!r}, expected 'softmax' or 'sigmoid'")
-    T, E = logits.shape
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (E,))
     if topk < 1:
         raise ValueError(f"topk: {topk}, expected at least 1")
+    T, E = logits.shape
+    i32, f32 = torch.int32, torch.float32
+    ld = _pitch(logits, "logits", logits.dtype, (T, E))
+    if bias is not None:
+        _exact(bias, "bias", f32, (E,))
     if out is None:
-        i32, d = torch.int32, logits.device
-        out = Routing(torch.empty((T, topk), dtype=i32, device=d),
-                      torch.empty((T, topk), dtype=torch.float32, device=d),
-                      torch.empty(E + 1, dtype=i32, device=d),
-                      torch.empty(T * topk, dtype=i32, device=d),
-                      torch.empty((T, topk), dtype=i32, device=d))
-    _need(out.ids, "ids", torch.int32, (T, topk))
-    _need(out.weights, "weights", torch.float32, (T, topk))
-    _need(out.offsets, "offsets", torch.int32, (E + 1,))
-    _need(out.row_token, "row_token", torch.int32, (T * topk,))
-    _need(out.token_rows, "token_rows", torch.int32, (T, topk))
+        new = logits.new_empty
+        ids, offsets = new((T, topk), dtype=i32), new(E + 1, dtype=i32)
+        out = Routing(ids, new((T, topk), dtype=f32), offsets, new(T * topk, dtype=i32),
+                      new((T, topk), dtype=i32))
+    else:
+        for t, name, dtype, shape in zip(out, Routing._fields, (i32, f32, i32, i32, i32),
+                                         ((T, topk), (T, topk), (E + 1,), (T * topk,), (T, topk))):
+            _exact(t, name, dtype, shape)
     need = route_workspace_size(T, E)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
-        if stream is not None and workspace.is_cuda:
-            workspace.record_stream(stream)
-    if workspace is not None:
+    if workspace is None:
+        if need:
+            workspace = logits.new_empty(need, dtype=torch.uint8)
+            if stream is not None and workspace.is_cuda:
+                # Freed on return: not to be handed out again before this stream is done with it.
+                workspace.record_stream(stream)
+    else:
         _need(workspace, "workspace", torch.uint8, (_AtLeast(need),))
     dev = _same_cuda("logits bias ids weights offsets row_token token_rows workspace", logits, bias,
                      *out, workspace)
-    st = lib().moe_fp4_route(
-        _ptr(logits), _IN_TYPES[logits.dtype], T, E, logits.stride(0) if T > 1 else E,
-        SCORE_SIGMOID if score == "sigmoid" else SCORE_SOFTMAX, _ptr(bias), 1 if renormalize else 0,
-        topk, num_groups, num_groups if topk_groups is None else topk_groups, _ptr(out.ids),
-        _ptr(out.weights), _ptr(out.offsets), _ptr(out.row_token), _ptr(out.token_rows),
-        _ptr(workspace), need, _stream(stream, dev))
+    st = (_lib or lib()).moe_fp4_route(
+        logits.data_ptr(), _IN_TYPES[logits.dtype], T, E, ld, _SCORES[score],
+        None if bias is None else bias.data_ptr(), 1 if renormalize else 0, topk, num_groups,
+        num_groups if topk_groups is None else topk_groups, out.ids.data_ptr(), out.weights.data_ptr(),
+        out.offsets.data_ptr(), out.row_token.data_ptr(), out.token_rows.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), need, _launch_stream(stream, dev))
     if st != OK:
         raise MoeFp4Error(st, "moe_fp4_route")
     return out
