@@ -431,7 +431,7 @@ def _pitch(t, name, dtype, shape):
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape):
         _need(t, name, dtype, shape)
     row, col = t.stride()
-    if col != 1 and shape[1] > 1:
+    if col != 1 and shape[1] > 1 and shape[0] > 0:  # (an empty tensor may have any strides)
         raise ValueError(f"{name}: rows must have unit column stride")
     return row if shape[0] > 1 else shape[1]
 
