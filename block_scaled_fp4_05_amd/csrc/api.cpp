@@ -92,10 +92,10 @@ size_t ffn_records_end(int64_t pairs, int32_t experts) {
   return 16 + 16 * (size_t)(pairs < experts ? pairs : experts);
 }
 
-// Tokens of a router block: one per wavefront for a few thousand tokens, more for more,
-// so that the blocks whose counts every block reads stay near 256.
+// Tokens of a router block: four, or as many more as keep the blocks, whose counts every
+// block reads, at 256 or below (up to the largest block).
 int64_t route_block(int64_t tokens) {
-  int64_t b = 16;
+  int64_t b = 4;
   while (b < moe_fp4::kRouteMaxBlock && b * 256 < tokens) b *= 2;
   return b;
 }
@@ -624,10 +624,15 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
       !aligned(workspace, 16))
     return MOE_FP4_ERR_ALIGN;
   if (num_experts > 1024 || topk > 32 || num_groups > 64) return MOE_FP4_ERR_UNSUPPORTED;
-  int32_t group_lanes = 64;
-  while (group_lanes * num_groups > 64) group_lanes /= 2;
-  const int32_t per_lane = (num_experts / num_groups + group_lanes - 1) / group_lanes;
-  if (per_lane > moe_fp4::kRouteMaxPerLane) return MOE_FP4_ERR_UNSUPPORTED;
+  const int32_t group_size = num_experts / num_groups;
+  int32_t token_lanes = tokens >= moe_fp4::kRouteNarrow ? 16 : 64, group_lanes = 0, per_lane = 0;
+  for (; token_lanes <= 64; token_lanes *= 4) {
+    group_lanes = token_lanes;
+    while (group_lanes * num_groups > token_lanes) group_lanes /= 2;
+    per_lane = group_lanes ? (group_size + group_lanes - 1) / group_lanes : 0;
+    if (group_lanes > 0 && per_lane <= moe_fp4::kRouteMaxPerLane && topk <= token_lanes) break;
+  }
+  if (token_lanes > 64) return MOE_FP4_ERR_UNSUPPORTED;
   if (tokens > 0 && (tokens > kFewLimit / topk || ld > kFewLimit / tokens))
     return MOE_FP4_ERR_UNSUPPORTED;
   const size_t need = moe_fp4_route_workspace_size(tokens, num_experts);
@@ -666,7 +671,11 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
   a.topk_groups = topk_groups;
   a.sigmoid = score == MOE_FP4_SCORE_SIGMOID ? 1 : 0;
   a.renormalize = renormalize;
+  a.token_lanes = token_lanes;
   a.group_lanes = group_lanes;
+  // Every lane holds none or per_lane experts, a power of two, at 16-byte addresses.
+  a.wide = aligned(logits, 16) && ld * esize % 16 == 0 && (per_lane & (per_lane - 1)) == 0 &&
+           per_lane * esize % 16 == 0 && group_size % per_lane == 0;
   a.per_lane = per_lane;
   a.block_tokens = (int32_t)route_block(tokens);
   a.counts_pitch = route_pitch(num_experts);

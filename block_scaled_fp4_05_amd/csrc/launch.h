@@ -202,7 +202,8 @@ hipError_t launch_ffn(const FfnArgs& args, hipStream_t stream);
 // Router (route.hip).
 constexpr int32_t kRouteF32 = 1, kRouteF16 = 2;  // the values of MOE_FP4_IN_*
 constexpr int32_t kRouteMaxPerLane = 16;   // experts a lane holds
-constexpr int32_t kRouteOneBlock = 32;     // tokens of the single-launch form
+constexpr int32_t kRouteOneBlock = 64;     // tokens of the single-launch form
+constexpr int32_t kRouteNarrow = 4096;     // tokens from which 16 lanes rank a token
 constexpr int32_t kRouteMaxBlock = 512;    // tokens of a block: 16 words of marks an expert
 struct RouteArgs {
   const void* logits;  // [tokens][ld] of dtype
@@ -216,7 +217,9 @@ struct RouteArgs {
   uint16_t* counts;     // workspace: [blocks][counts_pitch]
   int32_t dtype, tokens, experts, topk, num_groups, topk_groups;
   int32_t sigmoid, renormalize;
+  int32_t token_lanes;   // lanes that rank one token: 16 or 64
   int32_t group_lanes;   // lanes of one group, a power of two
+  int32_t wide;          // lanes read their logits in 16-byte pieces
   int32_t per_lane;      // consecutive experts of one lane
   int32_t block_tokens;  // tokens of a block
   int32_t counts_pitch;  // experts rounded up to 8

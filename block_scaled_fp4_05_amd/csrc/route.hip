@@ -9,10 +9,18 @@
 //             two best (sigmoid)
 //   ties      go to the lower index, in groups and experts
 //
-// A wavefront ranks one token: lane l holds consecutive experts of one group, so the
-// order of lanes is the order of experts and the first lane that holds the maximum
-// wins a tie.  Sigmoid values are ranked in FP64: neighbouring scores of a few hundred
+// A token is ranked by 64 lanes, or from kRouteNarrow tokens on by 16 where they can
+// hold its experts (16 each).  Four tokens a wavefront share every instruction: 16384
+// tokens of 256 BF16 logits, top-8, rank in 12.4 us against 21.5; but each lane then
+// works through four times the experts, which shows while there is a wavefront or two
+// for a SIMD: 2048 tokens with sigmoid scores in groups take 17.8 us against 16.0, one token
+// 6.7 against 5.3.  A lane holds consecutive experts of one group, so the order of
+// (lane, place) is the order of experts and the first holder of the maximum wins a
+// tie.  Sigmoid values are ranked in FP64: neighbouring scores of a few hundred
 // experts come closer than an FP32 step often enough to swap experts.
+//
+// Bound: instructions (each slot is two reductions over a token's lanes) and, up to a
+// few thousand tokens, the launches; the bytes (16384 tokens: 10.5 MB) would take 2 us.
 //
 // Grouping is a counting sort by expert, stable in token order and without a
 // scatter order that could vary: a block of tokens marks each expert's tokens in an
@@ -24,6 +32,7 @@
 
 #include <type_traits>
 
+#include "fp4_device.h"
 #include "gemm_common.h"
 #include "launch.h"
 
@@ -51,6 +60,7 @@ struct Key32 {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
   }
   static __device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
+  static __device__ __forceinline__ T smaller(T a, T b) { return a < b ? a : b; }
   template <int CTRL, int ROWS>
   static __device__ __forceinline__ T moved(T v) {
     return dpp<CTRL, ROWS>(0u, v);
@@ -66,7 +76,8 @@ struct Key64 {
   static __device__ __forceinline__ T of(double s) {
     return s != s ? kKeyNaN : s < kKeyMinusInf ? kKeyMinusInf : s;
   }
-  static __device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
+  static __device__ __forceinline__ T larger(T a, T b) { return __builtin_fmax(a, b); }
+  static __device__ __forceinline__ T smaller(T a, T b) { return __builtin_fmin(a, b); }
   template <int CTRL, int ROWS>
   static __device__ __forceinline__ T moved(T v) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -82,21 +93,43 @@ struct Key64 {
   }
 };
 
-// The largest key of the wavefront, in every lane.
-template <typename K>
-__device__ __forceinline__ typename K::T wave_max(typename K::T v) {
-  v = K::larger(v, K::template moved<0x111, 0xf>(v));
-  v = K::larger(v, K::template moved<0x112, 0xf>(v));
-  v = K::larger(v, K::template moved<0x114, 0xf>(v));
-  v = K::larger(v, K::template moved<0x118, 0xf>(v));
-  v = K::larger(v, K::template moved<0x142, 0xf>(v));
-  v = K::larger(v, K::template moved<0x143, 0xf>(v));
+// The largest key of a token's lanes (LT = 16, a row of the wavefront, or 64), in each
+// of them.
+template <typename K, int LT>
+__device__ __forceinline__ typename K::T token_max(typename K::T v) {
+  v = K::larger(v, K::template moved<0x128, 0xf>(v));  // row rotations by 8, 4, 2, 1
+  v = K::larger(v, K::template moved<0x124, 0xf>(v));
+  v = K::larger(v, K::template moved<0x122, 0xf>(v));
+  v = K::larger(v, K::template moved<0x121, 0xf>(v));
+  if (LT == 16) return v;
+  v = K::larger(v, K::template moved<0x142, 0xa>(v));  // row ends into the next rows
+  v = K::larger(v, K::template moved<0x143, 0xc>(v));
   return K::lane(v, 63);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+struct Word {  // an unsigned number as a key
+  typedef uint32_t T;
+  static __device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
+  template <int CTRL, int ROWS>
+  static __device__ __forceinline__ T moved(T v) {
+    return dpp<CTRL, ROWS>(0u, v);
+  }
+  static __device__ __forceinline__ T lane(T v, int l) {
+    return (T)__builtin_amdgcn_readlane((int)v, l);
+  }
+};
+
+template <int LT>
+__device__ __forceinline__ float token_sum(float v) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  for (int d = 1; d < LT; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+template <int LT>
+__device__ __forceinline__ float token_max_f(float v) {
+#pragma unroll
+  for (int d = 1; d < LT; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
   return v;
 }
 
@@ -107,62 +140,102 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t i) {
                               : __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
-// Rank one token: lane s < topk returns the expert and weight of slot s.
-template <bool SIGMOID, int VPL>
-__device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, int lane, int32_t* id,
+// A lane's logits x[0 .. per_lane) from element i on; valid ones are j < count.
+template <int VPL>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t i, int32_t count, float (&x)[VPL]) {
+  if (a.dtype == kRouteF32) {
+    const float* p = static_cast<const float*>(a.logits) + i;
+    if (VPL % 4 == 0 && a.wide) {
+      const float4_t* w = reinterpret_cast<const float4_t*>(p);
+#pragma unroll
+      for (int c = 0; c < VPL / 4; ++c) {
+        const float4_t v = count > 0 ? w[c] : float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * c + e] = v[e];
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = j < count ? p[j] : 0.0f;
+    return;
+  }
+  const uint16_t* p = static_cast<const uint16_t*>(a.logits) + i;
+  uint16_t raw[VPL];
+  if (VPL % 8 == 0 && a.wide) {
+    const u32x4_t* w = reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+    for (int c = 0; c < VPL / 8; ++c) {
+      const u32x4_t v = count > 0 ? w[c] : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) raw[8 * c + e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) raw[j] = j < count ? p[j] : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    x[j] = a.dtype == kRouteF16 ? (float)__builtin_bit_cast(_Float16, raw[j])
+                                : __builtin_bit_cast(float, (uint32_t)raw[j] << 16);
+}
+
+// Rank token t with LT lanes; `on`: there is such a token (lanes of a wavefront may hold
+// several).  Lane s < topk of the token's returns the expert and weight of slot s.
+template <bool SIGMOID, int LT, int VPL>
+__device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, bool on, int lane, int32_t* id,
                                            float* weight) {
   typedef typename std::conditional<SIGMOID, Key64, Key32>::type K;
   typedef typename K::T KeyT;
+  const int32_t own = lane % LT;                  // among the token's lanes
   const int32_t size = a.experts / a.num_groups;  // experts of a group
-  const int32_t group = lane / a.group_lanes, in = lane % a.group_lanes;
-  const int32_t first = in * a.per_lane;
+  const int32_t group = own / a.group_lanes;
+  const int32_t first = own % a.group_lanes * a.per_lane;
   const int32_t expert0 = group * size + first;
+  int32_t count = on && group < a.num_groups ? size - first : 0;  // experts of this lane
+  count = count < a.per_lane ? count : a.per_lane;
   KeyT key[VPL];
-  float val[VPL];  // logit (softmax) or score (sigmoid)
+  float val[VPL];
+  load_logits<VPL>(a, (int64_t)t * a.ld + expert0, count, val);
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const bool ok = group < a.num_groups && j < a.per_lane && first + j < size;
-    float x = -__builtin_inff();
-    if (ok) x = load_logit(a, (int64_t)t * a.ld + expert0 + j);
+    const bool ok = j < count;
     if (SIGMOID) {
-      const double p = 1.0 / (1.0 + exp(-(double)x));
-      val[j] = (float)p;
-      key[j] = ok ? K::of(a.bias ? p + (double)a.bias[expert0 + j] : p) : K::none();
+      const double p = 1.0 / (1.0 + exp(-(double)val[j]));
+      key[j] = ok ? K::of(a.bias ? p + (double)a.bias[ok ? expert0 + j : 0] : p) : K::none();
     } else {
-      val[j] = x;
-      key[j] = ok ? K::of(x) : K::none();
+      key[j] = ok ? K::of(val[j]) : K::none();
     }
   }
   float top = 0.0f, sum = 0.0f;
   if (!SIGMOID && !a.renormalize) {
-    float m = val[0];
+    float m = -__builtin_inff();
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) m = fmaxf(m, val[j]);
+    for (int j = 0; j < VPL; ++j) m = j < count ? fmaxf(m, val[j]) : m;
+    top = token_max_f<LT>(m);
+    // Terms far below the largest weigh little, so the fast exponential's error, which
+    // grows with the distance, does not show in the sum.
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-    top = m;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (key[j] != K::none()) sum += expf(val[j] - top);
-    sum = wave_sum(sum);
+    for (int j = 0; j < VPL; ++j) sum += j < count ? __expf(val[j] - top) : 0.0f;
+    sum = token_sum<LT>(sum);
   }
   if (a.topk_groups < a.num_groups) {
     KeyT best = K::none(), second = K::none();
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      if (key[j] > best) second = best, best = key[j];
-      else if (key[j] > second) second = key[j];
+      const KeyT low = K::smaller(best, key[j]);
+      best = K::larger(best, key[j]);
+      second = K::larger(second, low);
     }
     for (int d = 1; d < a.group_lanes; d <<= 1) {
       const KeyT b = __shfl_xor(best, d, 64), s = __shfl_xor(second, d, 64);
-      const KeyT low = best > b ? b : best;
+      const KeyT low = K::smaller(best, b);
       best = K::larger(best, b);
       second = K::larger(low, K::larger(second, s));
     }
     const KeyT score = SIGMOID && size > 1 ? best + second : best;
     int32_t ahead = 0;
     for (int32_t o = 0; o < a.num_groups; ++o) {
-      const KeyT other = K::lane(score, o * a.group_lanes);
+      const KeyT other = __shfl(score, lane - own + o * a.group_lanes, 64);
       ahead += other > score || (other == score && o < group) ? 1 : 0;
     }
     if (ahead >= a.topk_groups) {
@@ -171,39 +244,33 @@ __device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, int la
     }
   }
   int32_t my_id = 0;
-  float my_val = 0.0f;
   for (int32_t s = 0; s < a.topk; ++s) {
     KeyT best = key[0];
 #pragma unroll
     for (int j = 1; j < VPL; ++j) best = K::larger(best, key[j]);
-    const KeyT m = wave_max<K>(best);
-    const int win = __ffsll((unsigned long long)__ballot(best == m)) - 1;
-    int32_t at = 0;
-    float v = val[0];
+    const KeyT m = token_max<K, LT>(best);
+    // The lowest expert that holds it, as the largest complement.
+    uint32_t not_expert = 0;
 #pragma unroll
-    for (int j = VPL - 1; j >= 0; --j)
-      if (key[j] == m) at = j, v = val[j];
-    const int32_t chosen = __builtin_amdgcn_readlane(expert0 + at, win);
-    const float value = __builtin_bit_cast(
-        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, v), win));
-    if (lane == s) my_id = chosen, my_val = value;
-    if (lane == win) {
+    for (int j = VPL - 1; j >= 0; --j) not_expert = key[j] == m ? ~(uint32_t)(expert0 + j) : not_expert;
+    const int32_t chosen = (int32_t)~token_max<Word, LT>(not_expert);
+    if (own == s) my_id = chosen;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (j == at) key[j] = K::none();
-    }
+    for (int j = 0; j < VPL; ++j)
+      if (expert0 + j == chosen) key[j] = K::none();
   }
-  const bool mine = lane < a.topk;
+  // The chosen logits are read again (they are in the caches) rather than carried.
+  const bool mine = on && own < a.topk;
+  float my_val = mine ? load_logit(a, (int64_t)t * a.ld + my_id) : 0.0f;
+  if (SIGMOID) my_val = (float)(1.0 / (1.0 + exp(-(double)my_val)));
   float w = my_val;
   if (SIGMOID) {
-    if (a.renormalize) w = my_val / wave_sum(mine ? my_val : 0.0f);
+    if (a.renormalize) w = my_val / token_sum<LT>(mine ? my_val : 0.0f);
   } else if (a.renormalize) {
     // The full softmax's denominator cancels: only the chosen experts' terms are needed.
-    float m = mine ? my_val : -__builtin_inff();
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    const float m = token_max_f<LT>(mine ? my_val : -__builtin_inff());
     const float e = expf(my_val - m);
-    w = e / wave_sum(mine ? e : 0.0f);
+    w = e / token_sum<LT>(mine ? e : 0.0f);
   } else {
     w = expf(my_val - top) / sum;
   }
@@ -264,20 +331,22 @@ __device__ __forceinline__ void mark(uint32_t* marks, int32_t e, int32_t tl, int
 }
 
 // Ranks a block of tokens; leaves the block's rows per expert (16-bit) in counts.
-template <bool SIGMOID, int VPL>
+template <bool SIGMOID, int LT, int VPL>
 __global__ __launch_bounds__(kThreads) void k_rank(RouteArgs a) {
-  extern __shared__ __align__(16) int32_t count[];  // [experts]
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  extern __shared__ __align__(16) int32_t count[];  // [counts_pitch]
+  const int tid = threadIdx.x, lane = tid & 63, own = lane % LT;
   const int32_t t0 = blockIdx.x * a.block_tokens;
   const int32_t here = a.tokens - t0 < a.block_tokens ? a.tokens - t0 : a.block_tokens;
-  for (int i = tid; i < a.counts_pitch; i += kThreads) count[i] = 0;
+  for (int i = tid; i < a.counts_pitch; i += blockDim.x) count[i] = 0;
   __syncthreads();
-  for (int32_t tl = wave; tl < here; tl += kWaves) {
+  for (int32_t first = 0; first < here; first += blockDim.x / LT) {
+    const int32_t tl = first + tid / LT;
+    const bool on = tl < here;
     int32_t id;
     float w;
-    rank_token<SIGMOID, VPL>(a, t0 + tl, lane, &id, &w);
-    if (lane < a.topk) {
-      const int64_t o = (int64_t)(t0 + tl) * a.topk + lane;
+    rank_token<SIGMOID, LT, VPL>(a, t0 + (on ? tl : 0), on, lane, &id, &w);
+    if (on && own < a.topk) {
+      const int64_t o = (int64_t)(t0 + tl) * a.topk + own;
       a.ids[o] = id;
       a.weights[o] = w;
       atomicAdd(&count[id], 1);
@@ -285,7 +354,7 @@ __global__ __launch_bounds__(kThreads) void k_rank(RouteArgs a) {
   }
   __syncthreads();
   uint16_t* out = a.counts + (int64_t)blockIdx.x * a.counts_pitch;
-  for (int i = tid; i < a.counts_pitch; i += kThreads) out[i] = (uint16_t)count[i];
+  for (int i = tid; i < a.counts_pitch; i += blockDim.x) out[i] = (uint16_t)count[i];
 }
 
 // Places a block's rows: offsets from every block's counts, then the marks.
@@ -304,26 +373,26 @@ __global__ __launch_bounds__(kThreads) void k_place(RouteArgs a) {
   for (int i = tid; i < a.experts * words; i += kThreads) marks[i] = 0;
   __syncthreads();
   for (int32_t p = tid; p < here * a.topk; p += kThreads) mark(marks, ids[p], p / a.topk, words);
-  // A thread sums eight experts (16 bytes of counts) over every `stride`-th block.
-  const int cols = a.counts_pitch / 8, stride = kThreads / cols;
+  // A thread sums four experts (8 bytes of counts) over every `stride`-th block.
+  const int cols = a.counts_pitch / 4, stride = kThreads / cols;
   const int col = tid % cols, row = tid / cols;
   if (row < stride) {
-    int32_t all[8] = {}, low[8] = {};
+    int32_t all[4] = {}, low[4] = {};
+#pragma unroll 8
     for (int32_t b = row; b < (int32_t)gridDim.x; b += stride) {
-      const uint4 v = *reinterpret_cast<const uint4*>(a.counts + (int64_t)b * a.counts_pitch + 8 * col);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(a.counts + (int64_t)b * a.counts_pitch + 4 * col);
       const bool earlier = b < (int32_t)blockIdx.x;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int32_t c = (int32_t)(u[i / 2] >> (16 * (i % 2)) & 0xFFFFu);
+      for (int i = 0; i < 4; ++i) {
+        const int32_t c = (int32_t)((uint32_t)v[i / 2] >> (16 * (i % 2)) & 0xFFFFu);
         all[i] += c;
         low[i] += earlier ? c : 0;
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (all[i]) atomicAdd(&total[8 * col + i], all[i]);
-      if (low[i]) atomicAdd(&before[8 * col + i], low[i]);
+    for (int i = 0; i < 4; ++i) {
+      if (all[i]) atomicAdd(&total[4 * col + i], all[i]);
+      if (low[i]) atomicAdd(&before[4 * col + i], low[i]);
     }
   }
   __syncthreads();
@@ -332,46 +401,62 @@ __global__ __launch_bounds__(kThreads) void k_place(RouteArgs a) {
 }
 
 // Both steps of at most kRouteOneBlock tokens in one workgroup.
-template <bool SIGMOID, int VPL>
+template <bool SIGMOID, int LT, int VPL>
 __global__ __launch_bounds__(kThreads) void k_route_small(RouteArgs a) {
   extern __shared__ __align__(16) int32_t lds[];
+  const int words = a.tokens > 32 ? 2 : 1;
   int32_t* total = lds;
   int32_t* before = total + a.experts;
   int32_t* wave_sums = before + a.experts;
   uint32_t* marks = reinterpret_cast<uint32_t*>(wave_sums + kWaves);
-  int32_t* ids = reinterpret_cast<int32_t*>(marks + a.experts);
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  for (int i = tid; i < a.experts; i += blockDim.x) before[i] = 0, marks[i] = 0;
+  int32_t* ids = reinterpret_cast<int32_t*>(marks + a.experts * words);
+  const int tid = threadIdx.x, lane = tid & 63, own = lane % LT;
+  for (int i = tid; i < a.experts * words; i += blockDim.x) marks[i] = 0;
+  for (int i = tid; i < a.experts; i += blockDim.x) before[i] = 0;
   __syncthreads();
-  for (int32_t t = wave; t < a.tokens; t += blockDim.x >> 6) {
+  for (int32_t first = 0; first < a.tokens; first += blockDim.x / LT) {
+    const int32_t t = first + tid / LT;
+    const bool on = t < a.tokens;
     int32_t id;
     float w;
-    rank_token<SIGMOID, VPL>(a, t, lane, &id, &w);
-    if (lane < a.topk) {
-      a.ids[t * a.topk + lane] = id;
-      a.weights[t * a.topk + lane] = w;
-      ids[t * a.topk + lane] = id;
-      mark(marks, id, t, 1);
+    rank_token<SIGMOID, LT, VPL>(a, on ? t : 0, on, lane, &id, &w);
+    if (on && own < a.topk) {
+      a.ids[t * a.topk + own] = id;
+      a.weights[t * a.topk + own] = w;
+      ids[t * a.topk + own] = id;
+      mark(marks, id, t, words);
     }
   }
   __syncthreads();
-  for (int i = tid; i < a.experts; i += blockDim.x) total[i] = __popc(marks[i]);
+  for (int i = tid; i < a.experts; i += blockDim.x) {
+    int32_t c = 0;
+    for (int w = 0; w < words; ++w) c += __popc(marks[i * words + w]);
+    total[i] = c;
+  }
   __syncthreads();
   scan_offsets(a, total, before, wave_sums, true);
-  place_rows(a, ids, marks, before, 0, a.tokens, 1);
+  place_rows(a, ids, marks, before, 0, a.tokens, words);
 }
 
-template <bool SIGMOID, int VPL>
+// Threads that rank `tokens` at once, LT lanes each: whole wavefronts, up to kThreads.
+int rank_threads(int64_t tokens, int lt) {
+  const int64_t t = (tokens * lt + 63) / 64 * 64;
+  return t < 64 ? 64 : t < kThreads ? (int)t : kThreads;
+}
+
+template <bool SIGMOID, int LT, int VPL>
 hipError_t launch(const RouteArgs& a, hipStream_t stream) {
   if (a.tokens <= kRouteOneBlock) {
-    const int waves = a.tokens < 4 ? 4 : a.tokens < kWaves ? (int)a.tokens : kWaves;
-    const size_t lds = (size_t)(3 * a.experts + kWaves + a.tokens * a.topk) * 4;
-    hipLaunchKernelGGL((k_route_small<SIGMOID, VPL>), dim3(1), dim3(waves * 64), lds, stream, a);
+    // At least four wavefronts: they share the scan over the experts.
+    const int threads = rank_threads(a.tokens, LT);
+    const size_t lds = (size_t)((2 + (a.tokens > 32 ? 2 : 1)) * a.experts + kWaves + a.tokens * a.topk) * 4;
+    hipLaunchKernelGGL((k_route_small<SIGMOID, LT, VPL>), dim3(1), dim3(threads < 256 ? 256 : threads), lds,
+                       stream, a);
     return hipGetLastError();
   }
   const int blocks = (int)((a.tokens + a.block_tokens - 1) / a.block_tokens);
-  hipLaunchKernelGGL((k_rank<SIGMOID, VPL>), dim3(blocks), dim3(kThreads), (size_t)a.counts_pitch * 4,
-                     stream, a);
+  hipLaunchKernelGGL((k_rank<SIGMOID, LT, VPL>), dim3(blocks), dim3(rank_threads(a.block_tokens, LT)),
+                     (size_t)a.counts_pitch * 4, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int words = a.block_tokens / 32 > 1 ? a.block_tokens / 32 : 1;
@@ -380,19 +465,24 @@ hipError_t launch(const RouteArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool SIGMOID>
+template <bool SIGMOID, int LT>
 hipError_t launch_sized(const RouteArgs& a, hipStream_t stream) {
-  if (a.per_lane <= 1) return launch<SIGMOID, 1>(a, stream);
-  if (a.per_lane <= 2) return launch<SIGMOID, 2>(a, stream);
-  if (a.per_lane <= 4) return launch<SIGMOID, 4>(a, stream);
-  if (a.per_lane <= 8) return launch<SIGMOID, 8>(a, stream);
-  return launch<SIGMOID, 16>(a, stream);
+  if (a.per_lane <= 1) return launch<SIGMOID, LT, 1>(a, stream);
+  if (a.per_lane <= 2) return launch<SIGMOID, LT, 2>(a, stream);
+  if (a.per_lane <= 4) return launch<SIGMOID, LT, 4>(a, stream);
+  if (a.per_lane <= 8) return launch<SIGMOID, LT, 8>(a, stream);
+  return launch<SIGMOID, LT, 16>(a, stream);
+}
+
+template <bool SIGMOID>
+hipError_t launch_lanes(const RouteArgs& a, hipStream_t stream) {
+  return a.token_lanes == 16 ? launch_sized<SIGMOID, 16>(a, stream) : launch_sized<SIGMOID, 64>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
-  return a.sigmoid ? launch_sized<true>(a, stream) : launch_sized<false>(a, stream);
+  return a.sigmoid ? launch_lanes<true>(a, stream) : launch_lanes<false>(a, stream);
 }
 
 }  // namespace moe_fp4

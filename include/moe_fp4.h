@@ -453,7 +453,7 @@ enum { MOE_FP4_SCORE_SOFTMAX = 0, MOE_FP4_SCORE_SIGMOID = 1 };
  *   rows      all (token, slot) pairs ordered by expert, then token: expert e owns rows
  *             [offsets[e], offsets[e + 1]); row r is of token row_token[r]; slot s of
  *             token t has row token_rows[t][s].
- * Deterministic.  One launch up to 32 tokens, two above.
+ * Deterministic.  One launch up to 64 tokens, two above.
  *   logits     device, [tokens][ld] of dtype (MOE_FP4_IN_BF16, _FP32 or _FP16), aligned to
  *              its element, ld >= num_experts.
  *   tokens     >= 0 (0 writes the offsets, all 0).
@@ -461,7 +461,7 @@ enum { MOE_FP4_SCORE_SOFTMAX = 0, MOE_FP4_SCORE_SIGMOID = 1 };
  *   topk       1 .. 32, at most num_experts / num_groups * topk_groups.
  *   ids, weights, token_rows  device, [tokens][topk] int32 / float / int32;
  *   row_token  device, [tokens * topk] int32; offsets device, [num_experts + 1] int32.
- *   workspace  device, moe_fp4_route_workspace_size bytes (0 up to 32 tokens, NULL then
+ *   workspace  device, moe_fp4_route_workspace_size bytes (0 up to 64 tokens, NULL then
  *              allowed), 16-byte aligned; holds nothing between calls.
  * Errors: NULL, SHAPE (tokens < 0, num_experts < 1, ld < num_experts, num_groups < 1 or not a
  * divisor of num_experts, topk_groups outside 1 .. num_groups, topk < 1 or more than

@@ -73,7 +73,7 @@ def test_ffn_workspace_size():
         assert m.ffn_workspace_size(*bad) == 0
 
 
-ROUTE = dict(logits=_at(0), dtype=1, tokens=40, num_experts=64, ld=64, score=1, bias=None, renormalize=1,
+ROUTE = dict(logits=_at(0), dtype=1, tokens=100, num_experts=64, ld=64, score=1, bias=None, renormalize=1,
              topk=4, num_groups=8, topk_groups=2, ids=_at(1), weights=_at(2), offsets=_at(3),
              row_token=_at(4), token_rows=_at(5), workspace=_at(6), workspace_bytes=1 << 20, stream=None)
 
@@ -82,7 +82,7 @@ ROUTE = dict(logits=_at(0), dtype=1, tokens=40, num_experts=64, ld=64, score=1, 
     *[({nm: None}, NULL) for nm in ("logits", "ids", "weights", "offsets", "row_token", "token_rows", "workspace")],
     (dict(tokens=-1), SHAPE), (dict(num_experts=0), SHAPE), (dict(ld=63), SHAPE), (dict(topk=0), SHAPE),
     (dict(topk=17), SHAPE), (dict(num_groups=0), SHAPE), (dict(num_groups=7), SHAPE),
-    (dict(topk_groups=0), SHAPE), (dict(topk_groups=9), SHAPE), (dict(workspace_bytes=100), SHAPE),
+    (dict(topk_groups=0), SHAPE), (dict(topk_groups=9), SHAPE), (dict(workspace_bytes=3199), SHAPE),
     (dict(dtype=3), ARG), (dict(score=2), ARG), (dict(renormalize=2), ARG), (dict(score=0, bias=_at(7)), ARG),
     *[({nm: ROUTE[nm] + 2}, ALIGN) for nm in ("logits", "ids", "weights", "offsets", "row_token", "token_rows")],
     (dict(workspace=_at(6) + 8), ALIGN), (dict(bias=_at(7) + 2), ALIGN),
@@ -98,8 +98,8 @@ def test_route_refuses(change, status):
 
 
 def test_route_workspace_size():
-    assert m.route_workspace_size(32, 256) == 0
-    assert m.route_workspace_size(512, 256) == 32 * 256 * 2
+    assert m.route_workspace_size(64, 256) == 0
+    assert m.route_workspace_size(512, 256) == 128 * 256 * 2
     assert m.route_workspace_size(16384, 60) == 256 * 64 * 2
 
 
@@ -172,7 +172,7 @@ def test_ffn_binding_checks_its_tensors(change, message):
     ((torch.zeros(3, 8), 2), dict(score="top"), "score"),
     ((torch.zeros(3, 8), 0), {}, "topk"),
     ((torch.zeros(3, 8), 2), dict(bias=torch.zeros(7)), "bias: shape"),
-    ((torch.zeros(40, 8), 2), dict(workspace=torch.zeros(1, dtype=U8)), "workspace: shape"),
+    ((torch.zeros(100, 8), 2), dict(workspace=torch.zeros(1, dtype=U8)), "workspace: shape"),
     ((torch.zeros(3, 8), 2), dict(out=m.Routing(*[torch.zeros(3, 2, dtype=I32)] * 5)), "weights: dtype"),
     ((torch.zeros(3, 8), 2), {}, "must be a CUDA tensor"),
 ])

@@ -40,7 +40,7 @@ def _logits(T, E, dtype="fp32", seed=0):
     return torch.from_numpy(rng.standard_normal((T, E)) * 2).to(ref.DT[dtype])
 
 
-@pytest.mark.parametrize("T", [0, 1, 2, 16, 31, 32, 33, 100, 513, 3001])
+@pytest.mark.parametrize("T", [0, 1, 2, 16, 31, 32, 33, 63, 64, 65, 100, 513, 3001])
 @pytest.mark.parametrize("E,topk", [(1, 1), (2, 2), (8, 3), (60, 4), (64, 8), (65, 8), (256, 8), (257, 9),
                                     (384, 1), (1000, 32), (1024, 6)])
 def test_route_softmax(T, E, topk):
