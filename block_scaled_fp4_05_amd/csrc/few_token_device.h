@@ -118,7 +118,7 @@ __device__ __forceinline__ void move_codes(Codes<NT>& c, int32_t left) {
 }
 
 // The eight matrix products of a step: operand J covers elements 8J .. 8J+7 of each
-// lane's 64.  x(J): the token operands; f(t, a, x): multiply tile t.
+// lane's 64.  x(J): the token operands; f(J, t, a, x): multiply tile t.
 template <bool F16, int NT, int J, typename X, typename F>
 __device__ __forceinline__ void for_operands(const Codes<NT>& c, const uint32_t (&s)[NT], X&& x, F&& f) {
   if constexpr (J < 8) {
@@ -126,7 +126,7 @@ __device__ __forceinline__ void for_operands(const Codes<NT>& c, const uint32_t 
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const uint32_t codes = c.q[t][J / 4][J % 4];
-      f(t, dequant8_16bit<F16>(codes, __builtin_amdgcn_cvt_f32_fp8((int)s[t], J / 2)), xv);
+      f(J, t, dequant8_16bit<F16>(codes, __builtin_amdgcn_cvt_f32_fp8((int)s[t], J / 2)), xv);
     }
     for_operands<F16, NT, J + 1>(c, s, x, f);
   }
@@ -260,7 +260,7 @@ struct FewLoop {
             x.v[m] = *reinterpret_cast<const u32x4_t*>(lds + (at[m] ^ (uint32_t)(j << 4)));
           return x;
         },
-        [&](int t, u32x4_t a, const TokenOperands<MT>& x) {
+        [&](int, int t, u32x4_t a, const TokenOperands<MT>& x) {
 #pragma unroll
           for (int m = 0; m < MT; ++m) acc[t][m] = mfma16<F16>(a, x.v[m], acc[t][m]);
         });

@@ -40,7 +40,6 @@ struct __align__(16) RankRecord {
   int32_t row0;  // first row of h of this expert
   uint32_t tokens_lo, tokens_hi;
 };
-typedef const RankRecord __attribute__((address_space(4)))* sconst_record;
 
 // Dynamic LDS of k_ffn_up before the sums: ids and weights of every pair, the
 // bitmap, and the expert's token list and coefficients.
@@ -197,6 +196,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
 // the first PF rows of h.
 template <int NT, int PF>
 struct DownStage {
+  RankRecord rec;
   Codes<NT> c;
   uint32_t s[NT];
   u32x4_t h[PF];
@@ -235,13 +235,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
   const int32_t u0 = uniform((int32_t)((int64_t)wave * units / waves));
   const int32_t u1 = uniform((int32_t)((int64_t)(wave + 1) * units / waves));
 
-  auto record = [&](int32_t rank) {
-    const sconst_i32 p = (sconst_i32)(const void*)(a.records + rank);
-    RankRecord rec;
-    rec.expert = p[0], rec.row0 = p[1], rec.tokens_lo = (uint32_t)p[2], rec.tokens_hi = (uint32_t)p[3];
-    return rec;
-  };
-  auto rows_of = [](const RankRecord& rec) { return __popc(rec.tokens_lo) + __popc(rec.tokens_hi); };
+  auto tokens_of = [](const RankRecord& rec) { return (uint64_t)rec.tokens_hi << 32 | rec.tokens_lo; };
   // Byte offset of this lane's 16 bytes of row j of an expert's h.
   auto h_offset = [&](const RankRecord& rec, int32_t rows, int32_t step, int32_t j) {
     return j < rows && step * kFewStep + 4 * (lane & ~1) < k
@@ -259,8 +253,9 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
     if (++c.step == steps) c.step = 0, ++c.rank;
   };
   auto load = [&](DownStage<NT, PF>& d, const Cursor& c, bool on) {
-    const RankRecord rec = record(on ? c.rank : 0);
-    const int64_t wrow = (int64_t)rec.expert * a.hidden;
+    const sconst_i32 p = (sconst_i32)(const void*)(a.records + (on ? c.rank : 0));
+    d.rec.expert = p[0], d.rec.row0 = p[1], d.rec.tokens_lo = (uint32_t)p[2], d.rec.tokens_hi = (uint32_t)p[3];
+    const int64_t wrow = (int64_t)d.rec.expert * a.hidden;
     const rsrc_t q_rs = make_rsrc(a.w2_q + wrow * (k / 2), (uint32_t)a.hidden * (uint32_t)(k / 2));
     const rsrc_t s_rs = make_rsrc(a.w2_sf + wrow * (k / 16), (uint32_t)a.hidden * (uint32_t)(k / 16));
     load_codes<NT>(d.c, q_rs, q_off, on ? code_offset(c.step, g, k) : kOutOfRange);
@@ -269,51 +264,70 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
     for (int t = 0; t < NT; ++t)
       d.s[t] = __builtin_amdgcn_raw_buffer_load_b32(
           s_rs, on ? s_off[t] + (so < last ? so : last) : kOutOfRange, 0, 0);
-    const int32_t rows = on ? rows_of(rec) : 0;
+    const int32_t rows = on ? __popcll(tokens_of(d.rec)) : 0;
 #pragma unroll
     for (int j = 0; j < PF; ++j)
-      if (j < 2 || j < rows) d.h[j] = __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(rec, rows, c.step, j), 0, 0);
+      if (j < 2 || j < rows) d.h[j] = __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(d.rec, rows, c.step, j), 0, 0);
   };
-  auto compute = [&](DownStage<NT, PF>& d, const Cursor& c) {
-    const RankRecord rec = record(c.rank);
-    const uint64_t tokens = (uint64_t)rec.tokens_hi << 32 | rec.tokens_lo;
-    const int32_t rows = rows_of(rec);
+
+  // The expert being summed: its first rows' sums stay in registers until the expert ends.
+  float4_t acc[NT][2];
+  auto clear = [&](float4_t (&s)[NT][2]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  float* dest = nullptr;  // this lane's row's sums, null for none
+  // Add what eight rows have summed to their tokens' sums; column c + 8 holds the rests of column c.
+  auto flush = [&](const float4_t (&s)[NT][2], float* to) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float4_t v = s[t][0] + s[t][1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] += __builtin_bit_cast(
+            float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, (float)v[i]), 0x108, 0xf, 0xf, true));
+      if (to) *reinterpret_cast<float4_t*>(to + 16 * t) += v;
+    }
+  };
+  auto multiply = [&](const DownStage<NT, PF>& d, int32_t here, float4_t (&s)[NT][2]) {
+    const int32_t row = (r & 7) < here ? (r & 7) : here - 1;
+    const uint32_t at = (uint32_t)(row * 1024 + (((16 * g + (r >> 3)) ^ (row << 1)) << 4));
+    for_operands<false, NT, 0>(
+        d.c, d.s, [&](int j) { return *reinterpret_cast<const u32x4_t*>(hs + (at ^ (uint32_t)(j << 5))); },
+        [&](int j, int t, u32x4_t w, u32x4_t h) { s[t][j & 1] = mfma16<false>(w, h, s[t][j & 1]); });
+  };
+  clear(acc);
+  auto compute = [&](DownStage<NT, PF>& d, const Cursor& c, bool begins, bool ends) {
+    const uint64_t tokens = tokens_of(d.rec);
+    const int32_t rows = __popcll(tokens);
     if ((c.step + 1) * kFewStep > k) {
       const int32_t left = blocks_left(c.step * kFewStep + 64 * g, k);
       move_codes<NT>(d.c, left);
 #pragma unroll
       for (int t = 0; t < NT; ++t) d.s[t] = left > 0 ? d.s[t] >> (8 * (4 - left)) : 0u;
     }
-    if (tokens >> lane & 1) list[__popcll(tokens & ((1ull << lane) - 1))] = lane;
-    for (int32_t first = 0; first < rows; first += kRowGroup) {
+    if (begins) {
+      if (tokens >> lane & 1) list[__popcll(tokens & ((1ull << lane) - 1))] = lane;
+      dest = r < kRowGroup && r < rows ? mysum + list[r] * kCols + 4 * g : nullptr;
+    }
+#pragma unroll
+    for (int j = 0; j < PF; ++j)
+      if (j < rows) put_h(j, d.h[j]);
+    for (int32_t j = PF; j < rows && j < kRowGroup; ++j)
+      put_h(j, __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(d.rec, rows, c.step, j), 0, 0));
+    multiply(d, rows < kRowGroup ? rows : kRowGroup, acc);
+    for (int32_t first = kRowGroup; first < rows; first += kRowGroup) {  // an expert of many tokens
       const int32_t here = rows - first < kRowGroup ? rows - first : kRowGroup;
-      if (first == 0) {
-#pragma unroll
-        for (int j = 0; j < PF; ++j)
-          if (j < here) put_h(j, d.h[j]);
-      }
-      for (int32_t j = first == 0 ? PF : 0; j < here; ++j)
-        put_h(j, __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(rec, rows, c.step, first + j), 0, 0));
-      float4_t acc[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      const int32_t row = (r & 7) < here ? (r & 7) : here - 1;
-      const uint32_t at = (uint32_t)(row * 1024 + (((16 * g + (r >> 3)) ^ (row << 1)) << 4));
-      for_operands<false, NT, 0>(
-          d.c, d.s, [&](int j) { return *reinterpret_cast<const u32x4_t*>(hs + (at ^ (uint32_t)(j << 5))); },
-          [&](int t, u32x4_t w, u32x4_t h) { acc[t] = mfma16<false>(w, h, acc[t]); });
-      // Column c + 8 holds the rests of column c.
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[t][i] += __builtin_bit_cast(
-              float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, (float)acc[t][i]), 0x108, 0xf, 0xf, true));
-      if (r < here) {
-        float* p = mysum + list[first + r] * kCols + 4 * g;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<float4_t*>(p + 16 * t) += acc[t];
-      }
+      for (int32_t j = 0; j < here; ++j)
+        put_h(j, __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(d.rec, rows, c.step, first + j), 0, 0));
+      float4_t more[NT][2];
+      clear(more);
+      multiply(d, here, more);
+      flush(more, r < here ? mysum + list[first + r] * kCols + 4 * g : nullptr);
+    }
+    if (ends) {
+      flush(acc, dest);
+      clear(acc);
     }
   };
   if (u0 < u1) {
@@ -327,7 +341,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
     for (int32_t u = u0; u < u1; u += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        if (u + d < u1) compute(st[d], at);
+        if (u + d < u1)
+          compute(st[d], at, u + d == u0 || at.step == 0, u + d + 1 == u1 || at.step + 1 == steps);
         advance(at);
         load(st[d], in, u + d + kDepth < u1);
         advance(in);
@@ -356,11 +371,11 @@ hipError_t launch_up(const FfnArgs& a, int waves, hipStream_t stream) {
 }
 
 template <bool F16, int NT, int PF>
-hipError_t launch_down(const FfnArgs& a, int waves, hipStream_t stream) {
+hipError_t launch_down(const FfnArgs& a, hipStream_t stream) {
   const int hrows = a.tokens < kRowGroup ? a.tokens : kRowGroup;
-  const size_t lds = (size_t)waves * (hrows * 1024 + (a.tokens * 16 * NT + 64) * 4);
+  const size_t lds = (size_t)kDownWaves * (hrows * 1024 + (a.tokens * 16 * NT + 64) * 4);
   const dim3 grid((a.hidden + 16 * NT - 1) / (16 * NT));
-  hipLaunchKernelGGL((k_ffn_down<F16, NT, PF>), grid, dim3(waves * 64), lds, stream, a);
+  hipLaunchKernelGGL((k_ffn_down<F16, NT, PF>), grid, dim3(kDownWaves * 64), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -368,6 +383,10 @@ hipError_t launch_down(const FfnArgs& a, int waves, hipStream_t stream) {
 // 1024: the layer takes 118 us against 137 with one tile and 231 with one tile and eight
 // wavefronts); where that leaves CUs without an item, one tile and eight wavefronts
 // (one token, eight experts of 6144 x 256: 16.3 us against 17.9).
+// k_ffn_down: eight wavefronts (four: 145 us for the first layer, 48 for eight tokens of
+// 256 experts; twelve: 112 and 47) and one tile (two: 142 and 46).  All eight rows of h that a
+// product takes are kept in flight where experts have two tokens or more on average (109
+// against 118 us), else four (eight: 48 us against 45 for the eight tokens).
 template <bool F16>
 hipError_t launch_typed(const FfnArgs& a, hipStream_t stream) {
   const int64_t pairs = (int64_t)a.tokens * a.topk;
@@ -379,8 +398,8 @@ hipError_t launch_typed(const FfnArgs& a, hipStream_t stream) {
   else
     err = few ? launch_up<F16, 1, 1>(a, 8, stream) : launch_up<F16, 1, 8>(a, 8, stream);
   if (err != hipSuccess) return err;
-  return a.tokens == 1 ? launch_down<F16, 1, 1>(a, kDownWaves, stream)
-                       : launch_down<F16, 1, 4>(a, kDownWaves, stream);
+  if (a.tokens == 1) return launch_down<F16, 1, 1>(a, stream);
+  return pairs >= 2 * (int64_t)a.experts ? launch_down<F16, 1, 8>(a, stream) : launch_down<F16, 1, 4>(a, stream);
 }
 
 }  // namespace
