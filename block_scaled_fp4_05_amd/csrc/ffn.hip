@@ -154,9 +154,9 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
   const int32_t steps = (k + kFewStep - 1) / kFewStep;
   const int32_t s0 = uniform(wave * steps / waves), s1 = uniform((wave + 1) * steps / waves);
   const int tile = tid >> 6;
-  // An expert of more than 16 tokens takes several passes over its weights.
-  for (int32_t first = 0; first < rows; first += 16) {
-    loop.tokens = rows - first < 16 ? rows - first : 16;
+  // An expert of more than 2 XR tokens takes several passes over its weights.
+  for (int32_t first = 0; first < rows; first += 2 * XR) {
+    loop.tokens = rows - first < 2 * XR ? rows - first : 2 * XR;
 #pragma unroll
     for (int i = 0; i < XR; ++i) {
       const int32_t j = 2 * i + (lane >> 5);
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
     __syncthreads();
     const int32_t j = first + r;
     const int32_t col = c0 + tile * 8 + 4 * ((lane >> 4) & 1);
-    if (tile < NT && lane < 32 && j < rows && col < inter) {
+    if (tile < NT && lane < 32 && r < loop.tokens && col < inter) {
       const float4_t gate = take_sum(work, Loop::kLdsBytes, tile, lane, waves);
       const float4_t up = take_sum(work, Loop::kLdsBytes, tile, lane + 32, waves);
       const float cf = coef[j];
@@ -383,6 +383,9 @@ hipError_t launch_down(const FfnArgs& a, hipStream_t stream) {
 // 1024: the layer takes 118 us against 137 with one tile and 231 with one tile and eight
 // wavefronts); where that leaves CUs without an item, one tile and eight wavefronts
 // (one token, eight experts of 6144 x 256: 16.3 us against 17.9).
+// Room for 4, 8 or 16 tokens of an expert at once, by how many it has on average; the
+// wavefronts that fit on a CU depend on it (the first layer above: 106 us with 8, 110
+// with 16, 114 with 4; eight tokens of 256 experts 45.2, 46.6 and 44.3).
 // k_ffn_down: eight wavefronts (four: 145 us for the first layer, 48 for eight tokens of
 // 256 experts; twelve: 112 and 47) and one tile (two: 142 and 46).  All eight rows of h that a
 // product takes are kept in flight where experts have two tokens or more on average (109
@@ -391,12 +394,16 @@ template <bool F16>
 hipError_t launch_typed(const FfnArgs& a, hipStream_t stream) {
   const int64_t pairs = (int64_t)a.tokens * a.topk;
   const int64_t tiles = (a.inter + 7) / 8 * (pairs < a.experts ? pairs : a.experts);
-  const bool few = a.tokens <= 2;
+  const bool pair = tiles >= 512;
   hipError_t err;
-  if (tiles >= 512)
-    err = few ? launch_up<F16, 2, 1>(a, 4, stream) : launch_up<F16, 2, 8>(a, 4, stream);
+  if (a.tokens <= 2)
+    err = pair ? launch_up<F16, 2, 1>(a, 4, stream) : launch_up<F16, 1, 1>(a, 8, stream);
+  else if (pairs <= a.experts)
+    err = pair ? launch_up<F16, 2, 2>(a, 4, stream) : launch_up<F16, 1, 2>(a, 8, stream);
+  else if (pairs <= 4 * (int64_t)a.experts)
+    err = pair ? launch_up<F16, 2, 4>(a, 4, stream) : launch_up<F16, 1, 4>(a, 8, stream);
   else
-    err = few ? launch_up<F16, 1, 1>(a, 8, stream) : launch_up<F16, 1, 8>(a, 8, stream);
+    err = pair ? launch_up<F16, 2, 8>(a, 4, stream) : launch_up<F16, 1, 8>(a, 8, stream);
   if (err != hipSuccess) return err;
   if (a.tokens == 1) return launch_down<F16, 1, 1>(a, stream);
   return pairs >= 2 * (int64_t)a.experts ? launch_down<F16, 1, 8>(a, stream) : launch_down<F16, 1, 4>(a, stream);
