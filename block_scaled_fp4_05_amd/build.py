@@ -18,6 +18,9 @@ HEADERS = ["fp4_device.h", "gemm_common.h", "grouped_gemm_kernel.h", "launch.h",
 # bench.py --ceilings loads (not part of the C ABI in include/moe_fp4.h).
 PROBE_LIB = os.path.join(PKG, "libmoe_fp4_probe.so")
 PROBE_SOURCES = ["stream_probe.hip"]
+# The binding's short host path (a CPython extension module over torch's C++ tensors).
+CALLS_LIB = os.path.join(PKG, "_calls.so")
+CALLS_SOURCE = "calls.cpp"
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
@@ -81,6 +84,31 @@ def build_probe(verbose: bool = False) -> str:
     return build(verbose=verbose, out=PROBE_LIB, sources=PROBE_SOURCES)
 
 
+def build_calls(verbose: bool = False) -> str:
+    """The binding's short host path (_calls.so): host code only, against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = CALLS_LIB + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+           "-I", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, "-L", cpp_extension.TORCH_LIB_PATH,
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n" + res.stdout + res.stderr)
+    if verbose:
+        print(res.stdout + res.stderr)
+    os.replace(tmp, CALLS_LIB)
+    return CALLS_LIB
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
     print(build_probe(verbose=True))
+    print(build_calls(verbose=True))

@@ -7,6 +7,7 @@ compiled library is missing the calls raise; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import NamedTuple
 
@@ -97,8 +98,29 @@ def lib() -> ctypes.CDLL:
     L.moe_fp4_status_string.restype = ctypes.c_char_p
     L.moe_fp4_abi_version.argtypes = []
     L.moe_fp4_abi_version.restype = i
+    _load_calls(L)
     _lib = L
     return L
+
+
+# The few-token calls' short host path (csrc/calls.cpp), or None where it was not built for
+# this torch: the Python code below does the same, only slower.
+_calls = None
+
+
+def _load_calls(L) -> None:
+    global _calls
+    path = os.path.join(_PKG, "_calls.so")
+    try:
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except (ImportError, OSError):
+        return
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (L.moe_fp4_linear, L.moe_fp4_ffn, L.moe_fp4_ffn_workspace_size,
+                            L.moe_fp4_route, L.moe_fp4_route_workspace_size)))
+    _calls = module
 
 
 def status_string(status: int) -> str:
@@ -416,9 +438,12 @@ _IN_TYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32, torch.float16: IN_
 _OUT_TYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32, torch.float16: OUT_FP16}
 
 
-# The calls below are short on the GPU (a few microseconds), so their host time counts:
-# tensors are checked with the three plain comparisons that almost always hold, and
-# _need, which names what is wrong, runs only where one of them fails.
+# The calls below are short on the GPU (a few microseconds), so their host time counts.
+# Plain calls (tensors on the current device and its current stream) go through _calls,
+# which checks and allocates in C++ and returns None where anything is out of the
+# ordinary; the Python code then does the call or names what is wrong.  Here, tensors are
+# checked with the three plain comparisons that almost always hold, and _need runs only
+# where one of them fails.
 
 def _exact(t, name, dtype, shape):
     """A contiguous tensor of this dtype and shape."""
@@ -436,13 +461,22 @@ def _pitch(t, name, dtype, shape):
     return row if shape[0] > 1 else shape[1]
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(dev):
+    """The current stream of device `dev`, as the number the C entry points take."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _launch_stream(stream, dev):
     """_stream, without a stream object for the default."""
     if stream is not None:
         return _stream(stream, dev)
-    if torch._C._cuda_getDevice() != dev:
-        raise ValueError(f"stream on cuda:{torch._C._cuda_getDevice()}, tensors on cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    if _current_device() != dev:
+        raise ValueError(f"stream on cuda:{_current_device()}, tensors on cuda:{dev}")
+    return _raw_stream(dev)
 
 
 def _few_rows(x, residual, out, out_dtype, m, k, cols):
@@ -481,6 +515,12 @@ def linear(x, w_q, w_sf, w_scale, swiglu: bool = False, residual=None, out=None,
     stride) times NVFP4 weights w_q uint8 [n][k/2], w_sf uint8 [n][k/16], w_scale
     float32 [1].  Returns out [m][n] = x W^T (+ residual, x's type [m][n]), or with swiglu
     [m][n/2] = silu(first half) * second half; of out_dtype (default: x's type)."""
+    if (_calls or lib() and _calls) and stream is None and isinstance(x, torch.Tensor) and x.is_cuda:
+        dev = _current_device()
+        got = _calls.linear(x, w_q, w_sf, w_scale, swiglu, residual, out,
+                            -1 if out_dtype is None else _OUT_TYPES.get(out_dtype, 3), dev, _raw_stream(dev))
+        if got is not None:
+            return got
     m, k = _x_ok(x)
     _need(w_q, "w_q", torch.uint8, (None, k // 2))
     n = w_q.shape[0]
@@ -517,6 +557,13 @@ def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, re
     w2 [E][hidden][I] with scales float32 [E].  Returns out [tokens][hidden] = (residual +)
     the routing-weighted sum of the experts, of out_dtype (default: x's type).
     workspace: uint8 CUDA tensor of ffn_workspace_size bytes (default: a new one)."""
+    if (_calls or lib() and _calls) and stream is None and workspace is None and \
+            isinstance(x, torch.Tensor) and x.is_cuda:
+        dev = _current_device()
+        got = _calls.ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, residual, out,
+                         -1 if out_dtype is None else _OUT_TYPES.get(out_dtype, 3), dev, _raw_stream(dev))
+        if got is not None:
+            return got
     u8, f32 = torch.uint8, torch.float32
     T, H = _x_ok(x)
     _need(w13_q, "w13_q", u8, (None, None, H // 2))
@@ -585,6 +632,13 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
     [E]); num_groups / topk_groups limit the choice to the best groups of experts.
     Routing.offsets and .row_token are grouped_gemm's offsets and a_row_index,
     .token_rows and .weights combine's; .ids and .weights moe_ffn's."""
+    if (_calls or lib() and _calls) and stream is None and workspace is None and out is None and \
+            isinstance(logits, torch.Tensor) and logits.is_cuda and score in _SCORES:
+        dev = _current_device()
+        got = _calls.route(logits, topk, _SCORES[score], bias, renormalize, num_groups,
+                           num_groups if topk_groups is None else topk_groups, dev, _raw_stream(dev))
+        if got is not None:
+            return Routing(*got)
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _IN_TYPES or logits.dim() != 2:
         raise ValueError("logits: expected a 2-D float32, bfloat16 or float16 tensor")
     if score not in _SCORES:
