@@ -233,6 +233,18 @@ PyObject* ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Elements (of four bytes) a result takes of a common allocation: whole 256 bytes.
+int64_t aligned_part(int64_t n) { return (n + 63) / 64 * 64; }
+
+// A contiguous tensor of four-byte elements at element `at` of another's storage.
+at::Tensor part_of(const at::Tensor& all, at::ScalarType type, int64_t at, at::IntArrayRef shape) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                          c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // route(logits, topk, score, bias, renormalize, num_groups, topk_groups, device, stream):
 // new outputs, a workspace of its own, on the current stream; a tuple of five tensors
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -252,10 +264,14 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t score = integer(a[2]), groups = integer(a[5]), topk_groups = integer(a[6]);
     need(renormalize >= 0 && groups <= INT32_MAX && topk_groups <= INT32_MAX && groups >= 1 && topk_groups >= 1);
     void* stream = stream_on(a[7], a[8], dev);
-    const auto i32 = x.options().dtype(at::kInt);
-    const at::Tensor ids = at::empty({T, K}, i32), weights = at::empty({T, K}, x.options().dtype(at::kFloat)),
-                     offsets = at::empty({E + 1}, i32), row_token = at::empty({T * K}, i32),
-                     token_rows = at::empty({T, K}, i32);
+    need(T <= INT32_MAX && T * K <= INT32_MAX);
+    // One allocation for the five results: each allocation costs a tenth of a short call.
+    const int64_t part = aligned_part(T * K), last = aligned_part(E + 1);
+    const at::Tensor all = at::empty({4 * part + last}, x.options().dtype(at::kInt));
+    const at::Tensor ids = part_of(all, at::kInt, 0, {T, K}), weights = part_of(all, at::kFloat, part, {T, K}),
+                     row_token = part_of(all, at::kInt, 2 * part, {T * K}),
+                     token_rows = part_of(all, at::kInt, 3 * part, {T, K}),
+                     offsets = part_of(all, at::kInt, 4 * part, {E + 1});
     const size_t bytes = g_route_workspace(T, (int32_t)E);
     at::Tensor ws;
     if (bytes) ws = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));

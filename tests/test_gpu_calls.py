@@ -130,3 +130,23 @@ def test_short_path_keeps_no_references():
         calls()
     gc.collect()
     assert torch.cuda.memory_allocated() == before
+
+
+def test_route_results_do_not_share_elements():
+    """The five results of one call lie in one allocation: apart, aligned, and good for
+    views, in-place operations and the library's other calls."""
+    m = _m()
+    r = m.route(torch.randn(37, 21, device="cuda"), 5)
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * 4) for t in r)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    assert all(t.data_ptr() % 256 == 0 and t.is_contiguous() for t in r)
+    keep = [t.clone() for t in r]
+    for i, t in enumerate(r):
+        t.fill_(3)
+        assert all(torch.equal(u, v) for u, v in zip(r[i + 1:], keep[i + 1:]))
+    assert r.weights.view(-1)[2:].sum() == 3 * (37 * 5 - 2) and r.ids.t().contiguous().shape == (5, 37)
+    del keep, t
+    ids = r.ids
+    del r
+    torch.empty(1000, device="cuda").zero_()
+    assert (ids == 3).all()
