@@ -11,13 +11,14 @@
 //
 // A token is ranked by 64 lanes, or from kRouteNarrow tokens on by 16 where they can
 // hold its experts (16 each).  Four tokens a wavefront share every instruction: 16384
-// tokens of 256 BF16 logits, top-8, rank in 12.4 us against 21.5; but each lane then
-// works through four times the experts, which shows while there is a wavefront or two
-// for a SIMD: 2048 tokens with sigmoid scores in groups take 17.8 us against 16.0, one token
-// 6.7 against 5.3.  A lane holds consecutive experts of one group, so the order of
-// (lane, place) is the order of experts and the first holder of the maximum wins a
-// tie.  Sigmoid values are ranked in FP64: neighbouring scores of a few hundred
-// experts come closer than an FP32 step often enough to swap experts.
+// tokens of 256 BF16 logits, top-8, rank in 12.4 us against 21.5 (10.7 with the
+// expert in the key); but each lane then works through four times the experts, which
+// shows while there is a wavefront or two for a SIMD: 2048 tokens with sigmoid scores in
+// groups take 17.8 us against 16.0, one token 6.7 against 5.3.  A lane holds
+// consecutive experts of one group, so the order of (lane, place) is the order of
+// experts and the first holder of the maximum wins a tie.  Sigmoid values are ranked in
+// FP64: neighbouring scores of a few hundred experts come closer than an FP32 step
+// often enough to swap experts.
 //
 // Bound: instructions (each slot is two reductions over a token's lanes) and, up to a
 // few thousand tokens, the launches; the bytes (16384 tokens: 10.5 MB) would take 2 us.
@@ -41,6 +42,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
+constexpr int kFewPairs = 32;
 // Ranking values below every score: a NaN (below -inf), and an expert that is taken,
 // closed or no expert at all.
 constexpr double kKeyMinusInf = -1.0e308, kKeyNaN = -1.5e308;
@@ -50,9 +52,12 @@ __device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xf, false);
 }
 
-// Ranking keys: FP32 logits as integers of the same order, FP64 scores as they are.
+// Ranking keys: FP32 logits as integers of the same order; 16-bit logits so too, with
+// the expert's complement below them, which makes every key different and carries the
+// expert along; FP64 scores as they are.
 struct Key32 {
   typedef uint32_t T;
+  static constexpr bool kUnique = false;
   static __device__ __forceinline__ T none() { return 0u; }
   static __device__ __forceinline__ T of(float x) {
     if (x != x) return 1u;
@@ -70,11 +75,22 @@ struct Key32 {
   }
 };
 
+struct Key16 : Key32 {
+  static constexpr bool kUnique = true;
+  static __device__ __forceinline__ T of(float x, bool f16, int32_t expert) {
+    x += 0.0f;  // -0 ranks as +0
+    const uint32_t b = f16 ? __builtin_bit_cast(uint16_t, (_Float16)x) : __builtin_bit_cast(uint32_t, x) >> 16;
+    const uint32_t order = x != x ? 1u : (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
+    return order << 16 | (0xFFFFu - (uint32_t)expert);
+  }
+};
+
 struct Key64 {
   typedef double T;
+  static constexpr bool kUnique = false;
   static __device__ __forceinline__ T none() { return -__builtin_inf(); }
   static __device__ __forceinline__ T of(double s) {
-    return s != s ? kKeyNaN : s < kKeyMinusInf ? kKeyMinusInf : s;
+    return s != s ? kKeyNaN : s < kKeyMinusInf ? kKeyMinusInf : s + 0.0;
   }
   static __device__ __forceinline__ T larger(T a, T b) { return __builtin_fmax(a, b); }
   static __device__ __forceinline__ T smaller(T a, T b) { return __builtin_fmin(a, b); }
@@ -118,6 +134,26 @@ struct Word {  // an unsigned number as a key
     return (T)__builtin_amdgcn_readlane((int)v, l);
   }
 };
+
+// The lanes of the wavefront that hold its largest key.
+template <typename K>
+__device__ __forceinline__ uint64_t wave_holders(typename K::T v) {
+  if constexpr (sizeof(typename K::T) == 4) {
+    return __ballot(v == token_max<K, 64>(v));
+  } else {
+    // By the upper halves, as integers of the same order; by the lower ones only where
+    // several lanes share the upper one.
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t o = (int64_t)b < 0 ? ~b : b | 0x8000000000000000ull;
+    const uint32_t hi = (uint32_t)(o >> 32);
+    const bool top = hi == token_max<Word, 64>(hi);
+    const uint64_t tops = __ballot(top);
+    if (__popcll(tops) == 1) return tops;
+    const uint32_t lo = top ? (uint32_t)o : 0u;
+    const uint32_t most = token_max<Word, 64>(lo);
+    return __ballot(top && lo == most);
+  }
+}
 
 template <int LT>
 __device__ __forceinline__ float token_sum(float v) {
@@ -179,13 +215,19 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t i, int32
                                 : __builtin_bit_cast(float, (uint32_t)raw[j] << 16);
 }
 
+// kind of ranking: by FP32 logits, by 16-bit logits, by sigmoid scores
+enum { kByLogit = 0, kByShortLogit = 1, kByScore = 2 };
+template <int KIND>
+using KeyOf = std::conditional_t<KIND == kByScore, Key64, std::conditional_t<KIND == kByShortLogit, Key16, Key32>>;
+
 // Rank token t with LT lanes; `on`: there is such a token (lanes of a wavefront may hold
 // several).  Lane s < topk of the token's returns the expert and weight of slot s.
-template <bool SIGMOID, int LT, int VPL>
+template <int KIND, int LT, int VPL>
 __device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, bool on, int lane, int32_t* id,
                                            float* weight) {
-  typedef typename std::conditional<SIGMOID, Key64, Key32>::type K;
+  typedef KeyOf<KIND> K;
   typedef typename K::T KeyT;
+  constexpr bool SIGMOID = KIND == kByScore;
   const int32_t own = lane % LT;                  // among the token's lanes
   const int32_t size = a.experts / a.num_groups;  // experts of a group
   const int32_t group = own / a.group_lanes;
@@ -199,9 +241,11 @@ __device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, bool o
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const bool ok = j < count;
-    if (SIGMOID) {
+    if constexpr (SIGMOID) {
       const double p = 1.0 / (1.0 + exp(-(double)val[j]));
       key[j] = ok ? K::of(a.bias ? p + (double)a.bias[ok ? expert0 + j : 0] : p) : K::none();
+    } else if constexpr (K::kUnique) {
+      key[j] = ok ? K::of(val[j], a.dtype == kRouteF16, expert0 + j) : K::none();
     } else {
       key[j] = ok ? K::of(val[j]) : K::none();
     }
@@ -226,16 +270,23 @@ __device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, bool o
       best = K::larger(best, key[j]);
       second = K::larger(second, low);
     }
-    for (int d = 1; d < a.group_lanes; d <<= 1) {
-      const KeyT b = __shfl_xor(best, d, 64), s = __shfl_xor(second, d, 64);
+    // Over the group's lanes: neighbours, pairs, halves and rows of a row by lane moves.
+    auto join = [&](KeyT b, KeyT s) {
       const KeyT low = K::smaller(best, b);
       best = K::larger(best, b);
       second = K::larger(low, K::larger(second, s));
-    }
+    };
+    const int32_t gl = a.group_lanes;
+    if (gl > 1) join(K::template moved<0xB1, 0xf>(best), K::template moved<0xB1, 0xf>(second));
+    if (gl > 2) join(K::template moved<0x4E, 0xf>(best), K::template moved<0x4E, 0xf>(second));
+    if (gl > 4) join(K::template moved<0x141, 0xf>(best), K::template moved<0x141, 0xf>(second));
+    if (gl > 8) join(K::template moved<0x140, 0xf>(best), K::template moved<0x140, 0xf>(second));
+    for (int d = 16; d < gl; d <<= 1) join(__shfl_xor(best, d, 64), __shfl_xor(second, d, 64));
     const KeyT score = SIGMOID && size > 1 ? best + second : best;
     int32_t ahead = 0;
     for (int32_t o = 0; o < a.num_groups; ++o) {
-      const KeyT other = __shfl(score, lane - own + o * a.group_lanes, 64);
+      const KeyT other = LT == 64 ? K::lane(score, o * a.group_lanes)
+                                  : __shfl(score, lane - own + o * a.group_lanes, 64);
       ahead += other > score || (other == score && o < group) ? 1 : 0;
     }
     if (ahead >= a.topk_groups) {
@@ -248,12 +299,23 @@ __device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, bool o
     KeyT best = key[0];
 #pragma unroll
     for (int j = 1; j < VPL; ++j) best = K::larger(best, key[j]);
-    const KeyT m = token_max<K, LT>(best);
-    // The lowest expert that holds it, as the largest complement.
-    uint32_t not_expert = 0;
+    int32_t chosen;
+    if constexpr (K::kUnique) {
+      chosen = (int32_t)(0xFFFFu - (token_max<K, LT>(best) & 0xFFFFu));
+    } else if constexpr (LT == 64) {
+      const int holder = __ffsll((unsigned long long)wave_holders<K>(best)) - 1;
+      int32_t at = 0;
 #pragma unroll
-    for (int j = VPL - 1; j >= 0; --j) not_expert = key[j] == m ? ~(uint32_t)(expert0 + j) : not_expert;
-    const int32_t chosen = (int32_t)~token_max<Word, LT>(not_expert);
+      for (int j = VPL - 1; j >= 0; --j) at = key[j] == best ? j : at;
+      chosen = __builtin_amdgcn_readlane(expert0 + at, holder);
+    } else {
+      // The lowest expert that holds it, as the largest complement.
+      const KeyT m = token_max<K, LT>(best);
+      uint32_t not_expert = 0;
+#pragma unroll
+      for (int j = VPL - 1; j >= 0; --j) not_expert = key[j] == m ? ~(uint32_t)(expert0 + j) : not_expert;
+      chosen = (int32_t)~token_max<Word, LT>(not_expert);
+    }
     if (own == s) my_id = chosen;
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
@@ -331,7 +393,7 @@ __device__ __forceinline__ void mark(uint32_t* marks, int32_t e, int32_t tl, int
 }
 
 // Ranks a block of tokens; leaves the block's rows per expert (16-bit) in counts.
-template <bool SIGMOID, int LT, int VPL>
+template <int KIND, int LT, int VPL>
 __global__ __launch_bounds__(kThreads) void k_rank(RouteArgs a) {
   extern __shared__ __align__(16) int32_t count[];  // [counts_pitch]
   const int tid = threadIdx.x, lane = tid & 63, own = lane % LT;
@@ -344,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void k_rank(RouteArgs a) {
     const bool on = tl < here;
     int32_t id;
     float w;
-    rank_token<SIGMOID, LT, VPL>(a, t0 + (on ? tl : 0), on, lane, &id, &w);
+    rank_token<KIND, LT, VPL>(a, t0 + (on ? tl : 0), on, lane, &id, &w);
     if (on && own < a.topk) {
       const int64_t o = (int64_t)(t0 + tl) * a.topk + own;
       a.ids[o] = id;
@@ -401,7 +463,7 @@ __global__ __launch_bounds__(kThreads) void k_place(RouteArgs a) {
 }
 
 // Both steps of at most kRouteOneBlock tokens in one workgroup.
-template <bool SIGMOID, int LT, int VPL>
+template <int KIND, int LT, int VPL>
 __global__ __launch_bounds__(kThreads) void k_route_small(RouteArgs a) {
   extern __shared__ __align__(16) int32_t lds[];
   const int words = a.tokens > 32 ? 2 : 1;
@@ -419,7 +481,7 @@ __global__ __launch_bounds__(kThreads) void k_route_small(RouteArgs a) {
     const bool on = t < a.tokens;
     int32_t id;
     float w;
-    rank_token<SIGMOID, LT, VPL>(a, on ? t : 0, on, lane, &id, &w);
+    rank_token<KIND, LT, VPL>(a, on ? t : 0, on, lane, &id, &w);
     if (on && own < a.topk) {
       a.ids[t * a.topk + own] = id;
       a.weights[t * a.topk + own] = w;
@@ -428,6 +490,23 @@ __global__ __launch_bounds__(kThreads) void k_route_small(RouteArgs a) {
     }
   }
   __syncthreads();
+  const int32_t pairs = a.tokens * a.topk;
+  if (pairs <= kFewPairs) {
+    // Few enough to compare each with all: no scan.
+    for (int e = tid; e <= a.experts; e += blockDim.x) {
+      int32_t lower = 0;
+      for (int q = 0; q < pairs; ++q) lower += ids[q] < e ? 1 : 0;
+      a.offsets[e] = lower;
+    }
+    if (tid < pairs) {
+      const int32_t id = ids[tid];
+      int32_t row = 0;
+      for (int q = 0; q < pairs; ++q) row += ids[q] < id || (ids[q] == id && q < tid) ? 1 : 0;
+      a.token_rows[tid] = row;
+      a.row_token[row] = tid / a.topk;
+    }
+    return;
+  }
   for (int i = tid; i < a.experts; i += blockDim.x) {
     int32_t c = 0;
     for (int w = 0; w < words; ++w) c += __popc(marks[i * words + w]);
@@ -444,18 +523,18 @@ int rank_threads(int64_t tokens, int lt) {
   return t < 64 ? 64 : t < kThreads ? (int)t : kThreads;
 }
 
-template <bool SIGMOID, int LT, int VPL>
+template <int KIND, int LT, int VPL>
 hipError_t launch(const RouteArgs& a, hipStream_t stream) {
   if (a.tokens <= kRouteOneBlock) {
     // At least four wavefronts: they share the scan over the experts.
     const int threads = rank_threads(a.tokens, LT);
     const size_t lds = (size_t)((2 + (a.tokens > 32 ? 2 : 1)) * a.experts + kWaves + a.tokens * a.topk) * 4;
-    hipLaunchKernelGGL((k_route_small<SIGMOID, LT, VPL>), dim3(1), dim3(threads < 256 ? 256 : threads), lds,
+    hipLaunchKernelGGL((k_route_small<KIND, LT, VPL>), dim3(1), dim3(threads < 256 ? 256 : threads), lds,
                        stream, a);
     return hipGetLastError();
   }
   const int blocks = (int)((a.tokens + a.block_tokens - 1) / a.block_tokens);
-  hipLaunchKernelGGL((k_rank<SIGMOID, LT, VPL>), dim3(blocks), dim3(rank_threads(a.block_tokens, LT)),
+  hipLaunchKernelGGL((k_rank<KIND, LT, VPL>), dim3(blocks), dim3(rank_threads(a.block_tokens, LT)),
                      (size_t)a.counts_pitch * 4, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
@@ -465,24 +544,25 @@ hipError_t launch(const RouteArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool SIGMOID, int LT>
+template <int KIND, int LT>
 hipError_t launch_sized(const RouteArgs& a, hipStream_t stream) {
-  if (a.per_lane <= 1) return launch<SIGMOID, LT, 1>(a, stream);
-  if (a.per_lane <= 2) return launch<SIGMOID, LT, 2>(a, stream);
-  if (a.per_lane <= 4) return launch<SIGMOID, LT, 4>(a, stream);
-  if (a.per_lane <= 8) return launch<SIGMOID, LT, 8>(a, stream);
-  return launch<SIGMOID, LT, 16>(a, stream);
+  if (a.per_lane <= 1) return launch<KIND, LT, 1>(a, stream);
+  if (a.per_lane <= 2) return launch<KIND, LT, 2>(a, stream);
+  if (a.per_lane <= 4) return launch<KIND, LT, 4>(a, stream);
+  if (a.per_lane <= 8) return launch<KIND, LT, 8>(a, stream);
+  return launch<KIND, LT, 16>(a, stream);
 }
 
-template <bool SIGMOID>
+template <int KIND>
 hipError_t launch_lanes(const RouteArgs& a, hipStream_t stream) {
-  return a.token_lanes == 16 ? launch_sized<SIGMOID, 16>(a, stream) : launch_sized<SIGMOID, 64>(a, stream);
+  return a.token_lanes == 16 ? launch_sized<KIND, 16>(a, stream) : launch_sized<KIND, 64>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
-  return a.sigmoid ? launch_lanes<true>(a, stream) : launch_lanes<false>(a, stream);
+  if (a.sigmoid) return launch_lanes<kByScore>(a, stream);
+  return a.dtype == kRouteF32 ? launch_lanes<kByLogit>(a, stream) : launch_lanes<kByShortLogit>(a, stream);
 }
 
 }  // namespace moe_fp4
