@@ -15,6 +15,10 @@
 //     whatever the token count, each touching 64 places.
 //   - block scales: one load covers four steps (64 bytes of each row); a dword a
 //     step and lane touches as many lines as the codes do for an eighth of the bytes.
+// Codes go from memory to registers.  Loading them in 64-byte pieces of a row and turning
+// them in LDS was no gain (64 experts, 32 tokens: 105 us against 108; 256 experts, 8 tokens: 48.5
+// against 44.6), nor was the non-temporal hint, which discards the other half of a line that
+// two loads share (65536 x 6144, codes alone: 57 us against 48).
 //
 // Any K that is a multiple of 16 and at least 64 runs: a lane whose 64 elements pass
 // the end of the row reads the row's last 64 and moves them down; scales and
