@@ -15,10 +15,9 @@
 //     whatever the token count, each touching 64 places.
 //   - block scales: one load covers four steps (64 bytes of each row); a dword a
 //     step and lane touches as many lines as the codes do for an eighth of the bytes.
-// Codes go from memory to registers.  Loading them in 64-byte pieces of a row and turning
-// them in LDS was no gain (64 experts, 32 tokens: 105 us against 108; 256 experts, 8 tokens: 48.5
-// against 44.6), nor was the non-temporal hint, which discards the other half of a line that
-// two loads share (65536 x 6144, codes alone: 57 us against 48).
+//   - codes, in the variants that stream much for few tokens: see Pieces below.
+// No load takes the non-temporal hint: two loads share each line of codes (65536 x 6144,
+// codes alone: 57 us with it against 48).
 //
 // Any K that is a multiple of 16 and at least 64 runs: a lane whose 64 elements pass
 // the end of the row reads the row's last 64 and moves them down; scales and
@@ -121,6 +120,65 @@ __device__ __forceinline__ void move_codes(Codes<NT>& c, int32_t left) {
   }
 }
 
+// Pieces: the codes of a step on their way, as four neighbouring lanes read them from 64
+// consecutive bytes of a row: lane l holds pieces of row l / 4 of each tile, which the
+// wavefront turns into Codes through its own LDS.  Read as the products want them,
+// neighbouring lanes read different rows, and the L1 cache takes one line at a time.
+// 65536 x 6144, four tokens: 47.8 us against 52.0 with Codes read directly.  Variants
+// of one tile a wavefront (few rows: latency) or of more tokens (LDS, registers) read
+// directly: 6144 x 6144, one token 8.8 us against 9.3 turned; up projections of 64 experts, 32 tokens
+// 60.5 against 61.6.  So does the layer's down projection, which has a step or a few an
+// expert: 256 experts, eight tokens 16.7 us against 21.4.
+constexpr int kPieceBytes = 2048;  // LDS in which one tile's codes are turned
+
+// Which of the four 16-byte pieces of a 64-byte half lane l reads of row l / 4: staggered,
+// so that sixteen rows' equal pieces lie in different banks.
+__device__ __forceinline__ int32_t piece_of(int32_t lane) { return (lane ^ (lane >> 4)) & 3; }
+
+// row_off: start of row lane / 4 of each tile.  A piece that passes the row's end, k / 2, is
+// read 8 bytes earlier or, past the end, from its last 16 bytes: its scales are 0.
+template <int NT>
+__device__ __forceinline__ void load_pieces(Codes<NT>& c, rsrc_t q_rs, const uint32_t (&row_off)[NT],
+                                            int32_t step, int32_t end, int32_t lane, int32_t k) {
+  uint32_t off0 = (uint32_t)(step * (kFewStep / 2) + 16 * piece_of(lane)), off1 = off0 + 64u;
+  if ((step + 1) * kFewStep > k) {  // uniform
+    const uint32_t last = (uint32_t)(k / 2 - 16);
+    off0 = off0 < last ? off0 : last;
+    off1 = off1 < last ? off1 : last;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t row = step < end ? row_off[t] : kOutOfRange;
+    c.q[t][0] = __builtin_amdgcn_raw_buffer_load_b128(q_rs, row + off0, 0, 0);
+    c.q[t][1] = __builtin_amdgcn_raw_buffer_load_b128(q_rs, row + off1, 0, 0);
+  }
+}
+
+// Pieces to Codes, through NT * kPieceBytes of the wavefront's LDS.
+template <int NT>
+__device__ __forceinline__ void turn_pieces(Codes<NT>& c, char* lds, int32_t step, int32_t lane, int32_t k) {
+  if ((step + 1) * kFewStep > k) {  // uniform: a piece may have been read 8 bytes early
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool early = step * (kFewStep / 2) + 64 * h + 16 * piece_of(lane) == k / 2 - 8;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (early) c.q[t][h] = u32x4_t{c.q[t][h][2], c.q[t][h][3], 0u, 0u};
+    }
+  }
+  const int32_t r = lane & 15, g = lane >> 4;
+  const char* from = lds + (g >> 1) * 1024 + 64 * r;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<u32x4_t*>(lds + t * kPieceBytes + h * 1024 + 16 * lane) = c.q[t][h];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      c.q[t][h] = *reinterpret_cast<const u32x4_t*>(from + t * kPieceBytes + 16 * ((2 * (g & 1) + h) ^ (r >> 2)));
+  }
+}
+
 // The eight matrix products of a step: operand J covers elements 8J .. 8J+7 of each
 // lane's 64.  x(J): the token operands; f(J, t, a, x): multiply tile t.
 template <bool F16, int NT, int J, typename X, typename F>
@@ -177,11 +235,18 @@ struct FewLoop {
     u32x4_t x[PF];
   };
   static constexpr int kChunk = 8;  // steps whose scales are in LDS at once
+  static constexpr bool kTurn = NT > 1 && XR <= 2;  // see Pieces
   static constexpr int kXBytes = XR * 1024, kSBytes = NT * 2048;
-  static constexpr int kLdsBytes = kXBytes + kSBytes;  // of a wavefront; its sums take the place of both
+  // Of a wavefront; its sums take the place of all.
+  static constexpr int kLdsBytes = kXBytes + kSBytes + (kTurn ? NT * kPieceBytes : 0);
+
+  // The weight row (0..15 of a tile) whose codes and scales a lane loads, and which quarter of
+  // what is read of that row.
+  static __device__ __forceinline__ int row_of(int lane) { return kTurn ? lane >> 2 : lane & 15; }
+  static __device__ __forceinline__ int quarter_of(int lane) { return kTurn ? lane & 3 : lane >> 4; }
 
   rsrc_t q_rs, s_rs, x_rs;
-  uint32_t q_off[NT], s_off[NT];  // row starts, bytes
+  uint32_t q_off[NT], s_off[NT];  // starts of row row_of(lane) of each tile, bytes
   uint32_t x_off[XR];             // start of this lane's 16 bytes of token 2i + lane / 32
   char* lds;                      // kLdsBytes of this wavefront
   int32_t k, tokens, lane;
@@ -193,15 +258,18 @@ struct FewLoop {
   }
 
   __device__ __forceinline__ void load(Stage& r, int32_t step, int32_t end) const {
-    load_codes<NT>(r.c, q_rs, q_off, step < end ? code_offset(step, lane >> 4, k) : kOutOfRange);
+    if (kTurn)
+      load_pieces<NT>(r.c, q_rs, q_off, step, end, lane, k);
+    else
+      load_codes<NT>(r.c, q_rs, q_off, step < end ? code_offset(step, lane >> 4, k) : kOutOfRange);
 #pragma unroll
     for (int i = 0; i < PF; ++i)
       r.x[i] = __builtin_amdgcn_raw_buffer_load_b128(x_rs, x_offset(i, step, end), 0, 0);
   }
 
-  // Scales of steps base .. base + 3: lane (row, i) takes the 16 bytes of step base + i.
+  // Scales of steps base .. base + 3: a row's quarter i is the 16 bytes of step base + i.
   __device__ __forceinline__ void load_scales(u32x4_t (&s)[NT], int32_t base, int32_t end) const {
-    const int32_t step = base + (lane >> 4);
+    const int32_t step = base + quarter_of(lane);
     const int32_t last = base + 4 < end ? base + 4 : end;
     if (last * kFewStep <= k) {
 #pragma unroll
@@ -225,7 +293,7 @@ struct FewLoop {
   __device__ __forceinline__ void put_scales(const u32x4_t (&s)[NT], int h) const {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<u32x4_t*>(lds + kXBytes + (t * 2 + h) * 1024 + lane * 16) = s[t];
+      *reinterpret_cast<u32x4_t*>(lds + kXBytes + (t * 2 + h) * 1024 + (quarter_of(lane) * 16 + row_of(lane)) * 16) = s[t];
   }
 
   // 16-byte piece c (0..31) of token t is kept at piece c ^ (t % 16): sixteen tokens'
@@ -244,7 +312,10 @@ struct FewLoop {
       if (2 * j < tokens)
         put_x(j, __builtin_amdgcn_raw_buffer_load_b128(x_rs, x_offset(j, step, step + 1), 0, 0));
     const int32_t g = lane >> 4, col = lane & 15;
-    if ((step + 1) * kFewStep > k) move_codes<NT>(r.c, blocks_left(step * kFewStep + 64 * g, k));
+    if (kTurn)
+      turn_pieces<NT>(r.c, lds + kXBytes + kSBytes, step, lane, k);
+    else if ((step + 1) * kFewStep > k)
+      move_codes<NT>(r.c, blocks_left(step * kFewStep + 64 * g, k));
     uint32_t s[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)

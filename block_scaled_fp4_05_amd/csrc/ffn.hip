@@ -151,8 +151,9 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
   const int r = lane & 15;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {  // rows 0-7 of a tile: gate; 8-15: the same columns of up
-    const int32_t col = c0 + 8 * t + (r & 7);
-    const uint32_t row = (uint32_t)((r >> 3) * inter + (col < inter ? col : inter - 1));
+    const int lr = Loop::row_of(lane);
+    const int32_t col = c0 + 8 * t + (lr & 7);
+    const uint32_t row = (uint32_t)((lr >> 3) * inter + (col < inter ? col : inter - 1));
     loop.q_off[t] = row * (uint32_t)(k / 2);
     loop.s_off[t] = row * (uint32_t)(k / 16);
   }

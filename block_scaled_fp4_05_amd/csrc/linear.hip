@@ -12,7 +12,7 @@
 // wavefront order (no atomics: the same inputs give the same bits).
 //
 // Measured, kernel time on weights that are in no cache: 65536 x 6144, four BF16 tokens, FP32
-// out: 52.0 us, 4.4 TB/s (a large copy reaches 5.05).  8192 x 6144 with SwiGLU, 16
+// out: 47.9 us, 4.7 TB/s (a large copy reaches 5.05).  8192 x 6144 with SwiGLU, 16
 // FP16 tokens: 11.8 us, 2.4 TB/s.  6144 x 6144, one token: 8.8 us, 2.4 TB/s: one or two
 // workgroups a CU, whose start, first loads and final sum nothing covers.
 #include <hip/hip_runtime.h>
@@ -51,12 +51,13 @@ __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
   loop.lane = lane;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    const int lr = Loop::row_of(lane);
     int32_t row;
     if (swiglu) {  // rows 0-7 of a tile: gate; 8-15: the same columns of up
-      const int32_t c = n0 + 8 * t + (r & 7);
-      row = (r >> 3) * half + (c < half ? c : half - 1);
+      const int32_t c = n0 + 8 * t + (lr & 7);
+      row = (lr >> 3) * half + (c < half ? c : half - 1);
     } else {
-      const int32_t c = n0 + 16 * t + r;
+      const int32_t c = n0 + 16 * t + lr;
       row = c < a.n ? c : a.n - 1;
     }
     loop.q_off[t] = (uint32_t)row * (uint32_t)(a.k / 2);
@@ -124,7 +125,7 @@ hipError_t launch_rows(const LinearArgs& a, int items, int waves, hipStream_t st
 
 // Two tiles an item (half the activation reads and half the wavefronts) once that
 // leaves an item for every CU: 8192 x 6144, 16 tokens 13.6 us against 14.8; 65536 x 6144,
-// 4 tokens 54 against 56; but 6144 x 6144, one token 9.8 against 9.7.  Four wavefronts an
+// 4 tokens 54 against 56 (before the codes were turned in LDS); but 6144 x 6144, one token 9.8 against 9.7.  Four wavefronts an
 // item, eight where there are few items to fill the CUs (one or two wavefronts
 // on 6144 x 6144: 17.9 and 13.1 us; eight on 65536 x 6144: 63 us).
 template <bool F16>

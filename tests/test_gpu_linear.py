@@ -59,6 +59,17 @@ def test_linear_swiglu(m, n, k, dtype, out):
     ref.check(got, *ref.linear(x.double(), ref.values(q, sf), float(np.float32(3 * scale)), True))
 
 
+@pytest.mark.parametrize("k", range(64, 592, 16))
+def test_linear_many_rows_ending_anywhere_in_a_step(k):
+    """Rows enough for two tiles a wavefront, whose codes are turned in LDS: every place
+    in a step where a row can end."""
+    for m, dtype in ((2, "bf16"), (4, "fp16")):
+        say(f"linear tail {m}x8200x{k} {dtype}")
+        _, q, sf, x, scale = _case(m, 8200, k, dtype)
+        got = _run(x.cuda(), q, sf, scale, out_dtype=torch.float32)
+        ref.check(got, *ref.linear(x.double(), ref.values(q, sf), scale))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_linear_every_code_and_scale_is_exact(dtype):
     """One-hot activations read single weights: the result is the rounded weight itself,
