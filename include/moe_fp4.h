@@ -448,7 +448,9 @@ enum { MOE_FP4_SCORE_SOFTMAX = 0, MOE_FP4_SCORE_SIGMOID = 1 };
  *             ranking value (SOFTMAX) or the sum of its two largest (SIGMOID).
  *   ties      go to the lower index, in both choices.  A NaN ranks below every number.
  *   weights   p of the chosen experts (the bias plays no part); renormalize: divided by
- *             their sum (with SOFTMAX, the softmax over the chosen experts).
+ *             their sum (with SOFTMAX, the softmax over the chosen experts).  A token
+ *             whose logits are all -inf has the formula's NaN weights (SIGMOID without
+ *             renormalize: 0); its experts are valid, and its rows placed, all the same.
  *   slots     in descending order of the ranking value.
  *   rows      all (token, slot) pairs ordered by expert, then token: expert e owns rows
  *             [offsets[e], offsets[e + 1]); row r is of token row_token[r]; slot s of
