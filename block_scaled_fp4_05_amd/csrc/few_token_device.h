@@ -124,11 +124,11 @@ __device__ __forceinline__ void move_codes(Codes<NT>& c, int32_t left) {
 // consecutive bytes of a row: lane l holds pieces of row l / 4 of each tile, which the
 // wavefront turns into Codes through its own LDS.  Read as the products want them,
 // neighbouring lanes read different rows, and the L1 cache takes one line at a time.
-// 65536 x 6144, four tokens: 47.8 us against 52.0 with Codes read directly.  Variants
-// of one tile a wavefront (few rows: latency) or of more tokens (LDS, registers) read
-// directly: 6144 x 6144, one token 8.8 us against 9.3 turned; up projections of 64 experts, 32 tokens
-// 60.5 against 61.6.  So does the layer's down projection, which has a step or a few an
-// expert: 256 experts, eight tokens 16.7 us against 21.4.
+// 65536 x 6144, four tokens: 47.8 us against 52.0 with Codes read directly; eight
+// tokens 59 against 63.  Variants of one tile a wavefront (few rows: latency) or of more
+// tokens (LDS, registers) read directly: 6144 x 6144, one token 8.8 us against 9.3 turned; up
+// projections of 64 experts, 32 tokens 60.5 against 61.6.  So does the layer's down projection,
+// which has a step or a few an expert: 256 experts, eight tokens 16.7 us against 21.4.
 constexpr int kPieceBytes = 2048;  // LDS in which one tile's codes are turned
 
 // Which of the four 16-byte pieces of a 64-byte half lane l reads of row l / 4: staggered,
@@ -227,23 +227,22 @@ struct TokenOperands {
 // them kept in flight, the rest (where there are as many tokens) loaded when needed.
 // Two steps are in flight; a load that has nothing to fetch is sent out of range
 // instead of being branched around, so that the compiler's counts of outstanding
-// loads stay exact.
-template <bool F16, int NT, int MT, int XR, int PF>
+// loads stay exact.  TURN: codes are read as Pieces.
+template <bool F16, int NT, int MT, int XR, int PF, bool TURN>
 struct FewLoop {
   struct Stage {
     Codes<NT> c;
     u32x4_t x[PF];
   };
   static constexpr int kChunk = 8;  // steps whose scales are in LDS at once
-  static constexpr bool kTurn = NT > 1 && XR <= 2;  // see Pieces
   static constexpr int kXBytes = XR * 1024, kSBytes = NT * 2048;
   // Of a wavefront; its sums take the place of all.
-  static constexpr int kLdsBytes = kXBytes + kSBytes + (kTurn ? NT * kPieceBytes : 0);
+  static constexpr int kLdsBytes = kXBytes + kSBytes + (TURN ? NT * kPieceBytes : 0);
 
   // The weight row (0..15 of a tile) whose codes and scales a lane loads, and which quarter of
   // what is read of that row.
-  static __device__ __forceinline__ int row_of(int lane) { return kTurn ? lane >> 2 : lane & 15; }
-  static __device__ __forceinline__ int quarter_of(int lane) { return kTurn ? lane & 3 : lane >> 4; }
+  static __device__ __forceinline__ int row_of(int lane) { return TURN ? lane >> 2 : lane & 15; }
+  static __device__ __forceinline__ int quarter_of(int lane) { return TURN ? lane & 3 : lane >> 4; }
 
   rsrc_t q_rs, s_rs, x_rs;
   uint32_t q_off[NT], s_off[NT];  // starts of row row_of(lane) of each tile, bytes
@@ -258,7 +257,7 @@ struct FewLoop {
   }
 
   __device__ __forceinline__ void load(Stage& r, int32_t step, int32_t end) const {
-    if (kTurn)
+    if (TURN)
       load_pieces<NT>(r.c, q_rs, q_off, step, end, lane, k);
     else
       load_codes<NT>(r.c, q_rs, q_off, step < end ? code_offset(step, lane >> 4, k) : kOutOfRange);
@@ -312,7 +311,7 @@ struct FewLoop {
       if (2 * j < tokens)
         put_x(j, __builtin_amdgcn_raw_buffer_load_b128(x_rs, x_offset(j, step, step + 1), 0, 0));
     const int32_t g = lane >> 4, col = lane & 15;
-    if (kTurn)
+    if (TURN)
       turn_pieces<NT>(r.c, lds + kXBytes + kSBytes, step, lane, k);
     else if ((step + 1) * kFewStep > k)
       move_codes<NT>(r.c, blocks_left(step * kFewStep + 64 * g, k));

@@ -55,7 +55,7 @@ __host__ __device__ constexpr size_t up_table_bytes(int pairs, int experts) {
 // A step's first two loads of x (four tokens) are kept in flight, the rest of a larger
 // expert's are loaded when needed.
 template <bool F16, int NT, int XR>
-using FfnLoop = FewLoop<F16, NT, 1, XR, (XR < 2 ? XR : 2)>;
+using FfnLoop = FewLoop<F16, NT, 1, XR, (XR < 2 ? XR : 2), (NT > 1 && XR <= 2)>;
 
 template <bool F16, int NT, int XR>
 __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {

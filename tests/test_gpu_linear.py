@@ -63,7 +63,7 @@ def test_linear_swiglu(m, n, k, dtype, out):
 def test_linear_many_rows_ending_anywhere_in_a_step(k):
     """Rows enough for two tiles a wavefront, whose codes are turned in LDS: every place
     in a step where a row can end."""
-    for m, dtype in ((2, "bf16"), (4, "fp16")):
+    for m, dtype in ((2, "bf16"), (4, "fp16"), (7, "bf16")):
         say(f"linear tail {m}x8200x{k} {dtype}")
         _, q, sf, x, scale = _case(m, 8200, k, dtype)
         got = _run(x.cuda(), q, sf, scale, out_dtype=torch.float32)
