@@ -217,18 +217,13 @@ __device__ __forceinline__ void store_as(void* out, int64_t i, float v, int32_t 
 // x / (1 + e^-x): exactly 0 or the identity where e^-x overflows or vanishes.
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
 
-template <int MT>
-struct TokenOperands {
-  u32x4_t v[MT];
-};
-
-// The sums of NT x 16 weight rows times up to MT x 16 tokens over a wavefront's steps
-// [s0, s1).  XR = loads of two tokens each that a step takes at most (8 MT), PF of
+// The sums of NT x 16 weight rows times up to 16 tokens over a wavefront's steps
+// [s0, s1).  XR = loads of two tokens each that a step takes at most (8), PF of
 // them kept in flight, the rest (where there are as many tokens) loaded when needed.
 // Two steps are in flight; a load that has nothing to fetch is sent out of range
 // instead of being branched around, so that the compiler's counts of outstanding
 // loads stay exact.  TURN: codes are read as Pieces.
-template <bool F16, int NT, int MT, int XR, int PF, bool TURN>
+template <bool F16, int NT, int XR, int PF, bool TURN>
 struct FewLoop {
   struct Stage {
     Codes<NT> c;
@@ -295,15 +290,15 @@ struct FewLoop {
       *reinterpret_cast<u32x4_t*>(lds + kXBytes + (t * 2 + h) * 1024 + (quarter_of(lane) * 16 + row_of(lane)) * 16) = s[t];
   }
 
-  // 16-byte piece c (0..31) of token t is kept at piece c ^ (t % 16): sixteen tokens'
+  // 16-byte piece c (0..31) of token t is kept at piece c ^ t: sixteen tokens'
   // equal pieces lie in different banks.
   __device__ __forceinline__ void put_x(int i, u32x4_t v) const {
     const int32_t t = 2 * i + (lane >> 5);
-    *reinterpret_cast<u32x4_t*>(lds + t * 512 + (((lane & 31) ^ (t & 15)) << 4)) = v;
+    *reinterpret_cast<u32x4_t*>(lds + t * 512 + (((lane & 31) ^ t) << 4)) = v;
   }
 
   // Step `step`, the i-th of those whose scales are in LDS.
-  __device__ __forceinline__ void compute(Stage& r, float4_t (&acc)[NT][MT], int32_t step, int i) const {
+  __device__ __forceinline__ void compute(Stage& r, float4_t (&acc)[NT], int32_t step, int i) const {
 #pragma unroll
     for (int j = 0; j < PF; ++j) put_x(j, r.x[j]);
 #pragma unroll
@@ -319,29 +314,16 @@ struct FewLoop {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       s[t] = *reinterpret_cast<const uint32_t*>(lds + kXBytes + t * 2048 + (col + 16 * i) * 16 + 4 * g);
-    uint32_t at[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int32_t t = 16 * m + col < tokens ? 16 * m + col : tokens - 1;
-      at[m] = (uint32_t)(t * 512 + (((8 * g) ^ (t & 15)) << 4));
-    }
+    const int32_t tok = col < tokens ? col : tokens - 1;
+    const uint32_t at = (uint32_t)(tok * 512 + (((8 * g) ^ tok) << 4));
     for_operands<F16, NT, 0>(
         r.c, s,
-        [&](int j) {
-          TokenOperands<MT> x;
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            x.v[m] = *reinterpret_cast<const u32x4_t*>(lds + (at[m] ^ (uint32_t)(j << 4)));
-          return x;
-        },
-        [&](int, int t, u32x4_t a, const TokenOperands<MT>& x) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[t][m] = mfma16<F16>(a, x.v[m], acc[t][m]);
-        });
+        [&](int j) { return *reinterpret_cast<const u32x4_t*>(lds + (at ^ (uint32_t)(j << 4))); },
+        [&](int, int t, u32x4_t a, u32x4_t x) { acc[t] = mfma16<F16>(a, x, acc[t]); });
   }
 
   // kChunk steps at a time: their scales first, then two steps in flight.
-  __device__ __forceinline__ void run(float4_t (&acc)[NT][MT], int32_t s0, int32_t s1) const {
+  __device__ __forceinline__ void run(float4_t (&acc)[NT], int32_t s0, int32_t s1) const {
     for (int32_t c0 = s0; c0 < s1; c0 += kChunk) {
       const int32_t c1 = c0 + kChunk < s1 ? c0 + kChunk : s1;
       u32x4_t sc[2][NT];
@@ -366,12 +348,10 @@ struct FewLoop {
 };
 
 // Leave a wavefront's sums in its own LDS: [tile][lane], four values each.
-template <int NT, int MT>
-__device__ __forceinline__ void put_sums(char* lds, const float4_t (&acc)[NT][MT], int lane) {
+template <int NT>
+__device__ __forceinline__ void put_sums(char* lds, const float4_t (&acc)[NT], int lane) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) reinterpret_cast<float4_t*>(lds)[(t * MT + m) * 64 + lane] = acc[t][m];
+  for (int t = 0; t < NT; ++t) reinterpret_cast<float4_t*>(lds)[t * 64 + lane] = acc[t];
 }
 
 // The sum over the wavefronts, in wavefront order, of one lane's values of a tile.

@@ -55,7 +55,7 @@ __host__ __device__ constexpr size_t up_table_bytes(int pairs, int experts) {
 // A step's first two loads of x (four tokens) are kept in flight, the rest of a larger
 // expert's are loaded when needed.
 template <bool F16, int NT, int XR>
-using FfnLoop = FewLoop<F16, NT, 1, XR, (XR < 2 ? XR : 2), (NT > 1 && XR <= 2)>;
+using FfnLoop = FewLoop<F16, NT, XR, (XR < 2 ? XR : 2), (NT > 1 && XR <= 2)>;
 
 template <bool F16, int NT, int XR>
 __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
@@ -168,12 +168,12 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
       const int32_t j = 2 * i + (lane >> 5);
       loop.x_off[i] = j < loop.tokens ? (uint32_t)(list[first + j] * a.ld_x * 2 + 16 * (lane & 31)) : kOutOfRange;
     }
-    float4_t acc[NT][1];
+    float4_t acc[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][0] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     if (first > 0) __syncthreads();  // the previous sums have been taken
     loop.run(acc, s0, s1);
-    put_sums<NT, 1>(loop.lds, acc, lane);
+    put_sums<NT>(loop.lds, acc, lane);
     __syncthreads();
     const int32_t j = first + r;
     const int32_t col = c0 + tile * 8 + 4 * ((lane >> 4) & 1);

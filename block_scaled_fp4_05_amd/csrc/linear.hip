@@ -26,20 +26,21 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 
-// XR: loads of two tokens (see FewLoop); at most eight of them are kept in flight.
-template <bool F16, int NT, int MT, int XR>
-using LinearLoop = FewLoop<F16, NT, MT, XR, (XR < 8 ? XR : 8), (NT > 1 && XR <= 4)>;
+// XR: loads of two tokens (see FewLoop), all of them kept in flight: with four of eight
+// 8192 x 6144, 16 tokens take 21.7 us instead of 13.7.
+template <bool F16, int NT, int XR>
+using LinearLoop = FewLoop<F16, NT, XR, XR, (NT > 1 && XR <= 4)>;
 
-template <bool F16, int NT, int MT, int XR>
+template <bool F16, int NT, int XR>
 __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
   extern __shared__ __align__(16) char smem[];
-  typedef LinearLoop<F16, NT, MT, XR> Loop;
+  typedef LinearLoop<F16, NT, XR> Loop;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6, r = lane & 15;
   const bool swiglu = a.swiglu != 0;
   const int32_t half = a.n / 2, cols = swiglu ? half : a.n;
   const int32_t n0 = blockIdx.x * (swiglu ? 8 : 16) * NT;
-  const int32_t m0 = blockIdx.y * 16 * MT;
+  const int32_t m0 = blockIdx.y * 16;
   const float scale = ((sconst_f32)a.w_scale)[0];
   Loop loop;
   loop.q_rs = make_rsrc(a.w_q, (uint32_t)((int64_t)a.n * (a.k / 2)));
@@ -47,7 +48,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
   loop.x_rs = make_rsrc(a.x, (uint32_t)(((a.m - 1) * a.ld_x + a.k) * 2));
   loop.lds = smem + wave * Loop::kLdsBytes;
   loop.k = a.k;
-  loop.tokens = a.m - m0 < 16 * MT ? a.m - m0 : 16 * MT;
+  loop.tokens = a.m - m0 < 16 ? a.m - m0 : 16;
   loop.lane = lane;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -68,20 +69,17 @@ __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
     const int32_t t = 2 * i + (lane >> 5);
     loop.x_off[i] = t < loop.tokens ? (uint32_t)((m0 + t) * a.ld_x * 2 + 16 * (lane & 31)) : kOutOfRange;
   }
-  float4_t acc[NT][MT];
+  float4_t acc[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int32_t steps = (a.k + kFewStep - 1) / kFewStep;
   loop.run(acc, uniform(wave * steps / waves), uniform((wave + 1) * steps / waves));
 
   // A thread's share of the result: four consecutive weight rows of one token.
-  const int tile = threadIdx.x >> 6;  // (nt, mt)
-  const int32_t tok = m0 + (tile % MT) * 16 + r;
-  const int32_t j0 = swiglu ? n0 + (tile / MT) * 8 + 4 * ((lane >> 4) & 1)
-                            : n0 + (tile / MT) * 16 + 4 * (lane >> 4);
-  const bool mine = tile < NT * MT && tok < a.m && j0 < cols && (!swiglu || lane < 32);
+  const int tile = threadIdx.x >> 6;
+  const int32_t tok = m0 + r;
+  const int32_t j0 = swiglu ? n0 + tile * 8 + 4 * ((lane >> 4) & 1) : n0 + tile * 16 + 4 * (lane >> 4);
+  const bool mine = tile < NT && tok < a.m && j0 < cols && (!swiglu || lane < 32);
   float res[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (a.residual && mine) {  // its latency passes under the barrier
     const uint16_t* rp = static_cast<const uint16_t*>(a.residual) + tok * a.ld_res + j0;
@@ -91,7 +89,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) res[i] = value16<F16>(raw[i]);
   }
-  put_sums<NT, MT>(loop.lds, acc, lane);
+  put_sums<NT>(loop.lds, acc, lane);
   __syncthreads();
   if (!mine) return;
   float4_t v = take_sum(smem, Loop::kLdsBytes, tile, lane, waves) * scale;
@@ -106,25 +104,26 @@ __global__ __launch_bounds__(kMaxThreads) void k_linear(LinearArgs a) {
     if (j0 + i < cols) store_as(a.out, o + i, a.residual ? v[i] + res[i] : v[i], a.out_dtype);
 }
 
-template <bool F16, int NT, int MT, int XR>
+template <bool F16, int NT, int XR>
 hipError_t launch(const LinearArgs& a, int items, int waves, hipStream_t stream) {
-  if (waves < NT * MT) waves = NT * MT;  // a wavefront finishes one tile of the result
-  const dim3 grid(items, (a.m + 16 * MT - 1) / (16 * MT));
-  const size_t lds = (size_t)waves * LinearLoop<F16, NT, MT, XR>::kLdsBytes;
-  hipLaunchKernelGGL((k_linear<F16, NT, MT, XR>), grid, dim3(waves * 64), lds, stream, a);
+  if (waves < NT) waves = NT;  // a wavefront finishes one tile of the result
+  const dim3 grid(items, (a.m + 15) / 16);
+  const size_t lds = (size_t)waves * LinearLoop<F16, NT, XR>::kLdsBytes;
+  hipLaunchKernelGGL((k_linear<F16, NT, XR>), grid, dim3(waves * 64), lds, stream, a);
   return hipGetLastError();
 }
 
-// Room for 2, 4, 8, 16 or 32 tokens: registers, and with them the wavefronts on a CU, depend on
+// Room for 2, 4, 8 or 16 tokens: registers, and with them the wavefronts on a CU, depend on
 // it (eight tokens with room for 8 against 16: 65536 x 6144 59 us against 71, 6144 x
-// 6144 11.9 against 13.3, 1001 x 784 4.0 against 4.4).
+// 6144 11.9 against 13.3, 1001 x 784 4.0 against 4.4).  More tokens take several workgroups
+// an item, whose codes then come from the caches: with room for 32, 32 tokens took 35.4 us against
+// 19.9 on 8192 x 6144 and 132 against 123 on 65536 x 6144; 20 on 6144 x 6144 19.5 against 20.2.
 template <bool F16, int NT>
 hipError_t launch_rows(const LinearArgs& a, int items, int waves, hipStream_t stream) {
-  if (a.m <= 2) return launch<F16, NT, 1, 1>(a, items, waves, stream);
-  if (a.m <= 4) return launch<F16, NT, 1, 2>(a, items, waves, stream);
-  if (a.m <= 8) return launch<F16, NT, 1, 4>(a, items, waves, stream);
-  if (a.m <= 16) return launch<F16, NT, 1, 8>(a, items, waves, stream);
-  return launch<F16, NT, 2, 16>(a, items, waves < 4 ? waves : 4, stream);
+  if (a.m <= 2) return launch<F16, NT, 1>(a, items, waves, stream);
+  if (a.m <= 4) return launch<F16, NT, 2>(a, items, waves, stream);
+  if (a.m <= 8) return launch<F16, NT, 4>(a, items, waves, stream);
+  return launch<F16, NT, 8>(a, items, waves, stream);
 }
 
 // Two tiles an item (half the activation reads and half the wavefronts) once that

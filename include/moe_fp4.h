@@ -372,8 +372,7 @@ int moe_fp4_combine(const uint16_t* rows, int64_t ld_rows, int64_t m_total,
  *   swiglu = 0:  out[t][j] = y[t][j] + (residual ? residual[t][j] : 0),  j < n
  *   swiglu = 1:  out[t][i] = silu(y[t][i]) * y[t][n/2 + i],              i < n/2
  * rounded once, to out_dtype, nearest even.  Deterministic.  The weights are read
- * once for every 16 tokens (32 from 17 tokens on), so the call is meant for a few dozen
- * tokens.
+ * once for every 16 tokens, so the call is meant for a few dozen tokens.
  *   x         device, [m][ld_x] of x_dtype (MOE_FP4_IN_BF16 or _FP16), 16-byte
  *             aligned, ld_x >= k and a multiple of 8.
  *   m         0 .. 16 * 65535 (0 is a no-op).
