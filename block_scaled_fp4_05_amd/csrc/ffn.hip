@@ -9,26 +9,28 @@
 // read.  Each kernel is bound by its weight stream (2/3 and 1/3 of the layer's
 // bytes); with one token, by the chain launch - ids - weights - sum, twice.
 //
-// Measured, kernel times: 64 experts of 4096 x 1024, 32 FP16 tokens, top-6: up 62 us (4.7 TB/s;
-// a large copy reaches 5.05), down 48 us (3.0 TB/s: half of its wavefronts' time waits for
-// loads, and every column tile reads all rows of h again).  256 experts of 6144 x 256, top-8: eight
-// tokens 22.4 and 16.7 us, one token 9.4 and 6.0 us.
+// Measured, kernel times: 64 experts of 4096 x 1024, 32 FP16 tokens, top-6: up 59 us (4.9 TB/s;
+// a large copy reaches 5.05), down 63 us (2.3 TB/s: half of its wavefronts' time waits for
+// loads and LDS, and every column tile reads all rows of h and takes them apart again).
+// 256 experts of 6144 x 256, top-8: eight tokens 22.4 and 18 us, one token 9.4 and 6.0 us.
 //
 // Experts in use are found on the device: every workgroup marks the ids in an LDS
 // bitmap and takes the r-th marked expert (ascending), so the grid needs only
 // min(experts, pairs) ranks and no host knowledge of the routing.  k_ffn_up leaves one record
 // per rank (expert, its first row of h, its tokens as a 64-bit mask) for k_ffn_down.
 //
-// h is kept as the sum of two BF16 values (the first holds h rounded, the second
-// the rest rounded: 2^-17 relative), already times c.  BF16 has FP32's range, so no
-// activation overflows on the way whatever the layer's type, and the matrix cores
-// take both parts as they are.
+// h is kept in FP32, already times c.  k_ffn_down takes each value apart into three BF16 values
+// of 8 significant bits each, whose sum is the value exactly (24 bits; BF16 has FP32's range), and
+// multiplies all three on the matrix cores: nothing of h is rounded away.  (Two parts, rounded to
+// 2^-17, were 1 to 2 us faster for eight tokens and 14 for the 32 below; an FP32 output showed it.)
 //
 // The sum over a token's experts: every wavefront of k_ffn_down adds its experts'
 // results, in ascending order, into a token array of its own in LDS, and the
 // wavefronts' arrays are added in wavefront order: no atomics, and the same inputs give the same bits.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "launch.h"
 #include "few_token_device.h"
@@ -181,19 +183,10 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_up(FfnArgs a) {
       const float4_t gate = take_sum(work, Loop::kLdsBytes, tile, lane, waves);
       const float4_t up = take_sum(work, Loop::kLdsBytes, tile, lane + 32, waves);
       const float cf = coef[j];
-      uint16_t hi[4], lo[4];
+      float4_t v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = silu(gate[i] * scale) * (up[i] * scale) * cf;
-        hi[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
-        // A value that is not finite has no rest.
-        const float rest = v - bf16_value(hi[i]);
-        lo[i] = __builtin_bit_cast(uint16_t, (__bf16)(rest - rest == 0.0f ? rest : 0.0f));
-      }
-      // Row layout: per 8 columns, 16 bytes of first parts, then 16 of rests.
-      char* p = a.h + ((int64_t)(row0 + j) * inter + (col & ~7)) * 4 + (col & 4) * 2;
-      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-      *reinterpret_cast<u32x2_t*>(p + 16) = u32x2_t{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+      for (int i = 0; i < 4; ++i) v[i] = silu(gate[i] * scale) * (up[i] * scale) * cf;
+      *reinterpret_cast<float4_t*>(a.h + ((int64_t)(row0 + j) * inter + col) * 4) = v;
     }
   }
 }
@@ -209,18 +202,49 @@ struct DownStage {
 };
 
 constexpr int kDepth = 2;     // units in flight
-constexpr int kRowGroup = 8;  // rows of h multiplied at once: first parts in columns 0-7, rests in 8-15
+constexpr int kParts = 3;     // BF16 values that hold an FP32 one
+constexpr int kRowGroup = 5;  // rows of h in one product: part p of row j in column 3 j + p
+constexpr int kRowBytes = kParts * 512;  // a row's parts of a unit, in LDS
+
+// Groups of rows that a dequantised weight is multiplied with at once: two where experts
+// have several tokens (PF), which take more LDS.
+__host__ __device__ constexpr int row_groups(int pf) { return pf > kRowGroup ? 2 : 1; }
+
+// Four FP32 values as three BF16 parts each, by taking off the upper half twice: the three
+// hold the leading, next and last 8 bits exactly.
+__device__ __forceinline__ void split_h(u32x4_t v, u32x2_t (&parts)[kParts]) {
+  float rest[4], last[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = v[i];
+    rest[i] = __builtin_bit_cast(float, b) - __builtin_bit_cast(float, b & 0xFFFF0000u);
+    const uint32_t m = __builtin_bit_cast(uint32_t, rest[i]) & 0xFFFF0000u;
+    last[i] = rest[i] - __builtin_bit_cast(float, m);
+  }
+  const float sum = (last[0] + last[1]) + (last[2] + last[3]);
+  if (__ballot(sum != sum)) {  // uniform: some value is not finite, and has no rest
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (last[i] != last[i]) rest[i] = last[i] = 0.0f;
+  }
+  auto upper = [](uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); };
+  auto bits = [](float f) { return __builtin_bit_cast(uint32_t, f); };
+  parts[0] = u32x2_t{upper(v[0], v[1]), upper(v[2], v[3])};
+  parts[1] = u32x2_t{upper(bits(rest[0]), bits(rest[1])), upper(bits(rest[2]), bits(rest[3]))};
+  parts[2] = u32x2_t{upper(bits(last[0]), bits(last[1])), upper(bits(last[2]), bits(last[3]))};
+}
 
 template <bool F16, int NT, int PF>
-__global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
+__global__ __launch_bounds__(kMaxThreads, PF > 4 ? 2 : 4) void k_ffn_down(FfnArgs a) {
   extern __shared__ __align__(16) char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int waves = blockDim.x >> 6;
   const int r = lane & 15, g = lane >> 4;
   constexpr int kCols = 16 * NT;
-  const int hrows = a.tokens < kRowGroup ? a.tokens : kRowGroup;
-  char* hs = smem + wave * hrows * 1024;
-  float* sums = reinterpret_cast<float*>(smem + waves * hrows * 1024);  // [wave][token][kCols]
+  constexpr int GR = row_groups(PF), kRows = GR * kRowGroup;  // rows multiplied at once
+  const int hrows = a.tokens < kRows ? a.tokens : kRows;
+  char* hs = smem + wave * hrows * kRowBytes;
+  float* sums = reinterpret_cast<float*>(smem + waves * hrows * kRowBytes);  // [wave][token][kCols]
   int32_t* list = reinterpret_cast<int32_t*>(sums + (size_t)waves * a.tokens * kCols) + wave * 64;
   float* mysum = sums + (size_t)wave * a.tokens * kCols;
   const int32_t k = a.inter;
@@ -244,12 +268,20 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
   auto tokens_of = [](const RankRecord& rec) { return (uint64_t)rec.tokens_hi << 32 | rec.tokens_lo; };
   // Byte offset of this lane's 16 bytes of row j of an expert's h.
   auto h_offset = [&](const RankRecord& rec, int32_t rows, int32_t step, int32_t j) {
-    return j < rows && step * kFewStep + 4 * (lane & ~1) < k
+    return j < rows && step * kFewStep + 4 * lane < k
                ? ((uint32_t)(rec.row0 + j) * (uint32_t)k + (uint32_t)(step * kFewStep)) * 4u + 16u * lane
                : kOutOfRange;
   };
+  // 16-byte piece i (0..31, eight values) of column c is kept at piece i ^ c: sixteen columns' equal
+  // pieces lie in different banks.
   auto put_h = [&](int j, u32x4_t v) {
-    *reinterpret_cast<u32x4_t*>(hs + j * 1024 + ((lane ^ (j << 1)) << 4)) = v;
+    u32x2_t parts[kParts];
+    split_h(v, parts);
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const int c = kParts * j + p;
+      *reinterpret_cast<u32x2_t*>(hs + c * 512 + (((lane >> 1) ^ c) << 4) + 8 * (lane & 1)) = parts[p];
+    }
   };
   // Where loading and computing stand: units in order are (rank, step).
   struct Cursor {
@@ -276,32 +308,77 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
       if (j < 2 || j < rows) d.h[j] = __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(d.rec, rows, c.step, j), 0, 0);
   };
 
-  // The expert being summed: its first rows' sums stay in registers until the expert ends.
-  float4_t acc[NT][2];
-  auto clear = [&](float4_t (&s)[NT][2]) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // The sums of a lane for the groups of rows.
+  struct Sums {
+    float4_t v[GR][NT][2];
   };
-  float* dest = nullptr;  // this lane's row's sums, null for none
-  // Add what eight rows have summed to their tokens' sums; column c + 8 holds the rests of column c.
-  auto flush = [&](const float4_t (&s)[NT][2], float* to) {
+  auto clear = [&](Sums& s) {
+#pragma unroll
+    for (int q = 0; q < GR; ++q)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s.v[q][t][0] = s.v[q][t][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  // The row of a group whose sum this lane carries, none for the columns of second and third parts.
+  const int32_t my_row = r % kParts == 0 && r < kParts * kRowGroup ? r / kParts : INT32_MAX / 2;
+  // Where the sums of that row of group q of rows first .. are in mysum, negative for none.
+  auto place = [&](int32_t first, int q, int32_t rows) {
+    const int32_t j = first + q * kRowGroup + my_row;
+    return j < rows ? list[j] * kCols + 4 * g : -1;
+  };
+  // Add what a group of rows has summed to its tokens' sums, a row's three columns first.
+  auto flush = [&](const float4_t (&s)[NT][2], int32_t to) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float4_t v = s[t][0] + s[t][1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] += __builtin_bit_cast(
-            float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, (float)v[i]), 0x108, 0xf, 0xf, true));
-      if (to) *reinterpret_cast<float4_t*>(to + 16 * t) += v;
+      for (int i = 0; i < 4; ++i) {
+        const int b = __builtin_bit_cast(int, (float)v[i]);  // the columns one and two to the right
+        const float second = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x101, 0xf, 0xf, true));
+        const float third = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x102, 0xf, 0xf, true));
+        v[i] += second + third;
+      }
+      if (to >= 0) *reinterpret_cast<float4_t*>(mysum + to + 16 * t) += v;
     }
   };
-  auto multiply = [&](const DownStage<NT, PF>& d, int32_t here, float4_t (&s)[NT][2]) {
-    const int32_t row = (r & 7) < here ? (r & 7) : here - 1;
-    const uint32_t at = (uint32_t)(row * 1024 + (((16 * g + (r >> 3)) ^ (row << 1)) << 4));
+  // Multiply the first G groups of the `here` rows in LDS.
+  auto multiply = [&](DownStage<NT, PF> d, int32_t here, Sums& s, auto groups) {
+    // Each product dequantises for itself: carried from one to the next, the weights' values
+    // would take more registers than there are.
+#pragma unroll
+    for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(d.c.q[t][0]), "+v"(d.c.q[t][1]));
+    constexpr int G = decltype(groups)::value;
+    struct Operands {
+      u32x4_t v[G];
+    };
+    uint32_t at[G];
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      const int32_t left = here - q * kRowGroup, last = kParts * (left < kRowGroup ? left : kRowGroup) - 1;
+      const int32_t c = q * kParts * kRowGroup + (r < last ? r : last);
+      at[q] = (uint32_t)(c * 512 + (((8 * g) ^ c) << 4));
+    }
     for_operands<false, NT, 0>(
-        d.c, d.s, [&](int j) { return *reinterpret_cast<const u32x4_t*>(hs + (at ^ (uint32_t)(j << 5))); },
-        [&](int j, int t, u32x4_t w, u32x4_t h) { s[t][j & 1] = mfma16<false>(w, h, s[t][j & 1]); });
+        d.c, d.s,
+        [&](int j) {
+          Operands x;
+#pragma unroll
+          for (int q = 0; q < G; ++q) x.v[q] = *reinterpret_cast<const u32x4_t*>(hs + (at[q] ^ (uint32_t)(j << 4)));
+          return x;
+        },
+        [&](int j, int t, u32x4_t w, const Operands& x) {
+#pragma unroll
+          for (int q = 0; q < G; ++q) s.v[q][t][j & 1] = mfma16<false>(w, x.v[q], s.v[q][t][j & 1]);
+        });
   };
+  auto multiply_rows = [&](const DownStage<NT, PF>& d, int32_t here, Sums& s) {
+    if (GR == 1 || here <= kRowGroup)
+      multiply(d, here, s, std::integral_constant<int, 1>());
+    else
+      multiply(d, here, s, std::integral_constant<int, GR>());
+  };
+  // The expert being summed: its first rows' sums stay in registers until the expert ends.
+  Sums acc;
+  int32_t dest[GR];
   clear(acc);
   auto compute = [&](DownStage<NT, PF>& d, const Cursor& c, bool begins, bool ends) {
     const uint64_t tokens = tokens_of(d.rec);
@@ -314,25 +391,30 @@ __global__ __launch_bounds__(kMaxThreads) void k_ffn_down(FfnArgs a) {
     }
     if (begins) {
       if (tokens >> lane & 1) list[__popcll(tokens & ((1ull << lane) - 1))] = lane;
-      dest = r < kRowGroup && r < rows ? mysum + list[r] * kCols + 4 * g : nullptr;
+#pragma unroll
+      for (int q = 0; q < GR; ++q) dest[q] = place(0, q, rows);
     }
 #pragma unroll
     for (int j = 0; j < PF; ++j)
       if (j < rows) put_h(j, d.h[j]);
-    for (int32_t j = PF; j < rows && j < kRowGroup; ++j)
+    for (int32_t j = PF; j < rows && j < kRows; ++j)
       put_h(j, __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(d.rec, rows, c.step, j), 0, 0));
-    multiply(d, rows < kRowGroup ? rows : kRowGroup, acc);
-    for (int32_t first = kRowGroup; first < rows; first += kRowGroup) {  // an expert of many tokens
-      const int32_t here = rows - first < kRowGroup ? rows - first : kRowGroup;
+    multiply_rows(d, rows < kRows ? rows : kRows, acc);
+    for (int32_t first = kRows; first < rows; first += kRows) {  // an expert of many tokens
+      const int32_t here = rows - first < kRows ? rows - first : kRows;
       for (int32_t j = 0; j < here; ++j)
         put_h(j, __builtin_amdgcn_raw_buffer_load_b128(h_rs, h_offset(d.rec, rows, c.step, first + j), 0, 0));
-      float4_t more[NT][2];
+      Sums more;
       clear(more);
-      multiply(d, here, more);
-      flush(more, r < here ? mysum + list[first + r] * kCols + 4 * g : nullptr);
+      multiply_rows(d, here, more);
+#pragma unroll
+      for (int q = 0; q < GR; ++q)
+        if (q * kRowGroup < here) flush(more.v[q], place(first, q, rows));
     }
     if (ends) {
-      flush(acc, dest);
+#pragma unroll
+      for (int q = 0; q < GR; ++q)
+        if (q * kRowGroup < rows) flush(acc.v[q], dest[q]);
       clear(acc);
     }
   };
@@ -378,8 +460,9 @@ hipError_t launch_up(const FfnArgs& a, int waves, hipStream_t stream) {
 
 template <bool F16, int NT, int PF>
 hipError_t launch_down(const FfnArgs& a, hipStream_t stream) {
-  const int hrows = a.tokens < kRowGroup ? a.tokens : kRowGroup;
-  const size_t lds = (size_t)kDownWaves * (hrows * 1024 + (a.tokens * 16 * NT + 64) * 4);
+  constexpr int kRows = row_groups(PF) * kRowGroup;
+  const int hrows = a.tokens < kRows ? a.tokens : kRows;
+  const size_t lds = (size_t)kDownWaves * (hrows * kRowBytes + (a.tokens * 16 * NT + 64) * 4);
   const dim3 grid((a.hidden + 16 * NT - 1) / (16 * NT));
   hipLaunchKernelGGL((k_ffn_down<F16, NT, PF>), grid, dim3(kDownWaves * 64), lds, stream, a);
   return hipGetLastError();
@@ -392,10 +475,11 @@ hipError_t launch_down(const FfnArgs& a, hipStream_t stream) {
 // Room for 2, 4, 8 or 16 tokens of an expert at once, by how many it has on average; the
 // wavefronts that fit on a CU depend on it (the first layer above: 106 us with 8, 110
 // with 16, 114 with 4; eight tokens of 256 experts 45.2, 46.6 and 44.3).
-// k_ffn_down: eight wavefronts (four: 145 us for the first layer, 48 for eight tokens of
-// 256 experts; twelve: 112 and 47) and one tile (two: 142 and 46).  All eight rows of h that a
-// product takes are kept in flight where experts have two tokens or more on average (109
-// against 118 us), else four (eight: 48 us against 45 for the eight tokens).
+// k_ffn_down: eight wavefronts (121 us for the first layer, 43 for eight tokens of 256 experts,
+// 15.0 for one; four: 153, 44 and 15.3; sixteen: 118, 47 and 18.5) and one tile (two were slower by
+// a third).  Eight of the ten rows of h that are multiplied at once are kept in flight where experts
+// have two tokens or more on average (121 against 135 us), else four of five (eight of ten: 50 us
+// against 43 for the eight tokens, with one workgroup a CU instead of two).
 template <bool F16>
 hipError_t launch_typed(const FfnArgs& a, hipStream_t stream) {
   const int64_t pairs = (int64_t)a.tokens * a.topk;

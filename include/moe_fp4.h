@@ -402,8 +402,8 @@ int moe_fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ld_x, const ui
  *     out[t]  = (residual[t] +) sum_s weights[t][s] * w2_scale[e] * W2[e] (silu(g) * u),
  *               e = ids[t][s], over the slots with 0 <= e < num_experts
  *
- * Sums in FP32; the intermediate silu(g) * u, times its weight, is carried in two BF16
- * parts (2^-17 relative); one rounding, to out_dtype, at the end.  A token may name an
+ * Sums in FP32; the intermediate silu(g) * u, times its weight, is FP32 and multiplied as
+ * such; one rounding, to out_dtype, at the end.  A token may name an
  * expert more than once (the weights add).  A token without a valid slot leaves its
  * residual, or 0.  Experts are summed in ascending order: deterministic.  Weights
  * of experts that no token names are not read, and whatever they hold touches no

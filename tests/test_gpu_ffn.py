@@ -137,6 +137,44 @@ def test_ffn_intermediate_beyond_fp16():
     ref.check(_run(L), y, d)
 
 
+@pytest.mark.parametrize("T", [1, 4, 9])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_ffn_intermediate_keeps_fp32(T, dtype):
+    """One-hot activations make gate and up exact, a unit down projection sums one value a
+    column: what is left of the error is the epilogue's few FP32 operations (swiglu's, and
+    topk + 3 for the weight), with no rounding of the intermediate to fewer bits."""
+    E, K, H, I = 3, 1, 256, 256
+    L = _layer(T, E, K, H, I, dtype, ids=[[t % E] for t in range(T)])
+    L["x"] = torch.eye(T, H, dtype=ref.DT[dtype])
+    L["w2_q"] = np.zeros((E, H, I // 2), np.uint8)
+    for j in range(H):
+        L["w2_q"][:, j, j // 2] = 0x20 if j % 2 else 0x02  # code of 1
+    L["w2_sf"] = np.full((E, H, I // 16), 0x38, np.uint8)  # block scale 1
+    got = _run(L, residual=False, out_dtype=torch.float32).cpu().double()
+    for t in range(T):
+        e = t % E
+        y = ref.values(L["w13_q"][e], L["w13_sf"][e])[:, t] * L["w13_scale"][e].double()
+        v, dv = ref.swiglu(y[:I], y[:I].abs() * ref.U, y[I:], y[I:].abs() * ref.U)
+        c = L["weights"][t, 0].double() * L["w2_scale"][e].double()
+        want, bound = v * c, dv * c + (v * c).abs() * (K + 3) * ref.U
+        assert ((got[t] - want).abs() <= bound).all(), float(((got[t] - want).abs() / bound.clamp(min=1e-300)).max())
+
+
+def test_ffn_infinite_intermediate_has_its_sign():
+    """An infinity in the intermediate is an infinity in the output, not a NaN: all weights
+    positive, one activation infinite."""
+    L = _layer(6, 2, 1, 64, 64, "bf16", ids=[[0], [1], [0], [0], [0], [0]])
+    for q, f in (("w13_q", "w13_sf"), ("w2_q", "w2_sf")):
+        L[q] = (L[q] & 0x66) | 0x11  # codes 0.5, 1.5, 3 and 6
+        L[f] = (L[f] & 0x7F) | 0x20
+    L["x"][3, 7] = float("inf")
+    out = _run(L).cpu()
+    assert (out[3] == float("inf")).all()
+    rows = [0, 1, 2, 4, 5]
+    y, d = _want(L)
+    ref.check(out[rows], y[rows], d[rows])
+
+
 def test_ffn_pitches_and_workspace():
     from block_scaled_fp4_05_amd import moe_fp4
     T, E, K, H, I = 5, 6, 3, 80, 64
