@@ -3,9 +3,16 @@
 Argument marshalling only: every step of the computation runs in the HIP
 kernels.  PyTorch supplies device memory and the current stream.  If the
 compiled library is missing the calls raise; there is no CPU fallback.
+
+Streams: a call runs on `stream` (default: the current stream), and the results and
+workspaces that it allocates itself belong to that stream.  As with any torch tensor, the
+caller makes the launch stream wait for inputs that other streams write, makes another stream
+wait for it before using the results there, and calls record_stream on a result that is dropped
+while another stream still uses it.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -162,6 +169,16 @@ def _stream(stream, dev):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call makes its new tensors (results and workspaces): on its launch stream.
+    From the current stream's pool they could be memory that work still queued there uses,
+    which the launch stream does not wait for."""
+    return _AS_IT_IS if stream is None else torch.cuda.stream(stream)
+
+
 class _AtLeast(int):
     """A shape entry that admits any extent of at least this value."""
 
@@ -233,11 +250,13 @@ def gemm_packed_raw(*args):
 
 def pack_weights(w_q: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Row-major weight codes [E][n][k/2] (uint8, CUDA) -> the packed layout the
-    packed GEMM reads (same shape and size; a byte permutation)."""
+    packed GEMM reads (same shape and size; a byte permutation).  A new `out` belongs to the
+    launch stream."""
     _need(w_q, "w_q", torch.uint8, (None, None, None))
     E, n, kb = w_q.shape
     if out is None:
-        out = torch.empty_like(w_q)
+        with _on(stream):
+            out = torch.empty_like(w_q)
     _need(out, "out", torch.uint8, (E, n, kb))
     dev = _same_cuda("w_q out", w_q, out)
     st = lib().moe_fp4_pack_weights(_ptr(w_q), _ptr(out), E, n, 2 * kb, _stream(stream, dev))
@@ -247,11 +266,12 @@ def pack_weights(w_q: torch.Tensor, out: torch.Tensor | None = None, stream=None
 
 
 def unpack_weights(w_packed: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Inverse of pack_weights."""
+    """Inverse of pack_weights.  A new `out` belongs to the launch stream."""
     _need(w_packed, "w_packed", torch.uint8, (None, None, None))
     E, n, kb = w_packed.shape
     if out is None:
-        out = torch.empty_like(w_packed)
+        with _on(stream):
+            out = torch.empty_like(w_packed)
     _need(out, "out", torch.uint8, (E, n, kb))
     dev = _same_cuda("w_packed out", w_packed, out)
     st = lib().moe_fp4_unpack_weights(_ptr(w_packed), _ptr(out), E, n, 2 * kb, _stream(stream, dev))
@@ -267,7 +287,8 @@ def quantize(x: torch.Tensor, tensor_scale: torch.Tensor | None = None, q=None, 
     tensor_scale None -> dynamic: a new 1-element float32 tensor receives g.
     Otherwise a 1-element float32 CUDA tensor: by default it holds a calibrated g
     (static); with dynamic=True it receives the computed g instead.
-    Returns (q uint8[rows][k/2], sf uint8[rows][k/16], tensor_scale float32[1]).
+    Returns (q uint8[rows][k/2], sf uint8[rows][k/16], tensor_scale float32[1]); new ones
+    belong to the launch stream.
     """
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit column stride")
@@ -279,17 +300,18 @@ def quantize(x: torch.Tensor, tensor_scale: torch.Tensor | None = None, q=None, 
         raise ValueError("x must be bfloat16 or float32")
     rows, k = x.shape
     dev = x.device
-    if q is None:
-        q = torch.empty((rows, k // 2), dtype=torch.uint8, device=dev)
-    if sf is None:
-        sf = torch.empty((rows, k // 16), dtype=torch.uint8, device=dev)
     if dynamic is None:
         dynamic = tensor_scale is None
     mode = SCALE_DYNAMIC if dynamic else SCALE_STATIC
-    if tensor_scale is None:
-        if not dynamic:
-            raise ValueError("a static quantisation needs tensor_scale")
-        tensor_scale = torch.empty(1, dtype=torch.float32, device=dev)
+    if tensor_scale is None and not dynamic:
+        raise ValueError("a static quantisation needs tensor_scale")
+    with _on(stream):
+        if q is None:
+            q = torch.empty((rows, k // 2), dtype=torch.uint8, device=dev)
+        if sf is None:
+            sf = torch.empty((rows, k // 16), dtype=torch.uint8, device=dev)
+        if tensor_scale is None:
+            tensor_scale = torch.empty(1, dtype=torch.float32, device=dev)
     _need(q, "q", torch.uint8, (_AtLeast(rows), k // 2))
     _need(sf, "sf", torch.uint8, (_AtLeast(rows), k // 16))
     _need(tensor_scale, "tensor_scale", torch.float32, (_AtLeast(1),))
@@ -326,11 +348,12 @@ def grouped_gemm(a_q, a_sf, a_scale, w_q, w_sf, w_scale, offsets, a_row_index=No
     w_q [E][n][k/2], w_sf [E][n][k/16], w_scale [E], offsets int32 [E+1],
     a_row_index int32 [m_total] or None.  m_total defaults to a_row_index's length,
     else a_rows.  packed: w_q is in the packed layout (pack_weights).  Returns out,
-    a BF16 tensor [m_total][n] (or the given `out`)."""
+    a BF16 tensor [m_total][n] that belongs to the launch stream (or the given `out`)."""
     E, n, k, a_rows, m_total = _gemm_operands(a_q, a_sf, a_scale, w_q, w_sf, w_scale, offsets,
                                               a_row_index, m_total)
     if out is None:
-        out = torch.empty((m_total, n), dtype=torch.bfloat16, device=w_q.device)
+        with _on(stream):
+            out = torch.empty((m_total, n), dtype=torch.bfloat16, device=w_q.device)
     _need(out, "out", torch.bfloat16, (_AtLeast(m_total), _AtLeast(n)), rows=True)
     dev = _same_cuda("a_q a_sf a_scale w_q w_sf w_scale offsets a_row_index out", a_q, a_sf, a_scale, w_q, w_sf, w_scale, offsets, a_row_index, out)
     fn = lib().moe_grouped_gemm_fp4_packed if packed else lib().moe_grouped_gemm_fp4
@@ -379,14 +402,15 @@ def grouped_gemm_swiglu(a_q, a_sf, a_scale, w_q, w_sf, w_scale, offsets, h_scale
     0..I-1 the gate, I..2I-1 the up projection; h_scale float32 CUDA tensor [1], the
     intermediate's static tensor scale.  Other arguments as grouped_gemm.  Returns
     (h_q uint8 [m_total][I/2], h_sf uint8 [m_total][I/16]), the down projection's
-    activations (or the given buffers)."""
+    activations; new ones belong to the launch stream."""
     E, n, k, a_rows, m_total = _gemm_operands(a_q, a_sf, a_scale, w_q, w_sf, w_scale, offsets,
                                               a_row_index, m_total)
     dev = w_q.device
-    if h_q is None:
-        h_q = torch.empty((m_total, n // 4), dtype=torch.uint8, device=dev)
-    if h_sf is None:
-        h_sf = torch.empty((m_total, n // 32), dtype=torch.uint8, device=dev)
+    with _on(stream):
+        if h_q is None:
+            h_q = torch.empty((m_total, n // 4), dtype=torch.uint8, device=dev)
+        if h_sf is None:
+            h_sf = torch.empty((m_total, n // 32), dtype=torch.uint8, device=dev)
     _need(h_scale, "h_scale", torch.float32, (_AtLeast(1),))
     _need(h_q, "h_q", torch.uint8, (_AtLeast(m_total), n // 4))
     _need(h_sf, "h_sf", torch.uint8, (_AtLeast(m_total), n // 32))
@@ -410,7 +434,8 @@ def combine(rows, token_rows, token_weights, out=None, residual=None, out_dtype=
     """Token-order combine: out[t] = (residual[t] +) sum_s token_weights[t][s] * rows[token_rows[t][s]]
     in FP32, slots in order.  rows: BF16 CUDA tensor [m_total][>= n] (the grouped GEMM's
     output); token_rows int32 / token_weights float32 [num_tokens][topk].  Returns out
-    ([num_tokens][n] of out_dtype, bfloat16 or float32)."""
+    ([num_tokens][n] of out_dtype, bfloat16 or float32); a new one belongs to the launch
+    stream."""
     _need(rows, "rows", torch.bfloat16, (None, None), rows=True)
     m_total, n = rows.shape
     _need(token_rows, "token_rows", torch.int32, (None, None))
@@ -419,7 +444,8 @@ def combine(rows, token_rows, token_weights, out=None, residual=None, out_dtype=
     if residual is not None:
         _need(residual, "residual", torch.float32, (T, _AtLeast(n)), rows=True)
     if out is None:
-        out = torch.empty((T, n), dtype=out_dtype, device=rows.device)
+        with _on(stream):
+            out = torch.empty((T, n), dtype=out_dtype, device=rows.device)
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out: dtype {out.dtype}, expected bfloat16 or float32")
     _need(out, "out", out.dtype, (T, _AtLeast(n)), rows=True)
@@ -479,14 +505,15 @@ def _launch_stream(stream, dev):
     return _raw_stream(dev)
 
 
-def _few_rows(x, residual, out, out_dtype, m, k, cols):
+def _few_rows(x, residual, out, out_dtype, m, k, cols, stream):
     """Check the activations, residual and output of a few-token call; returns
     (x type, x pitch, residual pitch, out, out type, out pitch)."""
     dt = x.dtype
     ld = _pitch(x, "x", dt, (m, k))
     ld_res = 0 if residual is None else _pitch(residual, "residual", dt, (m, cols))
     if out is None:
-        out = x.new_empty((m, cols)) if out_dtype is None else x.new_empty((m, cols), dtype=out_dtype)
+        with _on(stream):
+            out = x.new_empty((m, cols)) if out_dtype is None else x.new_empty((m, cols), dtype=out_dtype)
         if out.dtype not in _OUT_TYPES:
             raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16, float16 or float32")
         return _IN_TYPES[dt], ld, ld_res, out, _OUT_TYPES[out.dtype], cols
@@ -514,7 +541,8 @@ def linear(x, w_q, w_sf, w_scale, swiglu: bool = False, residual=None, out=None,
     """Few-token linear layer: x (bfloat16 or float16 CUDA tensor [m][k], unit column
     stride) times NVFP4 weights w_q uint8 [n][k/2], w_sf uint8 [n][k/16], w_scale
     float32 [1].  Returns out [m][n] = x W^T (+ residual, x's type [m][n]), or with swiglu
-    [m][n/2] = silu(first half) * second half; of out_dtype (default: x's type)."""
+    [m][n/2] = silu(first half) * second half; of out_dtype (default: x's type).  A new out
+    belongs to the launch stream."""
     if (_calls or lib() and _calls) and stream is None and isinstance(x, torch.Tensor) and x.is_cuda:
         dev = _current_device()
         got = _calls.linear(x, w_q, w_sf, w_scale, swiglu, residual, out,
@@ -528,7 +556,7 @@ def linear(x, w_q, w_sf, w_scale, swiglu: bool = False, residual=None, out=None,
         raise ValueError("swiglu: needs an even number of weight rows and no residual")
     _exact(w_sf, "w_sf", torch.uint8, (n, k // 16))
     _exact(w_scale, "w_scale", torch.float32, (1,))
-    dt, ld, ld_res, out, odt, ldo = _few_rows(x, residual, out, out_dtype, m, k, n // 2 if swiglu else n)
+    dt, ld, ld_res, out, odt, ldo = _few_rows(x, residual, out, out_dtype, m, k, n // 2 if swiglu else n, stream)
     dev = _same_cuda("x w_q w_sf w_scale residual out", x, w_q, w_sf, w_scale, residual, out)
     st = (_lib or lib()).moe_fp4_linear(
         x.data_ptr(), dt, m, ld, w_q.data_ptr(), w_sf.data_ptr(), w_scale.data_ptr(), n, k,
@@ -556,7 +584,8 @@ def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, re
     [0, E) is skipped), NVFP4 weights w13 [E][2I][hidden] (gate rows, then up rows) and
     w2 [E][hidden][I] with scales float32 [E].  Returns out [tokens][hidden] = (residual +)
     the routing-weighted sum of the experts, of out_dtype (default: x's type).
-    workspace: uint8 CUDA tensor of ffn_workspace_size bytes (default: a new one)."""
+    workspace: uint8 CUDA tensor of ffn_workspace_size bytes (default: a new one).  A new out
+    or workspace belongs to the launch stream."""
     if (_calls or lib() and _calls) and stream is None and workspace is None and \
             isinstance(x, torch.Tensor) and x.is_cuda:
         dev = _current_device()
@@ -579,12 +608,10 @@ def moe_ffn(x, ids, weights, w13_q, w13_sf, w13_scale, w2_q, w2_sf, w2_scale, re
     _exact(w2_q, "w2_q", u8, (E, H, I // 2))
     _exact(w2_sf, "w2_sf", u8, (E, H, I // 16))
     _exact(w2_scale, "w2_scale", f32, (E,))
-    dt, ld, ld_res, out, odt, ldo = _few_rows(x, residual, out, out_dtype, T, H, H)
+    dt, ld, ld_res, out, odt, ldo = _few_rows(x, residual, out, out_dtype, T, H, H, stream)
     if workspace is None:
-        workspace = w13_q.new_empty(ffn_workspace_size(T, K, E, I))
-        if stream is not None and workspace.is_cuda:
-            # Freed on return: not to be handed out again before this stream is done with it.
-            workspace.record_stream(stream)
+        with _on(stream):
+            workspace = w13_q.new_empty(ffn_workspace_size(T, K, E, I))
     else:
         _need(workspace, "workspace", u8, (_AtLeast(ffn_workspace_size(T, K, E, I)),))
     dev = _same_cuda("x ids weights w13_q w13_sf w13_scale w2_q w2_sf w2_scale residual out workspace",
@@ -631,7 +658,8 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
     grouped by expert.  score "softmax" or "sigmoid" (ranked by score + bias, float32
     [E]); num_groups / topk_groups limit the choice to the best groups of experts.
     Routing.offsets and .row_token are grouped_gemm's offsets and a_row_index,
-    .token_rows and .weights combine's; .ids and .weights moe_ffn's."""
+    .token_rows and .weights combine's; .ids and .weights moe_ffn's.  New results and a new
+    workspace belong to the launch stream."""
     if (_calls or lib() and _calls) and stream is None and workspace is None and out is None and \
             isinstance(logits, torch.Tensor) and logits.is_cuda and score in _SCORES:
         dev = _current_device()
@@ -652,9 +680,10 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
         _exact(bias, "bias", f32, (E,))
     if out is None:
         new = logits.new_empty
-        ids, offsets = new((T, topk), dtype=i32), new(E + 1, dtype=i32)
-        out = Routing(ids, new((T, topk), dtype=f32), offsets, new(T * topk, dtype=i32),
-                      new((T, topk), dtype=i32))
+        with _on(stream):
+            ids, offsets = new((T, topk), dtype=i32), new(E + 1, dtype=i32)
+            out = Routing(ids, new((T, topk), dtype=f32), offsets, new(T * topk, dtype=i32),
+                          new((T, topk), dtype=i32))
     else:
         for t, name, dtype, shape in zip(out, Routing._fields, (i32, f32, i32, i32, i32),
                                          ((T, topk), (T, topk), (E + 1,), (T * topk,), (T, topk))):
@@ -662,10 +691,8 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
     need = route_workspace_size(T, E)
     if workspace is None:
         if need:
-            workspace = logits.new_empty(need, dtype=torch.uint8)
-            if stream is not None and workspace.is_cuda:
-                # Freed on return: not to be handed out again before this stream is done with it.
-                workspace.record_stream(stream)
+            with _on(stream):
+                workspace = logits.new_empty(need, dtype=torch.uint8)
     else:
         _need(workspace, "workspace", torch.uint8, (_AtLeast(need),))
     dev = _same_cuda("logits bias ids weights offsets row_token token_rows workspace", logits, bias,
