@@ -555,13 +555,12 @@ int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const 
                   {w13_scale, num_experts * (int64_t)4},
                   {w2_q, num_experts * w2_b},
                   {w2_sf, num_experts * (w2_b / 8)},
-                  {w2_scale, num_experts * (int64_t)4},
-                  {residual, residual ? ((tokens - 1) * ld_res + hidden) * 2 : 0}};
-  for (const auto& b : in) {
-    if (overlap(workspace, (int64_t)need, b.p, b.bytes)) return MOE_FP4_ERR_ARG;
-    if (b.p != residual && overlap(out, ob, b.p, b.bytes)) return MOE_FP4_ERR_ARG;
-  }
+                  {w2_scale, num_experts * (int64_t)4}};
+  for (const auto& b : in)
+    if (overlap(workspace, (int64_t)need, b.p, b.bytes) || overlap(out, ob, b.p, b.bytes))
+      return MOE_FP4_ERR_ARG;
   if (overlap(workspace, (int64_t)need, out, ob) ||
+      (residual && overlap(workspace, (int64_t)need, residual, ((tokens - 1) * ld_res + hidden) * 2)) ||
       !residual_ok(residual, ld_res, x_dtype, out, out_dtype, ldo, tokens, hidden))
     return MOE_FP4_ERR_ARG;
   moe_fp4::FfnArgs a;

@@ -408,7 +408,9 @@ int moe_fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ld_x, const ui
  * residual, or 0.  Experts are summed in ascending order: deterministic.  Weights
  * of experts that no token names are not read, and whatever they hold touches no
  * output.
- *   x, residual, out, x_dtype, out_dtype as moe_fp4_linear, with rows of `hidden`.
+ *   x, residual, out, x_dtype, out_dtype as moe_fp4_linear, with rows of `hidden` (out may be
+ *              the residual's buffer, but overlap no other operand, also where that is
+ *              the residual's buffer as well).
  *   tokens     0 .. 64 (0 is a no-op); for more, the grouped GEMM chain.
  *   ids        device, [tokens][topk] int32; weights device, [tokens][topk] float.
  *   w13_q      device, [num_experts][2I][hidden/2], rows 0 .. I-1 the gate, I .. 2I-1

@@ -59,6 +59,10 @@ FFN = dict(x=_at(0), x_dtype=0, tokens=3, ld_x=64, ids=_at(1), weights=_at(2), t
     *[(dict(out=FFN[nm]), ARG) for nm in ("x", "ids", "weights", "w13_q", "w2_sf", "workspace")],
     *[(dict(workspace=FFN[nm]), ARG) for nm in ("x", "ids", "w13_q", "w2_q", "w2_scale")],
     (dict(residual=_at(9) + 2, ld_res=64), ARG), (dict(residual=_at(10), ld_res=64), ARG),
+    # The residual may be the output, but not while an input is that buffer too.
+    *[(dict(residual=_at(9), ld_res=64, out=_at(9), **{nm: _at(9)}), ARG)
+      for nm in ("x", "ids", "weights", "w13_q", "w13_sf", "w13_scale", "w2_q", "w2_sf", "w2_scale")],
+    (dict(residual=_at(0), ld_res=64, out=_at(0), workspace=_at(0)), ARG),
     (dict(tokens=0, x=None, ids=None, weights=None, out=None, workspace=None, workspace_bytes=0), OK),
 ])
 def test_ffn_refuses(change, status):
