@@ -9,7 +9,7 @@
 // and lane group g the 64 consecutive ones at 64 g, so that a lane's codes are two
 // 16-byte loads and its four block scales one dword.
 //
-// What reaches a lane through LDS, private to its wavefront (no barriers):
+// What reaches a lane through LDS, private to its wavefront (no barriers; lds_handover):
 //   - activations: loaded in whole 512-byte pieces of a token's row and read back as
 //     operands.  Loading operands straight from memory costs eight instructions a step
 //     whatever the token count, each touching 64 places.
@@ -32,6 +32,15 @@ namespace moe_fp4 {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kFewStep = 256;  // elements of K per wavefront step
+
+// Between a wavefront's writes to its own LDS and other lanes' reads of them, and between
+// those reads and the next writes.  The hardware keeps a wavefront's LDS operations in order;
+// this keeps the compiler from moving them past each other.  No instruction.
+__device__ __forceinline__ void lds_handover() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
 
 // Eight codes (one dword) times one block scale as eight exact 16-bit values: the
 // product has at most 6 significant bits and lies in [2^-10, 2688], inside both
@@ -154,7 +163,8 @@ __device__ __forceinline__ void load_pieces(Codes<NT>& c, rsrc_t q_rs, const uin
   }
 }
 
-// Pieces to Codes, through NT * kPieceBytes of the wavefront's LDS.
+// Pieces to Codes, through NT * kPieceBytes of the wavefront's LDS; hands over whatever else
+// has been written to it.
 template <int NT>
 __device__ __forceinline__ void turn_pieces(Codes<NT>& c, char* lds, int32_t step, int32_t lane, int32_t k) {
   if ((step + 1) * kFewStep > k) {  // uniform: a piece may have been read 8 bytes early
@@ -173,6 +183,10 @@ __device__ __forceinline__ void turn_pieces(Codes<NT>& c, char* lds, int32_t ste
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       *reinterpret_cast<u32x4_t*>(lds + t * kPieceBytes + h * 1024 + 16 * lane) = c.q[t][h];
+  }
+  lds_handover();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       c.q[t][h] = *reinterpret_cast<const u32x4_t*>(from + t * kPieceBytes + 16 * ((2 * (g & 1) + h) ^ (r >> 2)));
@@ -299,6 +313,7 @@ struct FewLoop {
 
   // Step `step`, the i-th of those whose scales are in LDS.
   __device__ __forceinline__ void compute(Stage& r, float4_t (&acc)[NT], int32_t step, int i) const {
+    lds_handover();  // the previous step's operands have been read
 #pragma unroll
     for (int j = 0; j < PF; ++j) put_x(j, r.x[j]);
 #pragma unroll
@@ -308,8 +323,9 @@ struct FewLoop {
     const int32_t g = lane >> 4, col = lane & 15;
     if (TURN)
       turn_pieces<NT>(r.c, lds + kXBytes + kSBytes, step, lane, k);
-    else if ((step + 1) * kFewStep > k)
-      move_codes<NT>(r.c, blocks_left(step * kFewStep + 64 * g, k));
+    else
+      lds_handover();
+    if (!TURN && (step + 1) * kFewStep > k) move_codes<NT>(r.c, blocks_left(step * kFewStep + 64 * g, k));
     uint32_t s[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -332,6 +348,7 @@ struct FewLoop {
       load(a, c0, c1);
       load_scales(sc[1], c0 + 4, c1);
       load(b, c0 + 1, c1);
+      lds_handover();  // the previous scales have been read
       put_scales(sc[0], 0);
       put_scales(sc[1], 1);
       int32_t s = c0;
@@ -350,6 +367,7 @@ struct FewLoop {
 // Leave a wavefront's sums in its own LDS: [tile][lane], four values each.
 template <int NT>
 __device__ __forceinline__ void put_sums(char* lds, const float4_t (&acc)[NT], int lane) {
+  lds_handover();  // the last operands have been read
 #pragma unroll
   for (int t = 0; t < NT; ++t) reinterpret_cast<float4_t*>(lds)[t * 64 + lane] = acc[t];
 }

@@ -250,6 +250,7 @@ __global__ __launch_bounds__(kMaxThreads, PF > 4 ? 2 : 4) void k_ffn_down(FfnArg
   const int32_t k = a.inter;
   const int32_t n0 = blockIdx.x * kCols;
   for (int i = lane; i < a.tokens * kCols; i += 64) mysum[i] = 0.0f;
+  lds_handover();
 
   uint32_t q_off[NT], s_off[NT];
 #pragma unroll
@@ -371,10 +372,12 @@ __global__ __launch_bounds__(kMaxThreads, PF > 4 ? 2 : 4) void k_ffn_down(FfnArg
         });
   };
   auto multiply_rows = [&](const DownStage<NT, PF>& d, int32_t here, Sums& s) {
+    lds_handover();  // the rows have been written
     if (GR == 1 || here <= kRowGroup)
       multiply(d, here, s, std::integral_constant<int, 1>());
     else
       multiply(d, here, s, std::integral_constant<int, GR>());
+    lds_handover();  // and read
   };
   // The expert being summed: its first rows' sums stay in registers until the expert ends.
   Sums acc;
@@ -390,7 +393,9 @@ __global__ __launch_bounds__(kMaxThreads, PF > 4 ? 2 : 4) void k_ffn_down(FfnArg
       for (int t = 0; t < NT; ++t) d.s[t] = left > 0 ? d.s[t] >> (8 * (4 - left)) : 0u;
     }
     if (begins) {
+      lds_handover();  // the previous expert's tokens have been read
       if (tokens >> lane & 1) list[__popcll(tokens & ((1ull << lane) - 1))] = lane;
+      lds_handover();
 #pragma unroll
       for (int q = 0; q < GR; ++q) dest[q] = place(0, q, rows);
     }
