@@ -522,7 +522,7 @@ int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const 
                 void* workspace, size_t workspace_bytes, void* stream) {
   if (!few_dtypes_ok(x_dtype, out_dtype)) return MOE_FP4_ERR_ARG;
   if (!w13_q || !w13_sf || !w13_scale || !w2_q || !w2_sf || !w2_scale) return MOE_FP4_ERR_NULL;
-  if (tokens > 0 && (!x || !ids || !weights || !out || !workspace)) return MOE_FP4_ERR_NULL;
+  if (tokens > 0 && (!x || !ids || !weights || !out)) return MOE_FP4_ERR_NULL;
   if (tokens < 0 || topk < 1 || num_experts < 1 || hidden < 1 || inter < 1) return MOE_FP4_ERR_SHAPE;
   if (tokens > 0 && (ld_x < hidden || ldo < hidden || (residual && ld_res < hidden)))
     return MOE_FP4_ERR_SHAPE;
@@ -541,6 +541,7 @@ int moe_fp4_ffn(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const 
   if (!few_rows_fit(tokens, ld_x, residual ? ld_res : 0, ldo)) return MOE_FP4_ERR_UNSUPPORTED;
   const size_t need = moe_fp4_ffn_workspace_size(tokens, topk, num_experts, inter);
   if (need == 0) return MOE_FP4_ERR_UNSUPPORTED;
+  if (!workspace) return MOE_FP4_ERR_NULL;
   if (workspace_bytes < need) return MOE_FP4_ERR_SHAPE;
   const int64_t ob = ((tokens - 1) * ldo + hidden) * out_size(out_dtype);
   const int64_t pb = tokens * topk * 4, xb = ((tokens - 1) * ld_x + hidden) * 2;

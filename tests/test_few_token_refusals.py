@@ -69,6 +69,15 @@ def test_ffn_refuses(change, status):
     assert m.ffn_raw(*dict(FFN, **change).values()) == status
 
 
+@pytest.mark.parametrize("change", [dict(tokens=65), dict(topk=700), dict(tokens=64, topk=33),
+                                    dict(inter=2 ** 20, topk=600)])
+def test_ffn_names_a_size_it_does_not_run_before_the_workspace_that_has_none(change):
+    """ffn_workspace_size is 0 for these: a caller that allocates it passes NULL."""
+    a = dict(FFN, **change)
+    assert m.ffn_workspace_size(a["tokens"], a["topk"], a["num_experts"], a["inter"]) == 0
+    assert m.ffn_raw(*dict(a, workspace=None, workspace_bytes=0).values()) == UNSUPPORTED
+
+
 def test_ffn_workspace_size():
     # The count, a 16-byte record per expert in use, and 4 bytes for each intermediate value.
     assert m.ffn_workspace_size(3, 2, 4, 80) == 16 + 16 * 4 + 6 * 80 * 4

@@ -115,6 +115,15 @@ def test_refusals_of_the_library_on_the_gpu():
         m.route(torch.zeros(3, 8, device="cuda"), 2, score="sigmoid", bias=torch.zeros(8, device="cuda").half())
 
 
+def test_more_tokens_than_the_layer_takes_are_refused_as_such():
+    m, f = _m(), _ffn()
+    many = dict(f, x=torch.zeros(65, 128, device="cuda").half(), weights=torch.zeros(65, 2, device="cuda"),
+                ids=torch.zeros(65, 2, dtype=I32, device="cuda"))
+    with pytest.raises(m.MoeFp4Error) as e:
+        m.moe_ffn(**many)
+    assert e.value.status == m.ERR_UNSUPPORTED
+
+
 def test_short_path_keeps_no_references():
     m = _m()
     a, f, x = _linear(), _ffn(), torch.randn(100, 16, device="cuda")
