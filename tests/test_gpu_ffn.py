@@ -86,6 +86,34 @@ def test_ffn_routings(ids, residual):
             assert torch.equal(out[t].cpu(), L["residual"][t] if residual else torch.zeros(96).bfloat16())
 
 
+def _skewed(T, E, busy, others):
+    """Every token to expert `busy`, but the first few to `others`."""
+    return [[others[t]] if t < len(others) else [busy] for t in range(T)]
+
+
+@pytest.mark.parametrize("T,E,K,H,I,ids", [
+    # One expert takes all: its weights pass by 16 times (two tiles a wavefront, room for four
+    # tokens, codes turned in LDS), and 13 groups of five rows are summed with four in flight.
+    (64, 256, 1, 64, 512, _skewed(64, 256, 200, [])),
+    # The same beside lighter experts, so that a wavefront's units begin and end inside one.
+    (64, 256, 1, 80, 528, _skewed(64, 256, 200, [3, 255, 3, 7, 9, 255])),
+    (41, 60, 1, 272, 800, _skewed(41, 60, 0, [59, 1, 2])),
+    # Room for 16 tokens with two tiles a wavefront, even and uneven.
+    (64, 8, 2, 64, 512, None),
+    (40, 8, 3, 80, 528, [[1, 1 + t % 7, 0] for t in range(40)]),
+    # More than eight steps a wavefront: two tiles, one tile.
+    (4, 8, 2, 8720, 512, None),
+    (2, 8, 4, 8464, 512, None),
+    (3, 3, 1, 16656, 64, None),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_ffn_uneven_loads_and_long_rows(T, E, K, H, I, ids, dtype):
+    say(f"ffn uneven T{T} E{E} K{K} H{H} I{I} {dtype}")
+    L = _layer(T, E, K, H, I, dtype, ids=ids)
+    ref.check(_run(L), *_want(L))
+    ref.check(_run(L, residual=False, out_dtype=torch.float32), *_want(L, False))
+
+
 def test_ffn_many_experts():
     """8192 experts, ids at both ends of the range."""
     E, H, I = 8192, 64, 64

@@ -97,6 +97,51 @@ def test_route_values_that_are_not_finite(score):
         assert r.weights[0, 3] == 0 and abs(float(r.weights[0, :3].sum()) - 1) < 1e-6
 
 
+# From 4096 tokens on, 16 lanes rank a token where they can hold its experts.
+@pytest.mark.parametrize("T", [4096, 4099])
+@pytest.mark.parametrize("E,topk", [(3, 2), (16, 1), (24, 5), (64, 8), (100, 6), (128, 16), (256, 8), (257, 8)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_route_sixteen_lanes_a_token(T, E, topk, dtype):
+    """Softmax and sigmoid, with many equal logits (a few distinct values) and few."""
+    say(f"route 16 lanes T{T} E{E} K{topk} {dtype}")
+    x = _logits(T, E, dtype)
+    _check(x, topk, renorm=False)
+    _check((x * 2).round(), topk, renorm=T % 2 == 0)
+    _check((x * 2).round(), topk, "sigmoid", None, T % 2 == 1)
+
+
+@pytest.mark.parametrize("T", [4096, 4099])
+@pytest.mark.parametrize("E,topk,groups,topk_groups", [
+    (256, 8, 8, 4), (160, 6, 8, 3), (48, 5, 3, 1), (64, 4, 16, 5), (30, 3, 2, 1), (128, 8, 4, 2), (256, 8, 16, 4)])
+@pytest.mark.parametrize("score,bias,dtype", [("softmax", False, "fp32"), ("softmax", False, "bf16"),
+                                              ("sigmoid", False, "fp32"), ("sigmoid", True, "bf16"),
+                                              ("sigmoid", True, "fp32")])
+def test_route_groups_with_sixteen_lanes_a_token(T, E, topk, groups, topk_groups, score, bias, dtype):
+    say(f"route 16 lanes T{T} E{E} K{topk} G{groups}/{topk_groups} {score} {bias} {dtype}")
+    b = torch.from_numpy(np.random.default_rng(E).standard_normal(E).astype(np.float32) * 0.1) if bias else None
+    x = _logits(T, E, dtype)
+    if dtype == "bf16":
+        x = (x * 2).round()
+    _check(x, topk, score, b, T % 2 == 0, groups, topk_groups)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_values_that_are_not_finite_with_sixteen_lanes_a_token(score, dtype):
+    x = _logits(4098, 20, dtype)
+    x[0::6, 3:] = float("-inf")
+    x[1::6, 4] = float("nan")
+    x[1::6, :4] = float("-inf")
+    x[2::6] = float("-inf")
+    x[3::6, 7] = float("inf")
+    x[4::6] = float("nan")
+    from block_scaled_fp4_05_amd import moe_fp4
+    r = moe_fp4.route(x.cuda(), 4, score=score)
+    assert np.array_equal(r.ids.cpu().numpy(), ref.route(x, 4, score, None, True, 1, 1)[0])
+    assert sorted(r.token_rows.flatten().tolist()) == list(range(4 * 4098))
+    assert torch.isfinite(r.weights[5::6]).all()
+
+
 def test_route_sigmoid_scores_closer_than_fp32():
     """Scores that differ by less than an FP32 step at 1 keep their order."""
     x = torch.full((2, 64), -3.0)
