@@ -158,8 +158,8 @@ __device__ __forceinline__ uint64_t wave_holders(typename K::T v) {
   }
 }
 
-template <int LT>
-__device__ __forceinline__ float token_sum(float v) {
+template <int LT, typename T>
+__device__ __forceinline__ T token_sum(T v) {
 #pragma unroll
   for (int d = 1; d < LT; d <<= 1) v += __shfl_xor(v, d, 64);
   return v;
@@ -326,11 +326,12 @@ __device__ __forceinline__ void rank_token(const RouteArgs& a, int32_t t, bool o
   }
   // The chosen logits are read again (they are in the caches) rather than carried.
   const bool mine = on && own < a.topk;
-  float my_val = mine ? load_logit(a, (int64_t)t * a.ld + my_id) : 0.0f;
-  if (SIGMOID) my_val = (float)(1.0 / (1.0 + exp(-(double)my_val)));
-  float w = my_val;
+  const float my_val = mine ? load_logit(a, (int64_t)t * a.ld + my_id) : 0.0f;
+  float w;
   if (SIGMOID) {
-    if (a.renormalize) w = my_val / token_sum<LT>(mine ? my_val : 0.0f);
+    // In FP64 up to the quotient: scores below 2^-126 lose their proportions in FP32.
+    const double p = 1.0 / (1.0 + exp(-(double)my_val));
+    w = (float)(a.renormalize ? p / token_sum<LT>(mine ? p : 0.0) : p);
   } else if (a.renormalize) {
     // The full softmax's denominator cancels: only the chosen experts' terms are needed.
     const float m = token_max_f<LT>(mine ? my_val : -__builtin_inff());

@@ -151,6 +151,18 @@ def test_route_sigmoid_scores_closer_than_fp32():
     assert r.ids.tolist() == [[50, 10], [10, 50]]
 
 
+@pytest.mark.parametrize("T", [1, 5, 70, 4100])
+def test_route_sigmoid_weights_below_fp32(T):
+    """Scores that FP32 holds in a few bits or not at all (below 2^-126) still have their
+    proportions as weights."""
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy(rng.uniform(-300.0, -85.0, (T, 20)).astype(np.float32))
+    x[0, :] = torch.linspace(-106.0, -99.0, 20)
+    _check(x, 4, "sigmoid")
+    _check(x, 4, "sigmoid", torch.linspace(0, 1, 20), True, 4, 2)
+    _check(x, 4, "sigmoid", None, False)
+
+
 def test_route_bias_may_close_experts():
     b = torch.zeros(32)
     b[5:] = float("-inf")
