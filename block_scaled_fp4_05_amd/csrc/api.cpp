@@ -93,7 +93,9 @@ size_t ffn_records_end(int64_t pairs, int32_t experts) {
 }
 
 // Tokens of a router block: four, or as many more as keep the blocks, whose counts every
-// block reads, at 256 or below (up to the largest block).
+// block reads, at 256 or below (up to the largest block).  256 experts, top-8: 2048 tokens 11.2 us
+// (128 blocks 10.9, 512 blocks 17.9), 8192 13.8 (14.8, 20.3), 16384 16.9 (22.1, 23.8).  Above 131072
+// tokens, where the block no longer grows, the counts read grow with the square of the tokens.
 int64_t route_block(int64_t tokens) {
   int64_t b = 4;
   while (b < moe_fp4::kRouteMaxBlock && b * 256 < tokens) b *= 2;

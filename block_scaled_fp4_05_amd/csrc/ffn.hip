@@ -5,9 +5,11 @@
 //   k_ffn_down  out[t]  = residual[t] + sum_e W2[e] (c[t, e] h[t, e]),
 //               c[t, e] = w2_scale[e] * (sum of t's routing weights for e)
 //
-// Every routed expert's weights are read once; experts no token is routed to are not
-// read.  Each kernel is bound by its weight stream (2/3 and 1/3 of the layer's
-// bytes); with one token, by the chain launch - ids - weights - sum, twice.
+// Experts no token is routed to are not read.  A routed expert's down projection is read once,
+// its gate and up projections once for every 2 XR of its tokens (launch_typed: the room goes by
+// the experts' average, so a much fuller expert takes several passes).
+// k_ffn_up is bound by its weight stream (2/3 of the layer's bytes), k_ffn_down by what follows
+// its loads (below); with one token both by the chain launch - ids - weights - sum.
 //
 // Measured, kernel times: 64 experts of 4096 x 1024, 32 FP16 tokens, top-6: up 59 us (4.9 TB/s;
 // a large copy reaches 5.05), down 63 us (2.3 TB/s: half of its wavefronts' time waits for

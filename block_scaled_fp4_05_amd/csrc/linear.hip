@@ -129,9 +129,11 @@ hipError_t launch_rows(const LinearArgs& a, int items, int waves, hipStream_t st
 // Two tiles an item (half the activation reads and half the wavefronts) once that
 // leaves an item for every CU: 8192 x 6144, 16 tokens 13.6 us against 14.8; 65536 x 6144,
 // 4 tokens 54 against 56 (before the codes were turned in LDS); but 6144 x 6144, one
-// token 9.8 against 9.7.  Four wavefronts an item, eight where there are few items to fill
+// token 9.8 against 9.7.  Four wavefronts an item, eight where there are too few items to fill
 // the CUs (one or two wavefronts on 6144 x 6144: 17.9 and 13.1 us; eight on 65536 x
-// 6144: 63 us).
+// 6144: 63 us).  With more than 256 tiles eight are slower again: one token of 4352 x 6144
+// 8.5 us against 7.9, of 6144 x 6144 9.0 against 8.7, 16 tokens of the latter 15.5 against 12.1;
+// two-tile items of 8192 x 6144 with 16 tokens and SwiGLU 12.4 against 11.5.
 template <bool F16>
 hipError_t launch_typed(const LinearArgs& a, hipStream_t stream) {
   const int steps = (a.k + kFewStep - 1) / kFewStep;

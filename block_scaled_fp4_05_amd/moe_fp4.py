@@ -659,7 +659,9 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
     [E]); num_groups / topk_groups limit the choice to the best groups of experts.
     Routing.offsets and .row_token are grouped_gemm's offsets and a_row_index,
     .token_rows and .weights combine's; .ids and .weights moe_ffn's.  New results and a new
-    workspace belong to the launch stream."""
+    workspace belong to the launch stream; without a stream, workspace or out the five results
+    share one allocation, which lives as long as any of them (clone one that is kept or saved
+    alone)."""
     if (_calls or lib() and _calls) and stream is None and workspace is None and out is None and \
             isinstance(logits, torch.Tensor) and logits.is_cuda and score in _SCORES:
         dev = _current_device()

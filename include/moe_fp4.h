@@ -446,7 +446,8 @@ enum { MOE_FP4_SCORE_SOFTMAX = 0, MOE_FP4_SCORE_SIGMOID = 1 };
  *   SIGMOID   p[e] = 1 / (1 + e^-x[e]); ranked by p[e] + bias[e] (or p[e]), in binary64.
  *   groups    num_groups > 1 splits the experts into equal consecutive groups; only the best
  *             topk_groups groups are eligible.  A group's score is its largest
- *             ranking value (SOFTMAX) or the sum of its two largest (SIGMOID).
+ *             ranking value (SOFTMAX) or the sum of its two largest (SIGMOID; a -inf in the
+ *             sum ranks it below all sums of numbers, two of them or a NaN lower still).
  *   ties      go to the lower index, in both choices.  A NaN ranks below every number.
  *   weights   p of the chosen experts (the bias plays no part); renormalize: divided by
  *             their sum (with SOFTMAX, the softmax over the chosen experts).  A token
