@@ -228,8 +228,9 @@ __device__ __forceinline__ void store_as(void* out, int64_t i, float v, int32_t 
     static_cast<__bf16*>(out)[i] = (__bf16)v;
 }
 
-// x / (1 + e^-x): exactly 0 or the identity where e^-x overflows or vanishes.
-__device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
+// x / (1 + e^-x): exactly 0 or the identity where e^-x overflows or vanishes.  expf, since the
+// fast exponential's relative error grows with |x|; a thread takes four, in the epilogues.
+__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
 
 // The sums of NT x 16 weight rows times up to 16 tokens over a wavefront's steps
 // [s0, s1).  XR = loads of two tokens each that a step takes at most (8), PF of

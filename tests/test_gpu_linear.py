@@ -84,6 +84,23 @@ def test_linear_every_code_and_scale_is_exact(dtype):
     assert torch.equal(got, ref.values(q, sf)[:, :16].t())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_linear_swiglu_far_from_zero(dtype):
+    """One-hot activations and a scale that is a power of two make gate and up exact, up to
+    +-45: the epilogue's exponential (2 u), sum, quotient and product (u each) are then within
+    6 u of silu(g) * u wherever g lies (below -87 FP32 runs out; not reached)."""
+    n, k, m = 512, 64, 16
+    _, q, sf, _, _ = _case(m, n, k, dtype)
+    x = torch.eye(m, k, dtype=ref.DT[dtype])
+    got = _run(x.cuda(), q, sf, 4.0, swiglu=True, out_dtype=torch.float32).cpu().double()
+    y = ref.values(q, sf)[:, :m].t() * 4
+    g, u = y[:, :n // 2], y[:, n // 2:]
+    assert float(g.min()) < -30 and float(g.max()) > 30
+    want = g * torch.sigmoid(g) * u
+    assert ((got - want).abs() <= 6 * ref.U * (1 + 2 ** -6) * want.abs()).all(), \
+        float(((got - want).abs() / want.abs().clamp(min=1e-300)).max() / ref.U)
+
+
 def test_linear_pitches_and_untouched_columns():
     m, n, k = 6, 45, 176
     rng, q, sf, x, scale = _case(m, n, k, "bf16")
