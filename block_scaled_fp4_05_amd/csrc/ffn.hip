@@ -11,10 +11,10 @@
 // k_ffn_up is bound by its weight stream (2/3 of the layer's bytes), k_ffn_down by what follows
 // its loads (below); with one token both by the chain launch - ids - weights - sum.
 //
-// Measured, kernel times: 64 experts of 4096 x 1024, 32 FP16 tokens, top-6: up 59 us (4.9 TB/s;
-// a large copy reaches 5.05), down 63 us (2.3 TB/s: half of its wavefronts' time waits for
+// Measured, kernel times: 64 experts of 4096 x 1024, 32 FP16 tokens, top-6: up 60 us (4.8 TB/s;
+// a large copy reaches 5.05), down 65.5 us (2.2 TB/s: half of its wavefronts' time waits for
 // loads and LDS, and every column tile reads all rows of h and takes them apart again).
-// 256 experts of 6144 x 256, top-8: eight tokens 22.4 and 18 us, one token 9.4 and 6.0 us.
+// 256 experts of 6144 x 256, top-8: eight tokens 22.1 and 18.2 us, one token 9.5 and 6.0 us.
 //
 // Experts in use are found on the device: every workgroup marks the ids in an LDS
 // bitmap and takes the r-th marked expert (ascending), so the grid needs only
@@ -24,7 +24,7 @@
 // h is kept in FP32, already times c.  k_ffn_down takes each value apart into three BF16 values
 // of 8 significant bits each, whose sum is the value exactly (24 bits; BF16 has FP32's range), and
 // multiplies all three on the matrix cores: nothing of h is rounded away.  (Two parts, rounded to
-// 2^-17, were 1 to 2 us faster for eight tokens and 14 for the 32 below; an FP32 output showed it.)
+// 2^-17, were 1.5 us faster for the eight tokens and 15 for the 32; an FP32 output showed it.)
 //
 // The sum over a token's experts: every wavefront of k_ffn_down adds its experts'
 // results, in ascending order, into a token array of its own in LDS, and the

@@ -12,8 +12,8 @@
 // wavefront order (no atomics: the same inputs give the same bits).
 //
 // Measured, kernel time on weights that are in no cache: 65536 x 6144, four BF16 tokens, FP32
-// out: 47.9 us, 4.7 TB/s (a large copy reaches 5.05).  8192 x 6144 with SwiGLU, 16
-// FP16 tokens: 11.8 us, 2.4 TB/s.  6144 x 6144, one token: 8.8 us, 2.4 TB/s: one or two
+// out: 47.4 us, 4.8 TB/s (a large copy reaches 5.05).  8192 x 6144 with SwiGLU, 16
+// FP16 tokens: 12.0 us, 2.4 TB/s.  6144 x 6144, one token: 8.6 us, 2.5 TB/s: one or two
 // workgroups a CU, whose start, first loads and final sum nothing covers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
