@@ -137,7 +137,8 @@ __device__ __forceinline__ void move_codes(Codes<NT>& c, int32_t left) {
 // tokens 59 against 63.  Variants of one tile a wavefront (few rows: latency) or of more
 // tokens (LDS, registers) read directly: 6144 x 6144, one token 8.8 us against 9.3 turned; up
 // projections of 64 experts, 32 tokens 60.5 against 61.6.  So does the layer's down projection,
-// which has a step or a few an expert: 256 experts, eight tokens 16.7 us against 21.4.
+// which has a step or a few an expert: 256 experts, eight tokens 16.7 us against 21.4 (with its
+// activations in two parts).
 constexpr int kPieceBytes = 2048;  // LDS in which one tile's codes are turned
 
 // Which of the four 16-byte pieces of a 64-byte half lane l reads of row l / 4: staggered,

@@ -476,12 +476,12 @@ hipError_t launch_down(const FfnArgs& a, hipStream_t stream) {
 }
 
 // k_ffn_up: two tiles an item and four wavefronts (64 experts, 32 tokens top-6, 4096 x
-// 1024: the layer takes 118 us against 137 with one tile and 231 with one tile and eight
+// 1024: the layer takes 122 us against 134 with one tile and 170 with one tile and eight
 // wavefronts); where that leaves CUs without an item, one tile and eight wavefronts
-// (one token, eight experts of 6144 x 256: 16.3 us against 17.9).
+// (one token, eight experts of 6144 x 256: 15.0 us against 15.2 with four and 17.9 with two tiles).
 // Room for 2, 4, 8 or 16 tokens of an expert at once, by how many it has on average; the
-// wavefronts that fit on a CU depend on it (the first layer above: 106 us with 8, 110
-// with 16, 114 with 4; eight tokens of 256 experts 45.2, 46.6 and 44.3).
+// wavefronts that fit on a CU depend on it (the first layer above: 122 us with 8, 125
+// with 16, 128 with 4; eight tokens of 256 experts 43 with 4, 44 with 8 and 16).
 // k_ffn_down: eight wavefronts (121 us for the first layer, 43 for eight tokens of 256 experts,
 // 15.0 for one; four: 153, 44 and 15.3; sixteen: 118, 47 and 18.5) and one tile (two were slower by
 // a third).  Eight of the ten rows of h that are multiplied at once are kept in flight where experts
