@@ -11,9 +11,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_fp4.so")
 SOURCES = ["api.cpp", "quantize.hip", "grouped_gemm.hip", "grouped_gemm_finalize.hip",
            "grouped_gemm_swiglu.hip", "grouped_gemm_tiled.hip", "grouped_gemm_big.hip", "grouped_gemm_mid.hip", "pack.hip", "combine.hip",
-           "linear.hip", "ffn.hip", "route.hip"]
+           "linear.hip", "ffn.hip", "route.hip",
+           "api_fp8.cpp", "quantize_fp8.hip", "gemm_fp8.hip", "gemm_fp8_tiled.hip", "rows.hip", "route_backward.hip"]
 HEADERS = ["fp4_device.h", "gemm_common.h", "grouped_gemm_kernel.h", "launch.h",
-           "few_token_device.h"]
+           "few_token_device.h", "api_checks.h", "fp8_device.h", "gemm_fp8.h"]
 # A measurement aid kept out of the library: the streaming-read probe that
 # bench.py --ceilings loads (not part of the C ABI in include/moe_fp4.h).
 PROBE_LIB = os.path.join(PKG, "libmoe_fp4_probe.so")

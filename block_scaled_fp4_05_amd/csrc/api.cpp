@@ -11,10 +11,13 @@
 #include <stdlib.h>
 
 #include "../../include/moe_fp4.h"
+#include "api_checks.h"
 #include "launch.h"
 
+using moe_fp4::aligned;
 using moe_fp4::GemmArgs;
 using moe_fp4::GemmTile;
+using moe_fp4::overlap;
 
 namespace {
 
@@ -22,14 +25,6 @@ constexpr int kAbiVersion = 2;
 // The work-list tables (8 bytes per expert) live in LDS beside each kernel's
 // own buffers (at most 68 KB); 8192 experts keep every kernel within 160 KB.
 constexpr int32_t kMaxExperts = 8192;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Whether the byte ranges [p, p + pb) and [q, q + qb) share a byte.
-bool overlap(const void* p, int64_t pb, const void* q, int64_t qb) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return pb > 0 && qb > 0 && a < b + (uintptr_t)qb && b < a + (uintptr_t)pb;
-}
 
 int check_gemm_shape(int32_t num_experts, int64_t m_total, int64_t n, int64_t k) {
   if (num_experts < 1 || m_total < 0 || n < 1 || k < 1) return MOE_FP4_ERR_SHAPE;

@@ -1,0 +1,203 @@
+// What the FP8 block-scaled products (gemm_fp8.hip, gemm_fp8_tiled.hip) share: where a
+// workgroup works, and how a result is stored.
+//
+// Products of two 16-row operands over one block of 128, which the block's two scales then
+// multiply: acc += d * (sa * sw), one multiply-add an element.  Weights are the first operand:
+// lane l of the result then holds activation row l % 16, whose scale is one value a lane, and
+// weight rows 4 (l / 16) .. +3; the weight scale is uniform, since 16 rows at a multiple of
+// 16 lie in one block of 128.  Lane l gives 32 bytes of row l % 16 of each operand; which 32
+// of the 128 does not matter as long as both operands agree: the 16-byte pieces l / 16 and
+// 4 + l / 16.
+//
+// Two ways.  The FP8 matrix cores take the bytes as they are, at twice the rate of the
+// FP16 ones, but not their sums: of eight consecutive products the smaller ones are cut
+// off 13 bits below the leading bit of the largest (measured bit by bit; groups of eight meet in
+// FP32).  On Gaussian data a result is off by 1.5e-5 of itself, far below the rounding to 16
+// bits (2^-9 or 2^-12 of it), so the compute-bound tiles use them for 16-bit results.  An FP32
+// result, and every result of the few-row kernel, whose time is the weight stream, is computed on
+// the FP16 cores from exactly converted operands, good to FP32's own roundings.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "few_token_device.h"
+#include "fp8_device.h"
+#include "gemm_common.h"
+#include "launch.h"
+
+namespace moe_fp4 {
+
+__device__ __forceinline__ float4_t fp8_block_product(const i32x8_t& w, const i32x8_t& a) {
+  const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// A lane's 32 bytes as FP16 values (exact: E4M3 is 2^-9 to 448 with four significant bits).
+struct Half32 {
+  half8_t v[4];
+};
+
+__device__ __forceinline__ Half32 fp8_widen(const i32x8_t& x) {
+  Half32 h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * i], 1.0f, false);
+    const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * i], 1.0f, true);
+    const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * i + 1], 1.0f, false);
+    const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * i + 1], 1.0f, true);
+    h.v[i] = half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  return h;
+}
+
+__device__ __forceinline__ float4_t fp8_block_product(const Half32& w, const Half32& a) {
+  float4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[i], a.v[i], d, 0, 0, 0);
+  return d;
+}
+
+// Where a workgroup works (uniform).
+struct Fp8Item {
+  int32_t e;     // expert; -1: no item
+  int32_t row0;  // first result row
+  int32_t rows;  // valid rows of the tile
+  int32_t n0;    // first result column
+};
+
+// Items of an expert of cnt rows, if this launch takes experts of that size.
+__device__ __forceinline__ int32_t fp8_items(const Fp8GemmArgs& p, int32_t cnt, int32_t bm) {
+  const bool take = cnt > 0 && cnt >= p.rows_lo && (p.rows_hi == 0 || cnt < p.rows_hi);
+  return take ? (cnt + bm - 1) / bm * p.n_tiles : 0;
+}
+
+// Workgroups for at most all items of tiles of bm rows: every expert has at most one that is not
+// full.  Two axes, since one holds fewer than 2^32 threads; a multiple of 8 in all.
+inline dim3 fp8_grid(const Fp8GemmArgs& p, int64_t bm) {
+  const int64_t most = p.offsets ? p.m_total / bm + (p.m_total < p.experts ? p.m_total : p.experts)
+                                 : (p.m_total + bm - 1) / bm;
+  const int64_t blocks = most * p.n_tiles, row = 1 << 16;
+  if (blocks <= row) return dim3((unsigned)((blocks + 7) / 8 * 8));
+  return dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+
+// Item of this workgroup among those of the grid (an upper bound of the items, a multiple of 8):
+// every thread counts the items of a run of experts and the one whose run holds the
+// workgroup's item names it.  Items are numbered so that an XCD (workgroup b runs on b % 8)
+// gets consecutive ones, which share weight tiles (M-tiles first) or activation rows.
+// band: M-tiles that are walked together with all N-tiles (0: all of them).
+template <int NTHR>
+__device__ __forceinline__ Fp8Item fp8_locate(const Fp8GemmArgs& p, int32_t bm, int32_t bn, int32_t band) {
+  constexpr int WAVES = NTHR / 64;
+  __shared__ int32_t sums[WAVES], found[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t m_total = (int32_t)p.m_total;
+  const int32_t block = blockIdx.y * gridDim.x + blockIdx.x, blocks = gridDim.x * gridDim.y;
+  Fp8Item it;
+  int32_t first, rows, local;
+  if (!p.offsets) {
+    const int32_t total = fp8_items(p, m_total, bm);
+    local = logical_block(block, blocks, total);
+    if (local >= total) return Fp8Item{-1, 0, 0, 0};
+    it.e = 0;
+    first = 0;
+    rows = m_total;
+  } else {
+    const int32_t E = p.experts;
+    const int32_t per = (E + NTHR - 1) / NTHR;
+    const int32_t lo = min(tid * per, E), hi = min(lo + per, E);
+    int32_t mine = 0;
+    int32_t at = lo < hi ? clamp_off(p.offsets[lo], m_total) : 0;
+    const int32_t start = at;
+    for (int32_t e = lo; e < hi; ++e) {
+      const int32_t next = clamp_off(p.offsets[e + 1], m_total);
+      mine += fp8_items(p, next - at, bm);
+      at = next;
+    }
+    int32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t t = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += t;
+    }
+    if (lane == 63) sums[wave] = incl;
+    __syncthreads();
+    int32_t base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      if (w < wave) base += sums[w];
+      total += sums[w];
+    }
+    const int32_t item = logical_block(block, blocks, total);
+    if (item >= total) return Fp8Item{-1, 0, 0, 0};
+    int32_t run = base + incl - mine;
+    if (item >= run && item < run + mine) {
+      at = start;
+      for (int32_t e = lo; e < hi; ++e) {
+        const int32_t next = clamp_off(p.offsets[e + 1], m_total);
+        const int32_t n = fp8_items(p, next - at, bm);
+        if (item < run + n) {
+          found[0] = e;
+          found[1] = at;
+          found[2] = next - at;
+          found[3] = item - run;
+          break;
+        }
+        run += n;
+        at = next;
+      }
+    }
+    __syncthreads();
+    it.e = uniform(found[0]);
+    first = uniform(found[1]);
+    rows = uniform(found[2]);
+    local = uniform(found[3]);
+  }
+  const int32_t mts = (rows + bm - 1) / bm;
+  int32_t mt, nt;
+  if (band == 0 || mts <= band) {
+    nt = local / mts;
+    mt = local - nt * mts;
+  } else {
+    const int32_t per_band = band * p.n_tiles, b = local / per_band, within = local - b * per_band;
+    const int32_t tall = min(band, mts - b * band);
+    nt = within / tall;
+    mt = b * band + within - nt * tall;
+  }
+  it.row0 = first + mt * bm;
+  it.rows = min(bm, rows - mt * bm);
+  it.n0 = nt * bn;
+  return it;
+}
+
+// The activation row that result row r reads.
+__device__ __forceinline__ int32_t fp8_source_row(const Fp8GemmArgs& p, int32_t r) {
+  if (!p.a_row_index) return r;
+  const int32_t s = p.a_row_index[r], last = (int32_t)p.a_rows - 1;
+  return s < 0 ? 0 : s > last ? last : s;
+}
+
+// Four consecutive columns of a result row, rounded to nearest even.
+__device__ __forceinline__ void fp8_store4(const Fp8GemmArgs& p, int64_t row, int32_t col, const float4_t& v) {
+  const int64_t at = row * p.ldo + col;
+  if (p.vec4 && col + 4 <= p.n) {
+    if (p.out_dtype == kFewOutF32) {
+      *reinterpret_cast<float4_t*>(static_cast<float*>(p.out) + at) = v;
+    } else if (p.out_dtype == kFewOutF16) {
+      typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<half4_t*>(static_cast<_Float16*>(p.out) + at) =
+          half4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    } else {
+      typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<bf16x4_t*>(static_cast<__bf16*>(p.out) + at) =
+          bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < p.n) store_as(p.out, at + i, v[i], p.out_dtype);
+}
+
+}  // namespace moe_fp4

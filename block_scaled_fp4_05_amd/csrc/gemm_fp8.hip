@@ -1,0 +1,167 @@
+// FP8 block-scaled grouped product for few rows (moe_grouped_gemm_fp8):
+//
+//   out[r][j] = sum_b sa[src(r)][b] sw[e][j / 128][b] sum_{k in block b} A[src(r)][k] W[e][j][k]
+//
+// Bound: the weight stream, one byte an element (up to some 64 rows give few operations a
+// byte).  A workgroup owns 16 NT weight rows and up to 16 MT activation rows of one expert;
+// its W wavefronts split K, each with D blocks of 128 in flight in registers, and their sums
+// meet in LDS in wavefront order (no atomics: the same inputs give the same bits).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_fp8.h"
+
+namespace moe_fp4 {
+namespace {
+
+// 32 bytes of a row: the 16-byte pieces g and 4 + g of a block.
+__device__ __forceinline__ i32x8_t load32(rsrc_t rs, uint32_t off0, uint32_t off1, int32_t k, int hint) {
+  u32x4_t lo, hi;
+  if (hint) {
+    lo = __builtin_amdgcn_raw_buffer_load_b128(rs, off0, k, kLoadStreamOnce);
+    hi = __builtin_amdgcn_raw_buffer_load_b128(rs, off1, k, kLoadStreamOnce);
+  } else {
+    lo = __builtin_amdgcn_raw_buffer_load_b128(rs, off0, k, 0);
+    hi = __builtin_amdgcn_raw_buffer_load_b128(rs, off1, k, 0);
+  }
+  return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+template <int NT, int MT>
+struct Stage {
+  i32x8_t w[NT], a[MT];
+  float sa[MT];
+  float sw;
+};
+
+template <int NT, int MT, int W, int D>
+__global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
+  extern __shared__ __align__(16) char smem[];
+  const Fp8Item it = fp8_locate<W * 64>(p, 16 * MT, 16 * NT, 0);
+  if (it.e < 0) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int32_t k = p.k, kbs = p.k_blocks, n = p.n;
+
+  const rsrc_t w_rs = make_rsrc(p.w_q + (int64_t)it.e * n * k, (uint32_t)n * (uint32_t)k);
+  const float* w_sf = p.w_sf + ((int64_t)it.e * p.n_blocks + it.n0 / kFp8Block) * kbs;
+  // Without a row index the tile's rows follow each other: offsets from its first row.
+  const int64_t base = p.a_row_index ? 0 : it.row0;
+  const int64_t a_rows = p.a_row_index ? p.a_rows : it.rows;
+  const rsrc_t a_rs = make_rsrc(p.a_q + base * k, (uint32_t)(a_rows * k));
+  const rsrc_t s_rs = make_rsrc(p.a_sf + base * kbs, (uint32_t)(a_rows * kbs * 4));
+  uint32_t w_off[NT], a_off[MT], s_off[MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int32_t row = it.n0 + 16 * t + r;
+    w_off[t] = (uint32_t)(row < n ? row : n - 1) * (uint32_t)k + 16u * g;
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int32_t row = 16 * m + r;
+    const int32_t src = fp8_source_row(p, it.row0 + (row < it.rows ? row : it.rows - 1)) - (int32_t)base;
+    a_off[m] = (uint32_t)src * (uint32_t)k + 16u * g;
+    s_off[m] = (uint32_t)src * (uint32_t)kbs * 4u;
+  }
+
+  float4_t acc[NT][MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[t][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int32_t b0 = uniform(wave * kbs / W), b1 = uniform((wave + 1) * kbs / W);
+  Stage<NT, MT> st[D];
+  auto load = [&](Stage<NT, MT>& s, int32_t b) {
+    // Pieces past k (the last block's) and blocks past the share read zeros.
+    const bool in = b < b1;
+    const bool ok0 = in && b * kFp8Block + 16 * g < k, ok1 = in && b * kFp8Block + 64 + 16 * g < k;
+    const int32_t kk = uniform(b * kFp8Block);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      s.w[t] = load32(w_rs, ok0 ? w_off[t] : kOutOfRange, ok1 ? w_off[t] + 64 : kOutOfRange, kk, 1);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      s.a[m] = load32(a_rs, ok0 ? a_off[m] : kOutOfRange, ok1 ? a_off[m] + 64 : kOutOfRange, kk, 0);
+      s.sa[m] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(s_rs, in ? s_off[m] : kOutOfRange, uniform(b * 4), 0));
+    }
+    s.sw = ((sconst_f32)w_sf)[in ? b : b1 - 1];
+  };
+  auto multiply = [&](const Stage<NT, MT>& s) {
+    Half32 a[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) a[m] = fp8_widen(s.a[m]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const Half32 w = fp8_widen(s.w[t]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float4_t d = fp8_block_product(w, a[m]);
+        const float scale = s.sa[m] * s.sw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][m][i] = __builtin_fmaf(d[i], scale, acc[t][m][i]);
+      }
+    }
+  };
+  if (b0 < b1) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(st[d], b0 + d);
+    for (int32_t b = b0; b < b1; b += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (b + d < b1) multiply(st[d]);
+        load(st[d], b + d + D);
+      }
+    }
+  }
+
+  // Sums of the wavefronts, each with its tiles in LDS.
+  float4_t* const sums = reinterpret_cast<float4_t*>(smem);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sums[((wave * NT + t) * MT + m) * 64 + lane] = acc[t][m];
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * MT * 64; i += W * 64) {
+    float4_t v = sums[i];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += sums[w * NT * MT * 64 + i];
+    const int tile = i >> 6, t = tile / MT, m = tile % MT, l = i & 63;
+    const int32_t row = 16 * m + (l & 15), col = it.n0 + 16 * t + 4 * (l >> 4);
+    if (row < it.rows && col < n) fp8_store4(p, (int64_t)it.row0 + row, col, v);
+  }
+}
+
+template <int NT, int MT, int W, int D>
+hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
+  p.n_tiles = (p.n + 16 * NT - 1) / (16 * NT);
+  const dim3 grid = fp8_grid(p, 16 * MT);
+  hipLaunchKernelGGL((k_gemm_fp8_stream<NT, MT, W, D>), grid, dim3(W * 64), W * NT * MT * 1024, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_stream(const Fp8GemmArgs& p, hipStream_t stream) {
+  const int64_t avg = p.m_total / p.experts;
+  if (avg <= 4) return launch<1, 1, 8, 3>(p, stream);
+  if (avg <= 16) return launch<4, 2, 8, 2>(p, stream);
+  return launch<4, 4, 4, 2>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& args, hipStream_t stream) {
+  Fp8GemmArgs p = args;
+  const int64_t avg = p.m_total / p.experts;
+  if (p.m_total <= kFp8TiledRows || avg < kFp8TiledRows / 2) return launch_stream(p, stream);
+  if (p.offsets && p.experts > 1) {
+    // Small experts, then large ones.
+    p.rows_hi = kFp8TiledRows;
+    const hipError_t err = launch_stream(p, stream);
+    if (err != hipSuccess) return err;
+    p.rows_lo = kFp8TiledRows;
+    p.rows_hi = 0;
+  }
+  return launch_gemm_fp8_tiled(p, stream);
+}
+
+}  // namespace moe_fp4

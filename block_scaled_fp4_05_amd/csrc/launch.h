@@ -12,6 +12,23 @@ hipError_t launch_quantize(const void* x, int in_dtype, int64_t rows, int64_t k,
                            uint8_t* q, uint8_t* sf, float* tensor_scale, int dynamic,
                            hipStream_t stream);
 
+// Unsigned division of numbers below 2^31 by a constant of the launch: a multiplication and a
+// shift.  With 2^(b-1) < d <= 2^b and m = floor(2^(31+b) / d) + 1 (below 2^32), i m / 2^(31+b)
+// exceeds i / d by less than 2^-b <= 1/d, so the floors are equal.
+struct FastDiv {
+  uint32_t mul = 0, shift = 0, d = 1;
+  static FastDiv of(uint32_t d) {
+    FastDiv f;
+    f.d = d;
+    while (((uint64_t)1 << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)(((uint64_t)1 << (31 + f.shift)) / d + 1);
+    return f;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t i) const {
+    return d == 1 ? i : __umulhi(i, mul) >> (shift - 1);
+  }
+};
+
 // Tile shapes of the grouped GEMM.  Rows per work item = 16 * m_blocks; output
 // columns per wavefront = 16 * n_blocks; a workgroup holds `waves` wavefronts,
 // each working on its own item; one pipeline stage covers 256 * k_sub
@@ -225,6 +242,107 @@ struct RouteArgs {
   int32_t counts_pitch;  // experts rounded up to 8
 };
 hipError_t launch_route(const RouteArgs& args, hipStream_t stream);
+
+// Input types (the values of MOE_FP4_IN_*).
+constexpr int32_t kInBF16 = 0, kInF32 = 1, kInF16 = 2;
+
+// FP8 quantisers (quantize_fp8.hip).
+struct Fp8QuantArgs {
+  const void* x;  // [rows][ld_x]
+  int64_t ld_x;
+  const void* grad;  // [rows][ld_grad]: SwiGLU's gradient is quantised; or NULL
+  int64_t ld_grad;
+  uint8_t* q;  // [rows][k]
+  float* sf;   // [rows][k in blocks]
+  FastDiv per_row;  // by the blocks of a row
+  uint32_t blocks;  // of all rows, below 2^31 - 2^16
+  int32_t k;        // columns of q
+  int32_t dtype, swiglu, pow2;
+};
+hipError_t launch_quantize_fp8(const Fp8QuantArgs& args, hipStream_t stream);
+
+struct Fp8WeightArgs {
+  const void* w;  // [experts][n][k]
+  uint8_t* q;     // [experts][n][k]
+  float* sf;      // [experts][n blocks][k blocks]
+  uint8_t* qt;    // [experts][k][n] or NULL
+  float* sft;     // [experts][k blocks][n blocks]
+  int32_t experts, n, k, dtype, pow2;
+};
+hipError_t launch_quantize_fp8_weights(const Fp8WeightArgs& args, hipStream_t stream);
+
+// FP8 block-scaled grouped product (gemm_fp8.hip, gemm_fp8_tiled.hip).
+struct Fp8GemmArgs {
+  const uint8_t* a_q;  // [a_rows][k]
+  const float* a_sf;   // [a_rows][k_blocks]
+  int64_t a_rows;
+  const int32_t* a_row_index;  // [m_total] or NULL
+  const uint8_t* w_q;          // [experts][n][k]
+  const float* w_sf;           // [experts][n_blocks][k_blocks]
+  const int32_t* offsets;      // [experts + 1] or NULL: one expert, all rows
+  int64_t m_total;
+  int32_t experts, n, k, n_blocks, k_blocks;
+  void* out;
+  int64_t ldo;
+  int32_t out_dtype;  // MOE_FP4_OUT_*
+  int32_t vec4;       // four consecutive columns may be stored together
+  // Set by the launchers: N-tiles of an expert, and the experts' rows this launch takes.
+  int32_t n_tiles = 0, rows_lo = 0, rows_hi = 0;
+};
+hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& args, hipStream_t stream);
+// Workgroup tiles, for experts of p.rows_lo rows or more.
+hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& p, hipStream_t stream);
+// Rows from which an expert takes them.
+constexpr int32_t kFp8TiledRows = 64;
+
+// Token rows in expert order and back (rows.hip): out's rows are mapped onto x's.
+struct RowsArgs {
+  const void* x;
+  int64_t ld_x;  // bytes
+  int64_t source_rows;
+  const int32_t* map;  // row -> row of x (dispatch), or [rows][topk] (its gradient)
+  int32_t topk;
+  void* out;
+  int64_t ld_out;  // bytes
+  int64_t rows, cols, row_bytes;
+  int32_t esize, dtype;
+  // Set by the launchers.
+  int64_t items = 0, segments = 0;
+  int32_t lanes = 0;
+};
+hipError_t launch_dispatch(const RowsArgs& args, hipStream_t stream);
+hipError_t launch_dispatch_backward(const RowsArgs& args, hipStream_t stream);
+
+struct CombineBackwardArgs {
+  const void* dout;  // BF16 or FP32 [num_tokens][ld_dout]
+  int64_t ld_dout;
+  int32_t f32_dout;
+  const uint16_t* rows;  // BF16 [m_total][ld_rows]
+  int64_t ld_rows, m_total;
+  const int32_t* token_rows;   // [num_tokens][topk]
+  const float* token_weights;  // [num_tokens][topk]
+  const int32_t* row_token;    // [m_total] or NULL
+  int32_t topk;
+  int64_t num_tokens, n;
+  uint16_t* drows;  // BF16 [m_total][ld_drows]
+  int64_t ld_drows;
+  float* dweights;  // [num_tokens][topk]
+};
+hipError_t launch_combine_backward(const CombineBackwardArgs& args, hipStream_t stream);
+
+// Gradient of the router's weights (route_backward.hip).
+struct RouteBackwardArgs {
+  const void* logits;  // [tokens][ld] of dtype
+  int64_t ld;
+  const int32_t* ids;     // [tokens][topk]
+  const float* dweights;  // [tokens][topk]
+  void* dlogits;          // [tokens][ld_out] of dtype
+  int64_t ld_out, tokens;
+  int32_t experts, topk, dtype, sigmoid, renormalize;
+  // Set by the launcher: lanes of a token's slots, tokens of a wavefront.
+  int32_t slot_lanes = 0, group_tokens = 0;
+};
+hipError_t launch_route_backward(const RouteBackwardArgs& args, hipStream_t stream);
 
 // LDS a workgroup may use on gfx950.
 constexpr size_t kLdsBytes = 160 * 1024;

@@ -27,7 +27,7 @@ LIB_PATH = os.environ.get("MOE_FP4_LIB") or os.path.join(_PKG, "libmoe_fp4.so")
 
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_HIP, ERR_ARG = range(7)
 OUT_BF16, OUT_FP32, OUT_FP16 = 0, 1, 2
-IN_BF16, IN_FP32, IN_FP16 = 0, 1, 2
+IN_BF16, IN_FP32, IN_FP16, IN_FP8 = 0, 1, 2, 3
 SCALE_STATIC, SCALE_DYNAMIC = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
@@ -35,7 +35,9 @@ SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 EXPORTED = ("moe_fp4_quantize", "moe_grouped_gemm_fp4", "moe_grouped_gemm_fp4_packed",
             "moe_grouped_gemm_fp4_finalize", "moe_grouped_gemm_fp4_swiglu", "moe_fp4_combine",
             "moe_fp4_linear", "moe_fp4_ffn", "moe_fp4_ffn_workspace_size", "moe_fp4_route",
-            "moe_fp4_route_workspace_size",
+            "moe_fp4_route_workspace_size", "moe_fp8_quantize", "moe_fp8_quantize_weights",
+            "moe_grouped_gemm_fp8", "moe_fp4_dispatch", "moe_fp4_dispatch_backward",
+            "moe_fp4_combine_backward", "moe_fp4_route_backward",
             "moe_fp4_pack_weights", "moe_fp4_unpack_weights", "moe_grouped_gemm_fp4_plan",
             "moe_grouped_gemm_fp4_workspace_size", "moe_fp4_stage_bytes",
             "moe_fp4_status_string", "moe_fp4_abi_version")
@@ -92,6 +94,21 @@ def lib() -> ctypes.CDLL:
     L.moe_fp4_route.argtypes = [vp, i, i64, i32, i64, i, vp, i, i32, i32, i32, vp, vp, vp, vp, vp,
                                 vp, ctypes.c_size_t, vp]
     L.moe_fp4_route.restype = i
+    L.moe_fp8_quantize.argtypes = [vp, i, i64, i64, i64, i, vp, i64, i, vp, vp, vp]
+    L.moe_fp8_quantize.restype = i
+    L.moe_fp8_quantize_weights.argtypes = [vp, i, i32, i64, i64, i, vp, vp, vp, vp, vp]
+    L.moe_fp8_quantize_weights.restype = i
+    L.moe_grouped_gemm_fp8.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, i64, i64, i64, vp, i, i64, vp]
+    L.moe_grouped_gemm_fp8.restype = i
+    L.moe_fp4_dispatch.argtypes = [vp, i, i64, i64, i64, vp, i64, vp, i64, vp]
+    L.moe_fp4_dispatch.restype = i
+    L.moe_fp4_dispatch_backward.argtypes = [vp, i, i64, i64, i64, vp, i32, i64, vp, i64, vp]
+    L.moe_fp4_dispatch_backward.restype = i
+    L.moe_fp4_combine_backward.argtypes = [vp, i, i64, i64, i64, vp, i64, i64, vp, vp, i32, vp, vp, i64,
+                                           vp, vp]
+    L.moe_fp4_combine_backward.restype = i
+    L.moe_fp4_route_backward.argtypes = [vp, i, i64, i32, i64, vp, vp, i32, i, i, vp, i64, vp]
+    L.moe_fp4_route_backward.restype = i
     for f in (L.moe_fp4_pack_weights, L.moe_fp4_unpack_weights):
         f.argtypes = [vp, vp, i32, i64, i64, vp]
         f.restype = i
@@ -707,4 +724,284 @@ def route(logits, topk: int, score: str = "softmax", bias=None, renormalize: boo
         None if workspace is None else workspace.data_ptr(), need, _launch_stream(stream, dev))
     if st != OK:
         raise MoeFp4Error(st, "moe_fp4_route")
+    return out
+
+
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 that n elements take."""
+    return -(-n // FP8_BLOCK)
+
+
+def _typed(t, name, dims, types=_IN_TYPES):
+    """A tensor of one of `types` with `dims` axes; returns its shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in types or t.dim() != dims:
+        kinds = " or ".join(str(x).removeprefix("torch.") for x in types)
+        raise ValueError(f"{name}: expected a {dims}-D {kinds} tensor")
+    return t.shape
+
+
+def _new(stream, like, shape, dtype):
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def quantize_fp8_raw(*args):
+    """moe_fp8_quantize with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp8_quantize(*args)
+
+
+def quantize_fp8(x, swiglu: bool = False, grad=None, power_of_two: bool = False, q=None, sf=None,
+                 stream=None):
+    """Rows to FP8 (E4M3) with one float32 scale per row and 128 columns.  x: bfloat16, float16 or
+    float32 CUDA tensor [rows][k], unit column stride.  swiglu: x is [rows][2k], gate and up
+    halves, and silu(gate) * up is quantised; with grad (x's type, [rows][k]) the gradient of
+    that with respect to x, [rows][2k].  power_of_two: scales rounded up to powers of two.
+    Returns (q float8_e4m3fn [rows][columns], sf float32 [rows][ceil(columns / 128)]);
+    new ones belong to the launch stream."""
+    rows, width = _typed(x, "x", 2)
+    k = width // 2 if swiglu else width
+    if swiglu and width % 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected an even number of columns")
+    if grad is not None and not swiglu:
+        raise ValueError("grad: only with swiglu")
+    ld = _pitch(x, "x", x.dtype, (rows, width))
+    ld_grad = 0 if grad is None else _pitch(grad, "grad", x.dtype, (rows, k))
+    cols = k if grad is None else width
+    if q is None:
+        q = _new(stream, x, (rows, cols), FP8)
+    else:
+        _exact(q, "q", FP8, (rows, cols))
+    if sf is None:
+        sf = _new(stream, x, (rows, _blocks(cols)), torch.float32)
+    else:
+        _exact(sf, "sf", torch.float32, (rows, _blocks(cols)))
+    dev = _same_cuda("x grad q sf", x, grad, q, sf)
+    st = (_lib or lib()).moe_fp8_quantize(
+        x.data_ptr(), _IN_TYPES[x.dtype], rows, k, ld, 1 if swiglu else 0,
+        None if grad is None else grad.data_ptr(), ld_grad, 1 if power_of_two else 0, q.data_ptr(),
+        sf.data_ptr(), _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp8_quantize")
+    return q, sf
+
+
+def quantize_fp8_weights_raw(*args):
+    """moe_fp8_quantize_weights with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp8_quantize_weights(*args)
+
+
+def quantize_fp8_weights(w, transposed: bool = False, power_of_two: bool = False, stream=None):
+    """Weights to FP8 (E4M3) with one float32 scale per 128 x 128 block: w bfloat16, float16 or
+    float32 CUDA tensor [E][n][k] or [n][k], contiguous.  Returns (q, sf), and with transposed
+    (q, sf, qt, sft), the last two of the transposed matrices ([E][k][n]): the same codes and
+    scales, the weights of the product that takes a gradient back through w.  They belong to the
+    launch stream."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w: expected a 2-D or 3-D bfloat16, float16 or float32 tensor")
+    _typed(w, "w", w.dim())
+    *lead, n, k = w.shape
+    if not w.is_contiguous():
+        raise ValueError("w: must be contiguous")
+    f32 = torch.float32
+    q, sf = _new(stream, w, (*lead, n, k), FP8), _new(stream, w, (*lead, _blocks(n), _blocks(k)), f32)
+    qt = sft = None
+    if transposed:
+        qt, sft = _new(stream, w, (*lead, k, n), FP8), _new(stream, w, (*lead, _blocks(k), _blocks(n)), f32)
+    dev = _same_cuda("w q sf qt sft", w, q, sf, qt, sft)
+    st = (_lib or lib()).moe_fp8_quantize_weights(
+        w.data_ptr(), _IN_TYPES[w.dtype], lead[0] if lead else 1, n, k, 1 if power_of_two else 0,
+        q.data_ptr(), sf.data_ptr(), None if qt is None else qt.data_ptr(),
+        None if sft is None else sft.data_ptr(), _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp8_quantize_weights")
+    return (q, sf, qt, sft) if transposed else (q, sf)
+
+
+def gemm_fp8_raw(*args):
+    """moe_grouped_gemm_fp8 with raw pointers (C argument order); returns the status."""
+    return lib().moe_grouped_gemm_fp8(*args)
+
+
+def _gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index, m_total, E, n, out, out_dtype, stream, what):
+    a_rows, k = _typed(a_q, "a_q", 2, (FP8,))
+    _exact(a_q, "a_q", FP8, (a_rows, k))
+    _exact(a_sf, "a_sf", torch.float32, (a_rows, _blocks(k)))
+    if a_row_index is not None:
+        m_total = a_row_index.shape[0] if m_total is None else m_total
+        _exact(a_row_index, "a_row_index", torch.int32, (m_total,))
+    elif m_total is None:
+        m_total = a_rows
+    if out is None:
+        if out_dtype not in _OUT_TYPES:
+            raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16, float16 or float32")
+        out = _new(stream, a_q, (m_total, n), out_dtype)
+    elif not isinstance(out, torch.Tensor) or out.dtype not in _OUT_TYPES:
+        raise ValueError("out: expected a bfloat16, float16 or float32 tensor")
+    ldo = _pitch(out, "out", out.dtype, (m_total, n))
+    dev = _same_cuda("a_q a_sf w_q w_sf offsets a_row_index out", a_q, a_sf, w_q, w_sf, offsets, a_row_index, out)
+    st = (_lib or lib()).moe_grouped_gemm_fp8(
+        a_q.data_ptr(), a_sf.data_ptr(), a_rows, None if a_row_index is None else a_row_index.data_ptr(),
+        w_q.data_ptr(), w_sf.data_ptr(), None if offsets is None else offsets.data_ptr(), E, m_total, n, k,
+        out.data_ptr(), _OUT_TYPES[out.dtype], ldo, _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, what)
+    return out
+
+
+def grouped_gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index=None, out=None, out_dtype=torch.bfloat16,
+                     m_total: int | None = None, stream=None):
+    """Grouped product of FP8 rows with FP8 weights in blocks of 128: a_q float8_e4m3fn
+    [a_rows][k], a_sf float32 [a_rows][ceil(k / 128)] (quantize_fp8); w_q [E][n][k], w_sf
+    [E][ceil(n / 128)][ceil(k / 128)] (quantize_fp8_weights); offsets int32 [E + 1]; a_row_index
+    int32 [m_total] or None.  m_total defaults to a_row_index's length, else a_rows.  Returns
+    out [m_total][n] of out_dtype (or the given out's type); a new one belongs to the launch
+    stream.  Rows outside the offsets are not written."""
+    E, n, k = _typed(w_q, "w_q", 3, (FP8,))
+    if isinstance(a_q, torch.Tensor) and a_q.dim() == 2 and a_q.shape[1] != k:
+        raise ValueError(f"w_q: shape {tuple(w_q.shape)}, expected {a_q.shape[1]} columns")
+    _exact(w_q, "w_q", FP8, (E, n, k))
+    _exact(w_sf, "w_sf", torch.float32, (E, _blocks(n), _blocks(k)))
+    _exact(offsets, "offsets", torch.int32, (E + 1,))
+    return _gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index, m_total, E, n, out, out_dtype, stream,
+                     "moe_grouped_gemm_fp8")
+
+
+def linear_fp8(a_q, a_sf, w_q, w_sf, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Dense product of FP8 rows [m][k] with FP8 weights [n][k] in blocks of 128, scales as for
+    grouped_gemm_fp8.  Returns out [m][n]; a new one belongs to the launch stream."""
+    n, k = _typed(w_q, "w_q", 2, (FP8,))
+    if isinstance(a_q, torch.Tensor) and a_q.dim() == 2 and a_q.shape[1] != k:
+        raise ValueError(f"w_q: shape {tuple(w_q.shape)}, expected {a_q.shape[1]} columns")
+    _exact(w_q, "w_q", FP8, (n, k))
+    _exact(w_sf, "w_sf", torch.float32, (_blocks(n), _blocks(k)))
+    return _gemm_fp8(a_q, a_sf, w_q, w_sf, None, None, None, 1, n, out, out_dtype, stream, "moe_grouped_gemm_fp8")
+
+
+_ROW_TYPES = {**_IN_TYPES, FP8: IN_FP8}
+
+
+def dispatch_raw(*args):
+    """moe_fp4_dispatch with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_dispatch(*args)
+
+
+def dispatch(x, row_token, out=None, stream=None):
+    """Token rows in expert order: out[r] = x[row_token[r]] (Routing.row_token), zeros where there is
+    no such token.  x: CUDA tensor [tokens][n] (bfloat16, float16, float32 or float8_e4m3fn),
+    unit column stride; row_token int32 [rows].  Returns out [rows][n] of x's type; a new one
+    belongs to the launch stream."""
+    T, n = _typed(x, "x", 2, _ROW_TYPES)
+    ld = _pitch(x, "x", x.dtype, (T, n))
+    _need(row_token, "row_token", torch.int32, (None,))
+    m = row_token.shape[0]
+    if out is None:
+        out = _new(stream, x, (m, n), x.dtype)
+    ldo = _pitch(out, "out", x.dtype, (m, n))
+    dev = _same_cuda("x row_token out", x, row_token, out)
+    st = (_lib or lib()).moe_fp4_dispatch(x.data_ptr(), _ROW_TYPES[x.dtype], T, n, ld, row_token.data_ptr(), m,
+                                          out.data_ptr(), ldo, _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_dispatch")
+    return out
+
+
+def dispatch_backward_raw(*args):
+    """moe_fp4_dispatch_backward with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_dispatch_backward(*args)
+
+
+def dispatch_backward(dy, token_rows, out=None, stream=None):
+    """The gradient of dispatch: out[t] = sum_s dy[token_rows[t][s]] in float32, slots without a row
+    in dy passed over.  dy: bfloat16, float16 or float32 CUDA tensor [rows][n], unit column
+    stride; token_rows int32 [tokens][topk] (Routing.token_rows).  Returns out [tokens][n] of
+    dy's type; a new one belongs to the launch stream."""
+    m, n = _typed(dy, "dy", 2)
+    ld = _pitch(dy, "dy", dy.dtype, (m, n))
+    _need(token_rows, "token_rows", torch.int32, (None, None))
+    T, K = token_rows.shape
+    if out is None:
+        out = _new(stream, dy, (T, n), dy.dtype)
+    ldo = _pitch(out, "out", dy.dtype, (T, n))
+    dev = _same_cuda("dy token_rows out", dy, token_rows, out)
+    st = (_lib or lib()).moe_fp4_dispatch_backward(
+        dy.data_ptr(), _IN_TYPES[dy.dtype], m, n, ld, token_rows.data_ptr(), K, T, out.data_ptr(), ldo,
+        _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_dispatch_backward")
+    return out
+
+
+def combine_backward_raw(*args):
+    """moe_fp4_combine_backward with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_combine_backward(*args)
+
+
+def combine_backward(dout, rows, token_rows, token_weights, row_token=None, drows=None, dweights=None,
+                     stream=None):
+    """The gradient of combine.  dout: bfloat16 or float32 CUDA tensor [tokens][n]; rows, token_rows and
+    token_weights as combine took them.  Returns (drows bfloat16 like rows, dweights float32
+    [tokens][topk]); the residual's gradient is dout itself.  Rows that no slot names: with
+    row_token (Routing.row_token) they are zeroed; without it a new drows is zeroed as a whole
+    first, and a given one keeps them.  New results belong to the launch stream."""
+    T, n = _typed(dout, "dout", 2, (torch.bfloat16, torch.float32))
+    ld = _pitch(dout, "dout", dout.dtype, (T, n))
+    _typed(rows, "rows", 2, (torch.bfloat16,))
+    m = rows.shape[0]
+    ld_rows = _pitch(rows, "rows", torch.bfloat16, (m, n))
+    _need(token_rows, "token_rows", torch.int32, (T, None))
+    K = token_rows.shape[1]
+    _exact(token_weights, "token_weights", torch.float32, (T, K))
+    if row_token is not None:
+        _exact(row_token, "row_token", torch.int32, (m,))
+    if drows is None:
+        with _on(stream):
+            drows = rows.new_empty((m, n)) if row_token is not None else rows.new_zeros((m, n))
+    ld_drows = _pitch(drows, "drows", torch.bfloat16, (m, n))
+    if dweights is None:
+        dweights = _new(stream, dout, (T, K), torch.float32)
+    else:
+        _exact(dweights, "dweights", torch.float32, (T, K))
+    dev = _same_cuda("dout rows token_rows token_weights row_token drows dweights", dout, rows, token_rows,
+                     token_weights, row_token, drows, dweights)
+    st = (_lib or lib()).moe_fp4_combine_backward(
+        dout.data_ptr(), OUT_FP32 if dout.dtype is torch.float32 else OUT_BF16, T, n, ld, rows.data_ptr(),
+        ld_rows, m, token_rows.data_ptr(), token_weights.data_ptr(), K,
+        None if row_token is None else row_token.data_ptr(), drows.data_ptr(), ld_drows,
+        dweights.data_ptr(), _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_combine_backward")
+    return drows, dweights
+
+
+def route_backward_raw(*args):
+    """moe_fp4_route_backward with raw pointers (C argument order); returns the status."""
+    return lib().moe_fp4_route_backward(*args)
+
+
+def route_backward(logits, ids, dweights, score: str = "softmax", renormalize: bool = True, out=None,
+                   stream=None):
+    """The gradient of route's weights with respect to its logits, the chosen experts held fixed.
+    logits, score and renormalize as route took them, ids int32 [tokens][topk] as it gave them
+    (Routing.ids); dweights float32 [tokens][topk], the gradient of Routing.weights.  Returns out
+    [tokens][E] of the logits' type; a new one belongs to the launch stream."""
+    T, E = _typed(logits, "logits", 2)
+    if score not in _SCORES:
+        raise ValueError(f"score: {score!r}, expected 'softmax' or 'sigmoid'")
+    ld = _pitch(logits, "logits", logits.dtype, (T, E))
+    _need(ids, "ids", torch.int32, (T, None))
+    K = ids.shape[1]
+    _exact(dweights, "dweights", torch.float32, (T, K))
+    if out is None:
+        out = _new(stream, logits, (T, E), logits.dtype)
+    ldo = _pitch(out, "out", logits.dtype, (T, E))
+    dev = _same_cuda("logits ids dweights out", logits, ids, dweights, out)
+    st = (_lib or lib()).moe_fp4_route_backward(
+        logits.data_ptr(), _IN_TYPES[logits.dtype], T, E, ld, ids.data_ptr(), dweights.data_ptr(), K,
+        _SCORES[score], 1 if renormalize else 0, out.data_ptr(), ldo, _launch_stream(stream, dev))
+    if st != OK:
+        raise MoeFp4Error(st, "moe_fp4_route_backward")
     return out

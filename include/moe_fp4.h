@@ -57,8 +57,9 @@ enum {
 };
 
 /* Input element types of moe_fp4_quantize (BF16, FP32), of the few-token entry points
- * (BF16, FP16) and of the router (all three). */
-enum { MOE_FP4_IN_BF16 = 0, MOE_FP4_IN_FP32 = 1, MOE_FP4_IN_FP16 = 2 };
+ * (BF16, FP16), of the router, the FP8 quantisers and the row gradients (BF16, FP32, FP16) and
+ * of moe_fp4_dispatch (all four; FP8 elements are bytes that it copies). */
+enum { MOE_FP4_IN_BF16 = 0, MOE_FP4_IN_FP32 = 1, MOE_FP4_IN_FP16 = 2, MOE_FP4_IN_FP8 = 3 };
 
 /* Tensor-scale modes of moe_fp4_quantize. */
 enum {
@@ -480,6 +481,170 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
                   int32_t topk_groups, int32_t* ids, float* weights, int32_t* offsets,
                   int32_t* row_token, int32_t* token_rows, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/*
+ * FP8 in blocks of 128: the second weight format.  An element is an E4M3 byte (OCP OFP8 v1.0)
+ * and a block of 128 shares one FP32 scale: activations q[rows][k], sf[rows][KB] with one
+ * scale for a row's 128 columns; weights w_q[E][n][k], w_sf[E][NB][KB] with one for 128 x
+ * 128 elements; KB = ceil(k / 128), NB = ceil(n / 128), and the last block of a row or column
+ * may be shorter.  An element's value is E4M3(byte) * scale.
+ */
+
+/*
+ * moe_fp8_quantize -- rows to FP8 blocks of 1 x 128.  With v the values below, per row and block:
+ *
+ *     s = fl(max(max |v|, 448 * 2^-126) / 448), with power_of_two the next power of two at
+ *     or above that;   code = E4M3_RNE(fl(v / s));   sf = s
+ *
+ * fl() one IEEE binary32 operation; the division is a true one.  A zero block has scale 2^-126
+ * and signed zero codes.  A NaN stays one and does not raise the scale; a block with an infinity
+ * has an infinite scale and stands for NaN throughout.
+ *   swiglu = 0               v = x, k columns.
+ *   swiglu = 1, grad NULL    x has 2k columns, gate and up: v = silu(gate) * up, k columns, in
+ *                            FP32, silu(g) = g / (1 + e^-g).
+ *   swiglu = 1, grad         its gradient, 2k columns: v = [grad * up * s (1 + gate (1 - s)) |
+ *                            grad * silu(gate)], s = 1 / (1 + e^-gate), in FP32; the blocks run
+ *                            over all 2k columns.
+ *   x          device, [rows][ld_x] of in_dtype (BF16, FP32 or FP16), 16-byte aligned, the
+ *              pitch a multiple of 16 bytes; grad [rows][ld_grad] of the same type, k columns.
+ *   rows       >= 0 (0 is a no-op).  k a multiple of 16.
+ *   q          device, [rows][columns of v] bytes, 16-byte aligned; sf [rows][blocks] floats.
+ * Deterministic.
+ * Errors: NULL, SHAPE (rows < 0, k < 1, k % 16, a pitch below its row), ALIGN, ARG (in_dtype,
+ * swiglu or power_of_two not 0 or 1, grad without swiglu, q or sf overlapping another buffer),
+ * UNSUPPORTED (about 2^31 blocks or more, k > 2^29 - 1024), HIP.
+ */
+int moe_fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t k, int64_t ld_x, int swiglu,
+                     const void* grad, int64_t ld_grad, int power_of_two, uint8_t* q, float* sf,
+                     void* stream);
+
+/*
+ * moe_fp8_quantize_weights -- contiguous w[E][n][k] (BF16, FP32 or FP16) to FP8 blocks of 128 x
+ * 128, by the rule above with the block's largest magnitude.  qt and sft (both or neither)
+ * receive the transposed matrices qt[E][k][n], sft[E][KB][NB]: the same codes and
+ * scales, as the weights of the product that takes a gradient back through w.
+ *   n       >= 1; a multiple of 16 with qt.  k a multiple of 16.
+ *   w, q, qt 16-byte aligned; sf, sft 4-byte.
+ * Errors: NULL (w, q, sf; one of qt and sft), SHAPE (num_experts, n, k < 1, k % 16, n % 16
+ * with qt), ALIGN, ARG (in_dtype, power_of_two, an output overlapping another buffer),
+ * UNSUPPORTED (num_experts > 8192, n * k >= 2^31 - 4096, n > 128 * 65535), HIP.
+ */
+int moe_fp8_quantize_weights(const void* w, int in_dtype, int32_t num_experts, int64_t n, int64_t k,
+                             int power_of_two, uint8_t* q, float* sf, uint8_t* qt, float* sft,
+                             void* stream);
+
+/*
+ * moe_grouped_gemm_fp8 -- the grouped product of FP8 rows with FP8 weights.  For each expert e and
+ * each row r in [off[e], off[e+1]):
+ *
+ *     out[r][j] = round( sum_b a_sf[src(r)][b] * w_sf[e][j / 128][b]
+ *                              * sum_{k in block b} A(src(r), k) * W(e, j, k) ),  j < n
+ *     src(r) = a_row_index ? a_row_index[r] : r
+ *
+ * Blocks are summed in FP32 and the result is rounded once, to out_dtype, nearest even.  Inside a
+ * block the products are exact and their sum FP32 for an FP32 out and for experts of few
+ * rows; for a 16-bit out, experts of many rows use the FP8 matrix cores, which cut each of eight
+ * consecutive products 13 bits below the leading bit of the largest of them (about 1.5e-5 of a
+ * result on Gaussian data, against a rounding of 2^-9 or 2^-12).  Deterministic.  Columns
+ * >= n and rows outside [off[0], off[E]) are not written; an empty expert writes nothing.
+ *   a_q, a_sf      device, [a_rows][k] bytes, 16-byte aligned, and [a_rows][KB] floats.
+ *   a_row_index    device, [m_total] int32 in [0, a_rows), or NULL for identity (then a_rows
+ *                  >= m_total).
+ *   w_q, w_sf      device, [E][n][k] bytes, 16-byte aligned, and [E][NB][KB] floats.
+ *   expert_offsets as in moe_grouped_gemm_fp4 (device-side preconditions, clamped alike), or NULL
+ *                  with num_experts = 1: all m_total rows, the dense linear layer.
+ *   m_total        >= 0 (0 is a no-op).  n >= 1.  k a multiple of 16.
+ *   out            device, [m_total][ldo] of out_dtype (MOE_FP4_OUT_*), aligned to its
+ *                  element, ldo >= n (stores are widest with 16-byte aligned rows).
+ * Errors: NULL, SHAPE (num_experts, n or k < 1, m_total < 0, ldo < n, too few a_rows), ALIGN, ARG
+ * (out_dtype, out overlapping an operand), UNSUPPORTED (k % 16, k > 2^22, num_experts > 8192,
+ * n * k >= 2^31 - 4096, a_rows * k too with a row index, m_total above about 2^29, or (m_total / 16
+ * + E) * n / 16 above 2^31), HIP.
+ */
+int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
+                         const int32_t* a_row_index, const uint8_t* w_q, const float* w_sf,
+                         const int32_t* expert_offsets, int32_t num_experts, int64_t m_total, int64_t n,
+                         int64_t k, void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * moe_fp4_dispatch -- token rows copied into expert order (moe_fp4_route's row_token):
+ *
+ *     out[r][j] = x[row_token[r]][j],  0 where row_token[r] is outside [0, tokens)
+ *
+ * The grouped GEMMs gather their rows by themselves; this is for rows that travel (send
+ * buffers of expert parallelism) or that other code reads.
+ *   x, out     device, [tokens][ld_x] and [m_total][ldo] of dtype (MOE_FP4_IN_*), aligned to the
+ *              element (widest accesses where both bases and pitches are multiples of 16 bytes).
+ *   row_token  device, [m_total] int32, any values.
+ * Columns >= n of out are not touched.  m_total == 0 is a no-op.
+ * Errors: NULL, SHAPE (tokens or m_total < 0, n < 1, a pitch below n), ALIGN, ARG (dtype, out
+ * overlapping x or row_token), UNSUPPORTED (tokens or m_total >= 2^31), HIP.
+ *
+ * moe_fp4_dispatch_backward -- its gradient, a sum over each token's rows in slot order in FP32:
+ *
+ *     dx[t][j] = round( sum_s dy[token_rows[t][s]][j] )  over the slots with a row in [0, m_total)
+ *
+ * A token without one gets 0.  BF16, FP32 or FP16; arguments alike, with dy[m_total][ld_dy], dx
+ * [tokens][ld_dx] and token_rows [tokens][topk] (topk up to 1024).  Deterministic.
+ */
+int moe_fp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t n, int64_t ld_x,
+                     const int32_t* row_token, int64_t m_total, void* out, int64_t ldo, void* stream);
+int moe_fp4_dispatch_backward(const void* dy, int dtype, int64_t m_total, int64_t n, int64_t ld_dy,
+                              const int32_t* token_rows, int32_t topk, int64_t tokens, void* dx,
+                              int64_t ld_dx, void* stream);
+
+/*
+ * moe_fp4_combine_backward -- the gradient of moe_fp4_combine with respect to its rows and weights
+ * (with respect to its residual it is dout itself).  For token t and slot s with a row r =
+ * token_rows[t][s] in [0, m_total):
+ *
+ *     drows[r][j]    = bf16( fl(token_weights[t][s] * dout[t][j]) )
+ *     dweights[t][s] = sum_j rows[r][j] * dout[t][j]      (FP32)
+ *
+ * and dweights[t][s] = 0 for the other slots.  A row that no slot names is zeroed if row_token
+ * is given and none of row_token's token's slots names it; without row_token it is not written.
+ * Preconditions, not checked (a violation stays inside the buffers): no row is named twice, and
+ * row_token agrees with token_rows, as moe_fp4_route leaves them.
+ *   dout      device, [num_tokens][ld_dout] BF16 or FP32 (the type combine wrote), 16-byte
+ *             aligned, the pitch a multiple of 16 bytes.
+ *   rows, drows device, [m_total][ld_rows] and [m_total][ld_drows] BF16, 16-byte aligned, pitches
+ *             multiples of 8.
+ *   row_token device, [m_total] int32, or NULL.
+ *   n         a multiple of 16.
+ * Deterministic.
+ * Errors: NULL, SHAPE (sizes < 0, topk or n < 1, a pitch below n), ALIGN, ARG (dout_dtype, drows
+ * or dweights overlapping another buffer), UNSUPPORTED (n % 16, topk > 1024, num_tokens > 2^23,
+ * m_total above 2^27), HIP.
+ */
+int moe_fp4_combine_backward(const void* dout, int dout_dtype, int64_t num_tokens, int64_t n, int64_t ld_dout,
+                             const uint16_t* rows, int64_t ld_rows, int64_t m_total,
+                             const int32_t* token_rows, const float* token_weights, int32_t topk,
+                             const int32_t* row_token, uint16_t* drows, int64_t ld_drows, float* dweights,
+                             void* stream);
+
+/*
+ * moe_fp4_route_backward -- the gradient of moe_fp4_route's weights with respect to its logits, the
+ * choice of experts held fixed (a selection bias plays no part).  With p the scores as in
+ * moe_fp4_route, d[s] the gradient of slot s's weight and e_s = ids[t][s]:
+ *
+ *     SOFTMAX, renormalize   w = softmax of the chosen logits;  dx[e_s] += w_s (d_s - sum w d)
+ *     SOFTMAX                dx[e] = p_e (sum over e_s = e of d_s - sum_s p_s d_s), every e
+ *     SIGMOID, renormalize   w = p / sum of the chosen p;  dx[e_s] += w_s (1 - p_s)(d_s - sum w d)
+ *     SIGMOID                dx[e_s] += p_s (1 - p_s) d_s
+ *
+ * and 0 for the other experts, in FP32, rounded once to dtype.  A slot whose id is outside [0,
+ * num_experts) plays no part.  A token whose chosen logits (SOFTMAX without renormalize: all its
+ * logits) are all -inf has the formula's NaN.  Deterministic.
+ *   logits     device, [tokens][ld] of dtype (BF16, FP32 or FP16), aligned to its element.
+ *   ids, dweights device, [tokens][topk] int32 / float, topk 1 .. 32.
+ *   dlogits    device, [tokens][ld_out] of dtype; columns >= num_experts are not touched.
+ * Errors: NULL, SHAPE (tokens < 0, num_experts or topk < 1, a pitch below num_experts), ALIGN, ARG
+ * (dtype, score, renormalize, dlogits overlapping another buffer), UNSUPPORTED (num_experts >
+ * 1024, topk > 32, tokens > 2^24), HIP.
+ */
+int moe_fp4_route_backward(const void* logits, int dtype, int64_t tokens, int32_t num_experts, int64_t ld,
+                           const int32_t* ids, const float* dweights, int32_t topk, int score,
+                           int renormalize, void* dlogits, int64_t ld_out, void* stream);
 
 /*
  * moe_grouped_gemm_fp4_workspace_size -- device workspace bytes the grouped GEMM
