@@ -162,6 +162,7 @@ int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
   a.ldo = ldo;
   a.out_dtype = out_dtype;
   a.vec4 = ldo % 4 == 0 && aligned(out, 4 * es);
+  a.vec8 = ldo % 8 == 0 && aligned(out, 16);
   return status_of(moe_fp4::launch_grouped_gemm_fp8(a, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -200,4 +200,24 @@ __device__ __forceinline__ void fp8_store4(const Fp8GemmArgs& p, int64_t row, in
     if (col + i < p.n) store_as(p.out, at + i, v[i], p.out_dtype);
 }
 
+// Eight consecutive columns of a result row, of which those below n are stored.
+__device__ __forceinline__ void fp8_store8(const Fp8GemmArgs& p, int64_t row, int32_t col, const float4_t& lo,
+                                           const float4_t& hi) {
+  if (p.vec8 && col + 8 <= p.n && p.out_dtype != kFewOutF32) {
+    u32x4_t v;
+    if (p.out_dtype == kFewOutF16) {
+      v = __builtin_bit_cast(u32x4_t, half8_t{(_Float16)lo[0], (_Float16)lo[1], (_Float16)lo[2], (_Float16)lo[3],
+                                              (_Float16)hi[0], (_Float16)hi[1], (_Float16)hi[2], (_Float16)hi[3]});
+    } else {
+      typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+      v = __builtin_bit_cast(u32x4_t, bf16x8_t{(__bf16)lo[0], (__bf16)lo[1], (__bf16)lo[2], (__bf16)lo[3],
+                                               (__bf16)hi[0], (__bf16)hi[1], (__bf16)hi[2], (__bf16)hi[3]});
+    }
+    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.out) + row * p.ldo + col) = v;
+    return;
+  }
+  if (col < p.n) fp8_store4(p, row, col, lo);
+  if (col + 4 < p.n) fp8_store4(p, row, col + 4, hi);
+}
+
 }  // namespace moe_fp4

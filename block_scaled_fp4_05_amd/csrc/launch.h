@@ -285,7 +285,7 @@ struct Fp8GemmArgs {
   void* out;
   int64_t ldo;
   int32_t out_dtype;  // MOE_FP4_OUT_*
-  int32_t vec4;       // four consecutive columns may be stored together
+  int32_t vec4, vec8;  // four and eight consecutive columns may be stored together
   // Set by the launchers: N-tiles of an expert, and the experts' rows this launch takes.
   int32_t n_tiles = 0, rows_lo = 0, rows_hi = 0;
 };
