@@ -130,12 +130,11 @@ int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
       a_rows > kLimit || (a_row_index && a_rows > kLimit / k))
     return MOE_FP4_ERR_UNSUPPORTED;
   if (m_total == 0) return MOE_FP4_OK;
+  if (ldo > (1 << 20)) return MOE_FP4_ERR_UNSUPPORTED;  // 256 rows of FP32 within 32-bit offsets
   // Items are counted in 32 bits.
   const int64_t m_tiles = m_total / 16 + (m_total < num_experts ? m_total : num_experts) + 1;
   if (m_tiles > kLimit / ((n + 15) / 16)) return MOE_FP4_ERR_UNSUPPORTED;
-  const int64_t ob = extent(m_total, n, ldo, es);
-  if (ob < 0) return MOE_FP4_ERR_SHAPE;
-  const int64_t nb = blocks(n), kb = blocks(k);
+  const int64_t ob = extent(m_total, n, ldo, es), nb = blocks(n), kb = blocks(k);
   const Range r[] = {{a_q, a_rows * k},
                      {a_sf, a_rows * kb * 4},
                      {a_row_index, a_row_index ? m_total * 4 : 0},
@@ -162,7 +161,6 @@ int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
   a.ldo = ldo;
   a.out_dtype = out_dtype;
   a.vec4 = ldo % 4 == 0 && aligned(out, 4 * es);
-  a.vec8 = ldo % 8 == 0 && aligned(out, 16);
   return status_of(moe_fp4::launch_grouped_gemm_fp8(a, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -60,116 +60,119 @@ __device__ __forceinline__ float4_t fp8_block_product(const Half32& w, const Hal
 
 // Where a workgroup works (uniform).
 struct Fp8Item {
-  int32_t e;     // expert; -1: no item
+  int32_t e;     // expert
   int32_t row0;  // first result row
   int32_t rows;  // valid rows of the tile
   int32_t n0;    // first result column
 };
 
-// Items of an expert of cnt rows, if this launch takes experts of that size.
+// Items of an expert of cnt rows (none for a decreasing pair of offsets).
 __device__ __forceinline__ int32_t fp8_items(const Fp8GemmArgs& p, int32_t cnt, int32_t bm) {
-  const bool take = cnt > 0 && cnt >= p.rows_lo && (p.rows_hi == 0 || cnt < p.rows_hi);
-  return take ? (cnt + bm - 1) / bm * p.n_tiles : 0;
+  return cnt > 0 ? (cnt + bm - 1) / bm * p.n_tiles : 0;
 }
 
-// Workgroups for at most all items of tiles of bm rows: every expert has at most one that is not
-// full.  Two axes, since one holds fewer than 2^32 threads; a multiple of 8 in all.
-inline dim3 fp8_grid(const Fp8GemmArgs& p, int64_t bm) {
+// At most so many items of tiles of bm rows: every expert has at most one that is not full.
+inline int64_t fp8_most_items(const Fp8GemmArgs& p, int64_t bm) {
   const int64_t most = p.offsets ? p.m_total / bm + (p.m_total < p.experts ? p.m_total : p.experts)
                                  : (p.m_total + bm - 1) / bm;
-  const int64_t blocks = most * p.n_tiles, row = 1 << 16;
-  if (blocks <= row) return dim3((unsigned)((blocks + 7) / 8 * 8));
-  return dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+  return most * p.n_tiles;
 }
 
-// Item of this workgroup among those of the grid (an upper bound of the items, a multiple of 8):
-// every thread counts the items of a run of experts and the one whose run holds the
-// workgroup's item names it.  Items are numbered so that an XCD (workgroup b runs on b % 8)
-// gets consecutive ones, which share weight tiles (M-tiles first) or activation rows.
-// band: M-tiles that are walked together with all N-tiles (0: all of them).
+// Finds a workgroup's items.  Every thread counts the items of a run of experts; the one whose run
+// holds an item names it.  In rounds of gridDim workgroups (a multiple of 8), items are numbered
+// so that an XCD (workgroup b runs on b % 8) gets consecutive ones, which share weight tiles
+// (M-tiles first) or activation rows.  band: M-tiles that are walked together with all N-tiles.
+// Every thread of the workgroup constructs it and calls batch (barriers inside).
 template <int NTHR>
-__device__ __forceinline__ Fp8Item fp8_locate(const Fp8GemmArgs& p, int32_t bm, int32_t bn, int32_t band) {
-  constexpr int WAVES = NTHR / 64;
-  __shared__ int32_t sums[WAVES], found[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int32_t m_total = (int32_t)p.m_total;
-  const int32_t block = blockIdx.y * gridDim.x + blockIdx.x, blocks = gridDim.x * gridDim.y;
-  Fp8Item it;
-  int32_t first, rows, local;
-  if (!p.offsets) {
-    const int32_t total = fp8_items(p, m_total, bm);
-    local = logical_block(block, blocks, total);
-    if (local >= total) return Fp8Item{-1, 0, 0, 0};
-    it.e = 0;
-    first = 0;
-    rows = m_total;
-  } else {
-    const int32_t E = p.experts;
-    const int32_t per = (E + NTHR - 1) / NTHR;
-    const int32_t lo = min(tid * per, E), hi = min(lo + per, E);
-    int32_t mine = 0;
-    int32_t at = lo < hi ? clamp_off(p.offsets[lo], m_total) : 0;
-    const int32_t start = at;
-    for (int32_t e = lo; e < hi; ++e) {
-      const int32_t next = clamp_off(p.offsets[e + 1], m_total);
-      mine += fp8_items(p, next - at, bm);
-      at = next;
-    }
-    int32_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int32_t t = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += t;
-    }
-    if (lane == 63) sums[wave] = incl;
-    __syncthreads();
-    int32_t base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      if (w < wave) base += sums[w];
-      total += sums[w];
-    }
-    const int32_t item = logical_block(block, blocks, total);
-    if (item >= total) return Fp8Item{-1, 0, 0, 0};
-    int32_t run = base + incl - mine;
-    if (item >= run && item < run + mine) {
-      at = start;
+struct Fp8Locator {
+  const Fp8GemmArgs& p;
+  const int32_t bm, bn, band;
+  int32_t lo, hi, run, own, start;  // this thread's experts, the items before and of them, first row
+  int32_t total, count;             // items of all workgroups, of this one
+  int32_t blocks, full, last, rounds;
+
+  __device__ __forceinline__ Fp8Locator(const Fp8GemmArgs& args, int32_t bm_, int32_t bn_, int32_t band_, int32_t* sums)
+      : p(args), bm(bm_), bn(bn_), band(band_) {
+    constexpr int WAVES = NTHR / 64;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t m_total = (int32_t)p.m_total;
+    lo = tid;
+    hi = tid == 0 ? 1 : tid;
+    start = run = 0;
+    own = total = fp8_items(p, m_total, bm);
+    if (p.offsets) {
+      const int32_t E = p.experts, per = (E + NTHR - 1) / NTHR;
+      lo = min(tid * per, E);
+      hi = min(lo + per, E);
+      own = 0;
+      int32_t at = lo < hi ? clamp_off(p.offsets[lo], m_total) : 0;
+      start = at;
       for (int32_t e = lo; e < hi; ++e) {
         const int32_t next = clamp_off(p.offsets[e + 1], m_total);
-        const int32_t n = fp8_items(p, next - at, bm);
-        if (item < run + n) {
-          found[0] = e;
-          found[1] = at;
-          found[2] = next - at;
-          found[3] = item - run;
-          break;
-        }
-        run += n;
+        own += fp8_items(p, next - at, bm);
         at = next;
       }
+      int32_t incl = own;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int32_t t = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += t;
+      }
+      if (lane == 63) sums[wave] = incl;
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        if (w < wave) run += sums[w];
+        total += sums[w];
+      }
+      run += incl - own;
+      total = uniform(total);
+    }
+    // (Two axes, since one holds fewer than 2^32 threads.)
+    const int32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+    blocks = gridDim.x * gridDim.y;
+    rounds = (total + blocks - 1) / blocks;
+    count = full = last = 0;
+    if (rounds > 0) {
+      const int32_t rest = total - (rounds - 1) * blocks;
+      full = logical_block(block, blocks, blocks);
+      last = logical_block(block, blocks, rest);
+      count = rounds - 1 + (last < rest ? 1 : 0);
+    }
+  }
+
+  // Items j0 .. j0 + n - 1 of this workgroup into ring[j % (2 n)].
+  __device__ __forceinline__ void batch(int32_t j0, int32_t n, Fp8Item* ring) const {
+    const int32_t m_total = (int32_t)p.m_total;
+    int32_t at = start, first = run;
+    int32_t j = j0;
+    for (int32_t e = lo; e < hi; ++e) {
+      const int32_t next = p.offsets ? clamp_off(p.offsets[e + 1], m_total) : m_total;
+      const int32_t rows = next - at, items = fp8_items(p, rows, bm);
+      for (; j < j0 + n && j < count; ++j) {
+        const int32_t item = j * blocks + (j == rounds - 1 ? last : full);
+        if (item >= first + items) break;
+        if (item < first) continue;
+        const int32_t local = item - first, mts = (rows + bm - 1) / bm;
+        int32_t mt, nt;
+        if (mts <= band) {
+          nt = local / mts;
+          mt = local - nt * mts;
+        } else {
+          const int32_t per_band = band * p.n_tiles, b = local / per_band, within = local - b * per_band;
+          const int32_t tall = min(band, mts - b * band);
+          nt = within / tall;
+          mt = b * band + within - nt * tall;
+        }
+        ring[j % (2 * n)] = Fp8Item{e, at + mt * bm, min(bm, rows - mt * bm), nt * bn};
+      }
+      first += items;
+      at = next;
     }
     __syncthreads();
-    it.e = uniform(found[0]);
-    first = uniform(found[1]);
-    rows = uniform(found[2]);
-    local = uniform(found[3]);
   }
-  const int32_t mts = (rows + bm - 1) / bm;
-  int32_t mt, nt;
-  if (band == 0 || mts <= band) {
-    nt = local / mts;
-    mt = local - nt * mts;
-  } else {
-    const int32_t per_band = band * p.n_tiles, b = local / per_band, within = local - b * per_band;
-    const int32_t tall = min(band, mts - b * band);
-    nt = within / tall;
-    mt = b * band + within - nt * tall;
-  }
-  it.row0 = first + mt * bm;
-  it.rows = min(bm, rows - mt * bm);
-  it.n0 = nt * bn;
-  return it;
-}
+};
 
 // The activation row that result row r reads.
 __device__ __forceinline__ int32_t fp8_source_row(const Fp8GemmArgs& p, int32_t r) {
@@ -200,24 +203,14 @@ __device__ __forceinline__ void fp8_store4(const Fp8GemmArgs& p, int64_t row, in
     if (col + i < p.n) store_as(p.out, at + i, v[i], p.out_dtype);
 }
 
-// Eight consecutive columns of a result row, of which those below n are stored.
-__device__ __forceinline__ void fp8_store8(const Fp8GemmArgs& p, int64_t row, int32_t col, const float4_t& lo,
-                                           const float4_t& hi) {
-  if (p.vec8 && col + 8 <= p.n && p.out_dtype != kFewOutF32) {
-    u32x4_t v;
-    if (p.out_dtype == kFewOutF16) {
-      v = __builtin_bit_cast(u32x4_t, half8_t{(_Float16)lo[0], (_Float16)lo[1], (_Float16)lo[2], (_Float16)lo[3],
-                                              (_Float16)hi[0], (_Float16)hi[1], (_Float16)hi[2], (_Float16)hi[3]});
-    } else {
-      typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-      v = __builtin_bit_cast(u32x4_t, bf16x8_t{(__bf16)lo[0], (__bf16)lo[1], (__bf16)lo[2], (__bf16)lo[3],
-                                               (__bf16)hi[0], (__bf16)hi[1], (__bf16)hi[2], (__bf16)hi[3]});
-    }
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.out) + row * p.ldo + col) = v;
-    return;
-  }
-  if (col < p.n) fp8_store4(p, row, col, lo);
-  if (col + 4 < p.n) fp8_store4(p, row, col + 4, hi);
+// Eight consecutive results as 16-bit values, rounded to nearest even.
+__device__ __forceinline__ u32x4_t fp8_round8(const float4_t& lo, const float4_t& hi, int32_t dtype) {
+  if (dtype == kFewOutF16)
+    return __builtin_bit_cast(u32x4_t, half8_t{(_Float16)lo[0], (_Float16)lo[1], (_Float16)lo[2], (_Float16)lo[3],
+                                               (_Float16)hi[0], (_Float16)hi[1], (_Float16)hi[2], (_Float16)hi[3]});
+  typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+  return __builtin_bit_cast(u32x4_t, bf16x8_t{(__bf16)lo[0], (__bf16)lo[1], (__bf16)lo[2], (__bf16)lo[3],
+                                              (__bf16)hi[0], (__bf16)hi[1], (__bf16)hi[2], (__bf16)hi[3]});
 }
 
 }  // namespace moe_fp4

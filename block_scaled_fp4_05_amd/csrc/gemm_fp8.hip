@@ -37,8 +37,12 @@ struct Stage {
 template <int NT, int MT, int W, int D>
 __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
   extern __shared__ __align__(16) char smem[];
-  const Fp8Item it = fp8_locate<W * 64>(p, 16 * MT, 16 * NT, 0);
-  if (it.e < 0) return;
+  __shared__ int32_t counts[W];
+  __shared__ Fp8Item place[2];
+  const Fp8Locator<W * 64> locator(p, 16 * MT, 16 * NT, INT32_MAX, counts);
+  if (locator.count == 0) return;
+  locator.batch(0, 1, place);
+  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0)};
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, kbs = p.k_blocks, n = p.n;
@@ -135,33 +139,30 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
 template <int NT, int MT, int W, int D>
 hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
   p.n_tiles = (p.n + 16 * NT - 1) / (16 * NT);
-  const dim3 grid = fp8_grid(p, 16 * MT);
-  hipLaunchKernelGGL((k_gemm_fp8_stream<NT, MT, W, D>), grid, dim3(W * 64), W * NT * MT * 1024, stream, p);
+  const unsigned grid = (unsigned)((fp8_most_items(p, 16 * MT) + 7) / 8 * 8);
+  hipLaunchKernelGGL((k_gemm_fp8_stream<NT, MT, W, D>), dim3(grid), dim3(W * 64), W * NT * MT * 1024, stream, p);
   return hipGetLastError();
-}
-
-hipError_t launch_stream(const Fp8GemmArgs& p, hipStream_t stream) {
-  const int64_t avg = p.m_total / p.experts;
-  if (avg <= 4) return launch<1, 1, 8, 3>(p, stream);
-  if (avg <= 16) return launch<4, 2, 8, 2>(p, stream);
-  return launch<4, 4, 4, 2>(p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& args, hipStream_t stream) {
-  Fp8GemmArgs p = args;
-  const int64_t avg = p.m_total / p.experts;
-  if (p.m_total <= kFp8TiledRows || avg < kFp8TiledRows / 2) return launch_stream(p, stream);
-  if (p.offsets && p.experts > 1) {
-    // Small experts, then large ones.
-    p.rows_hi = kFp8TiledRows;
-    const hipError_t err = launch_stream(p, stream);
-    if (err != hipSuccess) return err;
-    p.rows_lo = kFp8TiledRows;
-    p.rows_hi = 0;
-  }
-  return launch_gemm_fp8_tiled(p, stream);
+// The few-row kernel while a call has so few tiles of 32 x 128 that they would leave CUs
+// without work; its K split then keeps them loading.  256 experts of 512 x 6144, top-8, one token
+// (32 tiles): 10.9 us against 31 with tiles; four tokens (132): 24.8 against 32.5; eight (264): 45
+// against 36.5; dense 8192 x 6144, 64 rows (192): 28.8 against 30; 128 rows (320): 51 against 31.
+hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& p, hipStream_t stream) {
+  const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts;
+  const int64_t tiles = (p.m_total / 32 + experts) * ((p.n + 127) / 128);
+  if (tiles >= 224) return launch_gemm_fp8_tiled(p, stream);
+  // Up to 16, 32 or 64 rows of an expert read its weights once (dense 8192 x 6144, 32 rows: 20.6 us
+  // with room for 32, 23.1 for 64, 27 for 16; 64 rows: 28.8 with room for 64, 35 for 32).  Of 16
+  // rows, items of 16 weight rows while there is about one for a CU, else of 32 (dense
+  // 6144 x 6144, 16 rows: 16.5 us against 20; one token above: 14 against 10.9).
+  const int64_t rows = (p.m_total + p.experts - 1) / p.experts;
+  if (rows > 32) return launch<2, 4, 4, 2>(p, stream);
+  if (rows > 16) return launch<2, 2, 4, 2>(p, stream);
+  const int64_t items = (p.m_total / 16 + experts) * ((p.n + 15) / 16);
+  return items <= 320 ? launch<1, 1, 8, 3>(p, stream) : launch<2, 1, 8, 2>(p, stream);
 }
 
 }  // namespace moe_fp4

@@ -27,22 +27,56 @@ __device__ __forceinline__ int tile_row(int t, int i) { return 32 * (t >> 1) + 4
 __device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swz_w(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 
-template <int WN, int WM, int MT, bool EXACT>
+template <int WN, int WM, int MT, int R>
 struct Tile {
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
   static constexpr int BN = 128 * WN, BM = 16 * MT * WM;
   static constexpr int kRows = BN + BM;         // weight rows, then activation rows
   static constexpr int kStage = kRows * 128;    // bytes
   static constexpr int kRound = kThreads / 8;   // rows that all threads copy at once
-  static constexpr int kWRounds = BN / kRound, kARounds = BM / kRound;
+  static constexpr int kWRounds = BN / kRound, kARounds = BM / kRound, kCopies = kWRounds + kARounds;
+  // Weight tiles, and stages of activation tiles, in registers: reads run WD - 1 tiles ahead, which
+  // with few products a tile has to be more.
+  static constexpr int WD = MT >= 3 ? 2 : 4, AD = MT >= 3 ? 1 : 2;
+  static constexpr int kScales = BM > 64 * kWaves ? BM : 64 * kWaves;
   static_assert(BN % kRound == 0 && BM % kRound == 0, "whole rounds");
+  static_assert(R == 2 || R == 3, "stages in LDS");
 };
 
-// 16 bytes a lane from memory to LDS: lane l's to `to` + 16 l (uniform).
-__device__ __forceinline__ void copy16(rsrc_t rs, uint8_t* to, uint32_t off) {
-#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass knows neither this width nor the registers below)
+// 16 (or 4) bytes a lane from memory to LDS: lane l's to `to` + 16 l (4 l), `to` uniform.  In
+// assembly, because the compiler, which cannot tell the stages apart in a loop, otherwise waits
+// for copies of later stages before it reads an earlier one; all waits for copies are
+// stage_barrier's.  (The compiler sets M0 itself wherever it uses it.)  Five wait states: M0 before its use, and a scalar register that a vector
+// instruction may just have written.
+__device__ __forceinline__ void copy16(const u32x4_t& rs, uint8_t* to, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)  // (the host pass has no such registers)
   typedef uint8_t __attribute__((address_space(3))) lds_byte;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_byte*)to, 16, off, 0, 0, 0);
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_byte*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rs) : "memory");
+#endif
+}
+__device__ __forceinline__ void copy4(const u32x4_t& rs, float* to, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef float __attribute__((address_space(3))) lds_float;
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_float*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rs) : "memory");
+#endif
+}
+
+// A raw buffer resource as four words (make_rsrc's), in scalar registers whatever the compiler
+// makes of the arguments.
+__device__ __forceinline__ u32x4_t rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t at = (uint64_t)reinterpret_cast<uintptr_t>(base);
+  return u32x4_t{(uint32_t)uniform((int32_t)at), (uint32_t)uniform((int32_t)(at >> 32)) & 0xFFFFu, (uint32_t)uniform((int32_t)bytes),
+                 (uint32_t)kRawBufferWord3};
+}
+
+// Everything this wavefront has read from LDS is in registers and all but its newest N vector memory
+// operations are complete (they complete in order); then all wavefronts meet.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 #endif
 }
 
@@ -78,120 +112,154 @@ __device__ __forceinline__ void add_scaled(float4_t& acc, const float4_t& d, flo
 #endif
 }
 
-template <int WN, int WM, int MT, bool EXACT>
-__global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, 2)))
+template <int I>
+struct Index {
+  static constexpr int value = I;
+};
+
+template <int WN, int WM, int MT, int R, bool EXACT>
+__global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WM * WN > 2 ? 2 : 1, MT >= 3 ? 2 : 4)))
 void k_gemm_fp8_tiled(Fp8GemmArgs p) {
-  typedef Tile<WN, WM, MT, EXACT> T;
-  __shared__ __align__(1024) uint8_t stage0[T::kStage], stage1[T::kStage];
-  const Fp8Item it = fp8_locate<T::kThreads>(p, T::BM, T::BN, 4);
-  if (it.e < 0) return;
+  typedef Tile<WN, WM, MT, R> T;
+  constexpr int WD = T::WD, AD = T::AD;
+  __shared__ __align__(1024) uint8_t stages[R][T::kStage];
+  __shared__ __align__(1024) float scales[R][T::kScales];  // of the stages' activation rows
+  __shared__ Fp8Item place[2];
+  __shared__ int32_t sums[T::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int wn = wave % WN, wm = wave / WN;
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, kbs = p.k_blocks, n = p.n;
 
-  // What this thread copies: piece (lane % 8) of rows tid / 8 + kRound * j, swizzled.
+  const Fp8Locator<T::kThreads> locator(p, T::BM, T::BN, 4, sums);
+  if (locator.count == 0) return;
+  locator.batch(0, 1, place);
+  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0)};
+
+  // ---- copies: this thread moves piece lane % 8 of rows tid / 8 + kRound * j, swizzled, and
+  // wavefront w the scales of activation rows 64 w ...
+  // (swz_a has a period of 16 rows, swz_w of 32: with 16 rows a round, odd rounds differ.)
+  static_assert(T::kRound % 16 == 0, "rows of a round");
+  const int piece_a = (lane & 7) ^ swz_a(tid >> 3);
+  const int piece_w[2] = {(lane & 7) ^ swz_w(tid >> 3), (lane & 7) ^ swz_w((tid >> 3) + T::kRound)};
   const uint8_t* const w_base = p.w_q + (int64_t)it.e * n * k;
-  const uint32_t w_bytes = (uint32_t)n * (uint32_t)k;
-  const int64_t base = p.a_row_index ? 0 : it.row0;
-  const int64_t a_rows = p.a_row_index ? p.a_rows : it.rows;
-  const uint8_t* const a_base = p.a_q + base * k;
-  const uint32_t a_bytes = (uint32_t)(a_rows * k);
-  const int piece_w = (lane & 7) ^ swz_w(tid >> 3), piece_a = (lane & 7) ^ swz_a(tid >> 3);
-  uint32_t off[T::kWRounds + T::kARounds];
+  // Without a row index the tile's rows follow each other: offsets from its first row.
+  const int64_t base = p.a_row_index ? 0 : it.row0, a_rows = p.a_row_index ? p.a_rows : (int64_t)it.rows;
+  uint32_t off[T::kCopies], scale_off;
 #pragma unroll
   for (int j = 0; j < T::kWRounds; ++j) {
     const int32_t row = it.n0 + (tid >> 3) + T::kRound * j;
-    off[j] = (uint32_t)(row < n ? row : n - 1) * (uint32_t)k + 16u * piece_w;
+    off[j] = (uint32_t)(row < n ? row : n - 1) * (uint32_t)k + 16u * piece_w[j & 1];
   }
+  {
+    int32_t row[T::kARounds + 1];
 #pragma unroll
-  for (int j = 0; j < T::kARounds; ++j) {
-    const int32_t row = (tid >> 3) + T::kRound * j;
-    const int32_t src = fp8_source_row(p, it.row0 + (row < it.rows ? row : it.rows - 1)) - (int32_t)base;
-    off[T::kWRounds + j] = (uint32_t)src * (uint32_t)k + 16u * piece_a;
+    for (int j = 0; j < T::kARounds; ++j) row[j] = min((tid >> 3) + T::kRound * j, it.rows - 1);
+    row[T::kARounds] = min(tid, it.rows - 1);
+    if (p.a_row_index) {
+      const int32_t last = (int32_t)p.a_rows - 1;
+#pragma unroll
+      for (int j = 0; j <= T::kARounds; ++j) row[j] = p.a_row_index[it.row0 + row[j]];
+#pragma unroll
+      for (int j = 0; j <= T::kARounds; ++j) row[j] = min(max(row[j], 0), last);
+    }
+#pragma unroll
+    for (int j = 0; j < T::kARounds; ++j) off[T::kWRounds + j] = (uint32_t)row[j] * (uint32_t)k + 16u * piece_a;
+    scale_off = (uint32_t)row[T::kARounds] * (uint32_t)kbs * 4u;
   }
   // A piece past k (only the last block has any) is copied from the row's start instead: its
-  // products are made zero below, and a NaN there is in the result already.
-  // Behind the last block nothing is fetched (a resource of no bytes, without a branch).
-  auto copy = [&](uint8_t* stage, int32_t b, int j) {
-    const uint32_t kk = (uint32_t)b * 128;
-    const int piece = j < T::kWRounds ? piece_w : piece_a;
-    const uint32_t at = b * 128 + 16 * piece >= k ? 0u - 16u * piece : kk;
-    const bool in = b < kbs;
-    const rsrc_t rs = j < T::kWRounds ? make_rsrc(w_base, in ? w_bytes : 0u) : make_rsrc(a_base, in ? a_bytes : 0u);
-    copy16(rs, stage + (T::kRound * j + 8 * wave) * 128, off[j] + at);
-  };
-
-  // Scales: one weight scale a block, one activation scale a lane and 16 rows.
-  const int32_t nb = min(it.n0 / kFp8Block + wn, p.n_blocks - 1);
-  const float* w_sf = p.w_sf + ((int64_t)it.e * p.n_blocks + nb) * kbs;
-  const float* a_sf[MT];
+  // products are made zero below, and a NaN there is in the result already.  Behind the last
+  // block nothing is fetched (a resource of no bytes, without a branch).
+  const u32x4_t w_rs = rsrc_words(w_base, (uint32_t)n * (uint32_t)k);
+  const u32x4_t a_rs = rsrc_words(p.a_q + base * k, (uint32_t)(a_rows * k));
+  const u32x4_t s_rs = rsrc_words(p.a_sf + base * kbs, (uint32_t)(a_rows * kbs * 4));
+  const uint32_t last_at = (uint32_t)(kbs - 1) * 128u;
+  const uint32_t last_w[2] = {last_at + 16u * piece_w[0] >= (uint32_t)k ? 0u - 16u * piece_w[0] : last_at,
+                              last_at + 16u * piece_w[1] >= (uint32_t)k ? 0u - 16u * piece_w[1] : last_at};
+  const uint32_t last_a = last_at + 16u * piece_a >= (uint32_t)k ? 0u - 16u * piece_a : last_at;
+  auto within = [&](const u32x4_t& rs, int32_t b) { return u32x4_t{rs[0], rs[1], b < kbs ? rs[2] : 0u, rs[3]}; };
+  auto copy = [&](uint8_t* to, int32_t b, int from, int end) {
+    const u32x4_t w_now = within(w_rs, b), a_now = within(a_rs, b);
+    const uint32_t here = (uint32_t)b * 128u, at_a = b == kbs - 1 ? last_a : here;
+    const uint32_t at_w[2] = {b == kbs - 1 ? last_w[0] : here, b == kbs - 1 ? last_w[1] : here};
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int32_t row = 16 * (MT * wm + m) + r;
-    a_sf[m] = p.a_sf + (int64_t)fp8_source_row(p, it.row0 + (row < it.rows ? row : it.rows - 1)) * kbs;
-  }
+    for (int j = from; j < end; ++j)
+      copy16(j < T::kWRounds ? w_now : a_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + (j < T::kWRounds ? at_w[j & 1] : at_a));
+  };
+  auto copy_scales = [&](float* to, int32_t b) { copy4(within(s_rs, b), to + 64 * wave, scale_off + (uint32_t)b * 4u); };
 
+  // ---- products
+  const float* const w_sf = p.w_sf + ((int64_t)it.e * p.n_blocks + min(it.n0 / kFp8Block + wn, p.n_blocks - 1)) * kbs;
   float4_t acc[8][MT];
 #pragma unroll
   for (int t = 0; t < 8; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[t][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
   // Pieces g and 4 + g of this lane's row of a 16-row tile.
   const int at_w = tile_row(0, r) * 128 + 16 * (g ^ (r >> 1)), at_a = r * 128 + 16 * (g ^ (r >> 1));
-  auto fragment = [&](const uint8_t* stage, int row0, int at) {
-    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(stage + row0 * 128 + at);
-    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(stage + row0 * 128 + (at ^ 64));
+  auto fragment = [&](const uint8_t* from, int row0, int at) {
+    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(from + row0 * 128 + at);
+    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(from + row0 * 128 + (at ^ 64));
     return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
   typedef typename Operand<EXACT>::type operand_t;
-  i32x8_t a[MT], w[2];
-  float scale[MT], next[MT], next_w = ((sconst_f32)w_sf)[0];
+  i32x8_t a[AD][MT], w[WD];
   float4_t d[MT];
-  auto read_w = [&](const uint8_t* stage, int t) { w[t & 1] = fragment(stage, 128 * wn + tile_row(t, 0), at_w); };
-  auto read_a = [&](const uint8_t* stage, int m) { a[m] = fragment(stage, T::BN + 16 * (MT * wm + m), at_a); };
+  float next_w = ((sconst_f32)w_sf)[0];
+  auto read_w = [&](const uint8_t* from, int t) { w[t % WD] = fragment(from, 128 * wn + tile_row(t, 0), at_w); };
+  auto read_a = [&](const uint8_t* from, i32x8_t (&to)[MT], int m) { to[m] = fragment(from, T::BN + 16 * (MT * wm + m), at_a); };
 
-  // One stage, tile by tile: tile t's products are issued while tile t + 1 is read and tile t - 1
-  // is scaled and added; the copies of the next stage are spread over the first tiles.  The
-  // last two tiles wait in registers for the barrier: their products run while the next
-  // stage's first operands are read.  The fences keep the compiler from reading all tiles
-  // first, which spills.
-  constexpr int kCopies = T::kWRounds + T::kARounds, kPerTile = (kCopies + 1) / 2;
-  auto step = [&](uint8_t* cur, uint8_t* nxt, int32_t b) {
-    const bool more = b + 1 < kbs;
+  // One stage, tile by tile: a tile's products are issued while tiles ahead are read and the tile
+  // before it is scaled and added.  The last two tiles wait in registers for the barrier, behind
+  // which the stage's place is filled anew, R stages ahead, and the next stage's first operands
+  // are read while those tiles are multiplied.  The fences keep the compiler from reading all
+  // tiles first, which spills.
+  constexpr int kHalf = (T::kCopies + 1) / 2;
+  auto step = [&](auto which, int32_t b) {
+    constexpr int S = decltype(which)::value;
+    uint8_t *const cur = stages[S % R], *const nxt = stages[(S + 1) % R];
+    i32x8_t(&now_a)[MT] = a[S % AD];
+    i32x8_t(&next_a)[MT] = a[(S + 1) % AD];
     if (b == kbs - 1 && k % kFp8Block != 0) {
       const bool z0 = b * 128 + 16 * g >= k, z1 = b * 128 + 64 + 16 * g >= k;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (z0) a[m][i] = 0;
-          if (z1) a[m][4 + i] = 0;
+          if (z0) now_a[m][i] = 0;
+          if (z1) now_a[m][4 + i] = 0;
         }
     }
+    float scale[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) scale[m] = next[m] * next_w;
-    const int32_t ahead = more ? b + 1 : b;
-    next_w = ((sconst_f32)w_sf)[ahead];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) next[m] = a_sf[m][ahead];
+    for (int m = 0; m < MT; ++m) scale[m] = scales[S % R][16 * (MT * wm + m) + r] * next_w;
+    next_w = ((sconst_f32)w_sf)[b + 1 < kbs ? b + 1 : b];
     operand_t ao[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) ao[m] = Operand<EXACT>::of(a[m]);
+    for (int m = 0; m < MT; ++m) ao[m] = Operand<EXACT>::of(now_a[m]);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       __builtin_amdgcn_sched_barrier(0);
       if (t == 6) {
-        __syncthreads();  // the next stage is there, and this one is in registers
+        // Newer than the next stage's copies: those of R - 2 later stages.
+        stage_barrier<(R - 2) * (T::kCopies + 1)>();
         __builtin_amdgcn_sched_barrier(0);
-      }
-      const operand_t wo = Operand<EXACT>::of(w[t & 1]);
-      if (t < 6) read_w(cur, t + 1);  // (tile 7 below, where tile 5's registers are free)
-      if (t == 7) read_w(nxt, 0);
-      if (t >= 6) {
+        if constexpr (AD == 2) {
 #pragma unroll
-        for (int j = (t - 6) * kPerTile; j < (t - 5) * kPerTile && j < kCopies; ++j) copy(cur, b + 2, j);
+          for (int m = 0; m < MT; ++m) read_a(nxt, next_a, m);
+        }
+      }
+      const operand_t wo = Operand<EXACT>::of(w[t % WD]);
+      if (t + WD - 1 < (WD == 2 ? 7 : 8)) read_w(cur, t + WD - 1);  // (two buffers: tile 7 below)
+      if (t == 6) {
+#pragma unroll
+        for (int j = 0; j < WD - 2; ++j) read_w(nxt, j);
+      }
+      if (t == 7) read_w(nxt, WD - 2);
+      if (t == 6) copy(cur, b + R, 0, kHalf);
+      if (t == 7) {
+        copy(cur, b + R, kHalf, T::kCopies);
+        copy_scales(scales[S % R], b + R);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -199,12 +267,12 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
         const float4_t now = fp8_block_product(wo, ao[m]);
         if (t > 0) add_scaled(acc[t - 1][m], d[m], scale[m]);
         d[m] = now;
-        if (t == 7) {
+        if (AD == 1 && t == 7) {
           __builtin_amdgcn_sched_barrier(0);
-          read_a(nxt, m);
+          read_a(nxt, next_a, m);
         }
       }
-      if (t == 5) {
+      if (WD == 2 && t == 5) {  // where tile 5's registers are free
         __builtin_amdgcn_sched_barrier(0);
         read_w(cur, 7);
       }
@@ -216,45 +284,112 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   };
 
 #pragma unroll
-  for (int m = 0; m < MT; ++m) next[m] = a_sf[m][0];
-#pragma unroll
-  for (int j = 0; j < kCopies; ++j) copy(stage0, 0, j);
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kCopies; ++j) copy(stage1, 1, j);
-  read_w(stage0, 0);
-#pragma unroll
-  for (int m = 0; m < MT; ++m) read_a(stage0, m);
-  for (int32_t b = 0; b < kbs; b += 2) {
-    step(stage0, stage1, b);
-    if (b + 1 < kbs) step(stage1, stage0, b + 1);
+  for (int s = 0; s < R; ++s) {
+    copy(stages[s], s, 0, T::kCopies);
+    copy_scales(scales[s], s);
   }
-
+  stage_barrier<(R - 1) * (T::kCopies + 1)>();
+#pragma unroll
+  for (int m = 0; m < MT; ++m) read_a(stages[0], a[0], m);
+#pragma unroll
+  for (int t = 0; t < WD - 1; ++t) read_w(stages[0], t);
+  for (int32_t b = 0; b < kbs;) {
+    step(Index<0>{}, b);
+    if (++b == kbs) break;
+    step(Index<1>{}, b);
+    if (++b == kbs) break;
+    if constexpr (R == 3) {
+      step(Index<2>{}, b);
+      if (++b == kbs) break;
+      step(Index<3>{}, b);
+      if (++b == kbs) break;
+      step(Index<4>{}, b);
+      if (++b == kbs) break;
+      step(Index<5>{}, b);
+      ++b;
+    }
+  }
   // Nothing is on its way into LDS when the workgroup ends.
-  __syncthreads();
+  stage_barrier<0>();
+
+  // Where there is no row or column a store is sent out of range.
+  constexpr int es = EXACT ? 4 : 2;
+  const rsrc_t o = make_rsrc(static_cast<char*>(p.out) + (int64_t)it.row0 * p.ldo * es, (uint32_t)it.rows * (uint32_t)p.ldo * es);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int32_t row = 16 * (MT * wm + m) + r;
-    if (row >= it.rows) continue;
+    const uint32_t row_at = (uint32_t)row * (uint32_t)p.ldo;
 #pragma unroll
-    for (int t = 0; t < 8; t += 2)
-      fp8_store8(p, (int64_t)it.row0 + row, it.n0 + 128 * wn + tile_row(t, 4 * g), acc[t][m], acc[t + 1][m]);
+    for (int t = 0; t < 8; t += 2) {
+      const int32_t col = it.n0 + 128 * wn + tile_row(t, 4 * g);
+      const uint32_t to = row < it.rows && col < n ? (row_at + (uint32_t)col) * es : kOutOfRange;
+      const u32x4_t v = fp8_round8(acc[t][m], acc[t + 1][m], p.out_dtype);
+      if (p.store_cols == 8) {
+        if constexpr (EXACT) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][m]), o, to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t + 1][m]), o, to, 16, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128(v, o, to, 0, 0);
+        }
+      } else if (p.store_cols == 4) {
+        const uint32_t to_hi = col + 4 < n ? to + 4 * es : kOutOfRange;
+        if constexpr (EXACT) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][m]), o, to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t + 1][m]), o, to_hi, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{v[0], v[1]}, o, to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{v[2], v[3]}, o, to_hi, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t to_i = col + i < n ? to + i * es : kOutOfRange;
+          if constexpr (EXACT) {
+            const float f = i < 4 ? acc[t][m][i & 3] : acc[t + 1][m][i & 3];
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f), o, to_i, 0, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[i >> 1] >> (16 * (i & 1))), o, to_i, 0, 0);
+          }
+        }
+      }
+    }
   }
 }
 
-template <int WN, int WM, int MT, bool EXACT>
+template <int WN, int WM, int MT, int R, bool EXACT>
 hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
-  typedef Tile<WN, WM, MT, EXACT> T;
+  typedef Tile<WN, WM, MT, R> T;
   p.n_tiles = (p.n + T::BN - 1) / T::BN;
-  hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, EXACT>), fp8_grid(p, T::BM), dim3(T::kThreads), 0, stream, p);
+  // Columns that can be stored together everywhere: 8 (16-bit results) or 4 of them in one piece.
+  const uint64_t es = EXACT ? 4 : 2, where = reinterpret_cast<uintptr_t>(p.out) | (uint64_t)p.ldo * es;
+  p.store_cols = where % 16 == 0 && p.n % 8 == 0 ? 8 : where % (4 * es) == 0 && p.n % 4 == 0 ? 4 : 1;
+  const int64_t items = (fp8_most_items(p, T::BM) + 7) / 8 * 8, row = 1 << 16;
+  const dim3 grid = items <= row ? dim3((unsigned)items) : dim3((unsigned)row, (unsigned)((items + row - 1) / row));
+  hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, R, EXACT>), grid, dim3(T::kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
+// The tile by the average rows of an expert; both sides measured in us:
+//   32 x 128 below 8 rows, three stages deep (256 experts of 512 x 6144, top-8, 16 tokens: 58,
+//     against 68 with 64 x 128);
+//   64 x 128 below 96 rows (the down projection, 6144 x 256, 32 rows: 136 against 176 with 128 x
+//     128), and while 128 x 128 would leave CUs without two workgroups (dense 8192 x 6144, 256
+//     rows: 33 against 39);
+//   256 x 256 from 384 rows (8 experts of 8192 x 4096, 512 rows: 208 against 223 with 128 x 128;
+//     1024 rows: 342 against 414; 64 experts of 2048 x 4096, 256 rows: 260 against 253) where they
+//     fill most of a round of 256 CUs (dense 8192^2, 2048 rows: 134 against 179; 8192 x 4096, 2500
+//     rows, 320 tiles: 123 against 106);
+//   128 x 128 else (4096 tokens of 256 experts: 269 against 276 with 64 x 128).
 template <bool EXACT>
 hipError_t launch_sized(const Fp8GemmArgs& p, hipStream_t stream) {
-  const int64_t tiles = p.m_total * p.n / (256 * 256), avg = p.m_total / p.experts;
-  if (tiles >= 192 && avg >= 192) return launch<2, 4, EXACT ? 2 : 4, EXACT>(p, stream);
-  return launch<1, 4, 2, EXACT>(p, stream);
+  const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts, avg = p.m_total / p.experts;
+  if (avg < 8) return launch<1, 2, 1, 3, EXACT>(p, stream);
+  const int64_t m2 = (p.m_total / 128 + experts) * ((p.n + 127) / 128);
+  if (avg < 96 || m2 < 512) return launch<1, 4, 1, 2, EXACT>(p, stream);
+  const int64_t big = (p.m_total + 255) / 256 * ((p.n + 255) / 256), rest = big % 256;
+  if (!EXACT && avg >= 384 && big >= 224 && (rest == 0 || rest >= 160 || big >= 1024))
+    return launch<2, 4, 4, 2, false>(p, stream);
+  return launch<1, 4, 2, 2, EXACT>(p, stream);
 }
 
 }  // namespace

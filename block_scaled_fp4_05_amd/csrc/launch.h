@@ -285,15 +285,12 @@ struct Fp8GemmArgs {
   void* out;
   int64_t ldo;
   int32_t out_dtype;  // MOE_FP4_OUT_*
-  int32_t vec4, vec8;  // four and eight consecutive columns may be stored together
-  // Set by the launchers: N-tiles of an expert, and the experts' rows this launch takes.
-  int32_t n_tiles = 0, rows_lo = 0, rows_hi = 0;
+  int32_t vec4;       // four consecutive columns may be stored together
+  // Set by the launchers: N-tiles of an expert, and the columns that are stored together.
+  int32_t n_tiles = 0, store_cols = 1;
 };
 hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& args, hipStream_t stream);
-// Workgroup tiles, for experts of p.rows_lo rows or more.
 hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& p, hipStream_t stream);
-// Rows from which an expert takes them.
-constexpr int32_t kFp8TiledRows = 64;
 
 // Token rows in expert order and back (rows.hip): out's rows are mapped onto x's.
 struct RowsArgs {

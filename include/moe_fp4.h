@@ -558,8 +558,8 @@ int moe_fp8_quantize_weights(const void* w, int in_dtype, int32_t num_experts, i
  *                  element, ldo >= n (stores are widest with 16-byte aligned rows).
  * Errors: NULL, SHAPE (num_experts, n or k < 1, m_total < 0, ldo < n, too few a_rows), ALIGN, ARG
  * (out_dtype, out overlapping an operand), UNSUPPORTED (k % 16, k > 2^22, num_experts > 8192,
- * n * k >= 2^31 - 4096, a_rows * k too with a row index, m_total above about 2^29, or (m_total / 16
- * + E) * n / 16 above 2^31), HIP.
+ * n * k >= 2^31 - 4096, a_rows * k too with a row index, ldo > 2^20, m_total above about 2^29, or
+ * (m_total / 16 + E) * n / 16 above 2^31), HIP.
  */
 int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
                          const int32_t* a_row_index, const uint8_t* w_q, const float* w_sf,

@@ -123,6 +123,57 @@ def test_large_dense():
     ref.check(out, *expected(a, sa, w, sw, [0, 1100], eight_bit=True), "large dense bf16")
 
 
+def sampled(rows, n, seed):
+    """Some result rows and columns, the first and last ones among them."""
+    rng = np.random.default_rng(seed)
+    pick = lambda size: np.unique(np.concatenate((rng.integers(0, size, 150), [0, 1, size - 2, size - 1])))  # noqa: E731
+    return pick(rows), pick(n)
+
+
+def check_sampled(out, a, sa, w, sw, offsets, eight_bit, seed):
+    rows, cols = sampled(out.shape[0], out.shape[1], seed)
+    y = torch.zeros(len(rows), len(cols), dtype=torch.float64)
+    b = torch.zeros_like(y)
+    for e in range(w.shape[0]):
+        at = np.nonzero((rows >= offsets[e]) & (rows < offsets[e + 1]))[0]
+        if len(at):
+            wv = ref.values(w[e], sw[e], 128)[cols]
+            y[at], b[at] = ref.product(ref.values(a[rows[at]], sa[rows[at]], 1), wv, eight_bit)
+    ref.check(out.cpu()[rows][:, cols], y, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,n,k", [(3580, 4000, 400), (2050, 7304, 1168), (400, 16380, 272)])
+def test_many_tiles_dense(rows, n, k, dtype):
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"linear_fp8 {rows} x {n} x {k} {dtype}")
+    a, sa, w, sw = operands(rows, rows, 1, n, k)
+    aq, asf, wq, wsf = on_gpu(a, sa, w, sw)
+    out = m.linear_fp8(aq, asf, wq[0], wsf[0], out_dtype=ref.DT[dtype])
+    check_sampled(out, a, sa, w, sw, [0, rows], dtype != "fp32", rows)
+    assert torch.equal(out, m.linear_fp8(aq, asf, wq[0], wsf[0], out_dtype=ref.DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "fp32"])
+@pytest.mark.parametrize("E,avg,n,k", [(40, 130, 900, 272), (6, 420, 2600, 144), (64, 12, 2048, 528), (96, 3, 520, 1040)])
+def test_many_tiles_of_many_experts(E, avg, n, k, dtype):
+    """Uneven experts, some empty, rows gathered through an index."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"grouped_gemm_fp8 {E} experts of {avg} rows, {n} x {k} {dtype}")
+    rng = np.random.default_rng(E)
+    counts = rng.multinomial(E * avg, rng.dirichlet(np.full(E, 3.0)))
+    counts[E // 2] = 0
+    offsets = np.concatenate(([0], np.cumsum(counts)))
+    M, T = int(offsets[-1]), 333
+    a, sa, w, sw = operands(E, T, E, n, k)
+    sa, sw = sa * np.float32(2.0 ** -6), sw * np.float32(2.0 ** -6)
+    index = rng.integers(0, T, M)
+    out = m.grouped_gemm_fp8(*on_gpu(a, sa, w, sw), i32(offsets), a_row_index=i32(index), out_dtype=ref.DT[dtype])
+    check_sampled(out, a[index], sa[index], w, sw, offsets, dtype != "fp32", E)
+
+
 def test_many_experts():
     require_gpu()
     from block_scaled_fp4_05_amd import moe_fp4 as m
