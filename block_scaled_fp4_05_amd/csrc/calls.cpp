@@ -1,7 +1,7 @@
-// Short host path of the Python binding's few-token calls (a CPython extension module;
-// no device code).
+// Short host path of the Python binding's few-token, FP8 and gradient calls (a CPython extension
+// module; no device code).
 //
-// These calls run a few microseconds on the GPU, and checking a dozen tensors and
+// These calls can run a few microseconds on the GPU, and checking a dozen tensors and
 // allocating the results from Python takes longer than that.  Each function here does
 // for plain torch.Tensor arguments what its namesake in moe_fp4.py does: the same
 // checks, the same allocations, the same call of the C entry point.  Where anything is
@@ -24,6 +24,12 @@ decltype(&moe_fp4_ffn) g_ffn;
 decltype(&moe_fp4_ffn_workspace_size) g_ffn_workspace;
 decltype(&moe_fp4_route) g_route;
 decltype(&moe_fp4_route_workspace_size) g_route_workspace;
+decltype(&moe_fp8_quantize) g_quantize_fp8;
+decltype(&moe_grouped_gemm_fp8) g_gemm_fp8;
+decltype(&moe_fp4_dispatch) g_dispatch;
+decltype(&moe_fp4_dispatch_backward) g_dispatch_backward;
+decltype(&moe_fp4_combine_backward) g_combine_backward;
+decltype(&moe_fp4_route_backward) g_route_backward;
 
 // What makes a call leave for the Python code.
 struct Leave {};
@@ -156,12 +162,13 @@ PyObject* guarded(F&& f) {
 }
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind: five addresses");
+  constexpr int kEntries = 11;
+  if (n != kEntries) {
+    PyErr_SetString(PyExc_TypeError, "bind: eleven addresses");
     return nullptr;
   }
-  uintptr_t p[5];
-  for (int i = 0; i < 5; ++i) {
+  uintptr_t p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -170,6 +177,12 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_ffn_workspace = reinterpret_cast<decltype(g_ffn_workspace)>(p[2]);
   g_route = reinterpret_cast<decltype(g_route)>(p[3]);
   g_route_workspace = reinterpret_cast<decltype(g_route_workspace)>(p[4]);
+  g_quantize_fp8 = reinterpret_cast<decltype(g_quantize_fp8)>(p[5]);
+  g_gemm_fp8 = reinterpret_cast<decltype(g_gemm_fp8)>(p[6]);
+  g_dispatch = reinterpret_cast<decltype(g_dispatch)>(p[7]);
+  g_dispatch_backward = reinterpret_cast<decltype(g_dispatch_backward)>(p[8]);
+  g_combine_backward = reinterpret_cast<decltype(g_combine_backward)>(p[9]);
+  g_route_backward = reinterpret_cast<decltype(g_route_backward)>(p[10]);
   Py_RETURN_NONE;
 }
 
@@ -296,7 +309,218 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// A matrix of one of the router's input types, with its pitch.
+struct Matrix {
+  const at::Tensor& t;
+  int64_t rows, cols, ld;
+  int dtype;
+  Matrix(PyObject* o, Device& dev, bool fp8 = false) : t(tensor(o)) {
+    need(t.dim() == 2);
+    rows = t.size(0);
+    cols = t.size(1);
+    dtype = fp8 && t.scalar_type() == at::kFloat8_e4m3fn ? MOE_FP4_IN_FP8 : in_code(t.scalar_type());
+    dev.add(t);
+    ld = pitch(t, rows, cols);
+  }
+};
+
+const int32_t* ints(void* p) { return static_cast<const int32_t*>(p); }
+
+PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
+  PyObject* out = PyTuple_New(2);
+  if (!out) return nullptr;
+  const at::Tensor* parts[] = {&a, &b};
+  for (int i = 0; i < 2; ++i) {
+    PyObject* t = THPVariable_Wrap(*parts[i]);
+    if (!t) return Py_DECREF(out), nullptr;
+    PyTuple_SET_ITEM(out, i, t);
+  }
+  return out;
+}
+
+// quantize_fp8(x, swiglu, grad, power_of_two, device, stream): new outputs
+PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 6 && g_quantize_fp8);
+    Device dev;
+    const Matrix x(a[0], dev);
+    const int swiglu = PyObject_IsTrue(a[1]), pow2 = PyObject_IsTrue(a[3]);
+    need(swiglu >= 0 && pow2 >= 0 && !(swiglu && x.cols % 2 != 0));
+    const int64_t k = swiglu ? x.cols / 2 : x.cols;
+    const void* grad = nullptr;
+    int64_t ld_grad = 0;
+    if (a[2] != Py_None) {
+      const Matrix g(a[2], dev);
+      need(swiglu && g.dtype == x.dtype && g.rows == x.rows && g.cols == k);
+      grad = g.t.data_ptr();
+      ld_grad = g.ld;
+    }
+    void* stream = stream_on(a[4], a[5], dev);
+    const int64_t cols = grad ? x.cols : k;
+    const at::Tensor q = at::empty({x.rows, cols}, x.t.options().dtype(at::kFloat8_e4m3fn));
+    const at::Tensor sf = at::empty({x.rows, blocks(cols)}, x.t.options().dtype(at::kFloat));
+    const int status = unlocked([&] {
+      return g_quantize_fp8(x.t.data_ptr(), x.dtype, x.rows, k, x.ld, swiglu, grad, ld_grad, pow2,
+                            static_cast<uint8_t*>(q.data_ptr()), static_cast<float*>(sf.data_ptr()), stream);
+    });
+    need(status == MOE_FP4_OK);
+    return pair(q, sf);
+  });
+}
+
+// gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index, out_type, device, stream): a new output;
+// offsets None: one expert, w_q [n][k]
+PyObject* gemm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 9 && g_gemm_fp8);
+    const at::Tensor &x = tensor(a[0]), &w = tensor(a[2]);
+    const bool dense = a[4] == Py_None;
+    need(x.dim() == 2 && w.dim() == (dense ? 2 : 3));
+    const int64_t rows = x.size(0), k = x.size(1), E = dense ? 1 : w.size(0), N = w.size(dense ? 0 : 1);
+    need(E <= INT32_MAX);
+    Device dev;
+    const void* xq = exact(a[0], at::kFloat8_e4m3fn, {rows, k}, dev);
+    const void* xs = exact(a[1], at::kFloat, {rows, blocks(k)}, dev);
+    const void *wq, *ws, *off = nullptr, *index = nullptr;
+    if (dense) {
+      wq = exact(a[2], at::kFloat8_e4m3fn, {N, k}, dev);
+      ws = exact(a[3], at::kFloat, {blocks(N), blocks(k)}, dev);
+    } else {
+      wq = exact(a[2], at::kFloat8_e4m3fn, {E, N, k}, dev);
+      ws = exact(a[3], at::kFloat, {E, blocks(N), blocks(k)}, dev);
+      off = exact(a[4], at::kInt, {E + 1}, dev);
+    }
+    int64_t m = rows;
+    if (a[5] != Py_None) {
+      m = tensor(a[5]).numel();
+      index = exact(a[5], at::kInt, {m}, dev);
+    }
+    const int64_t type = integer(a[6]);
+    need(type >= 0 && type < 3);
+    void* stream = stream_on(a[7], a[8], dev);
+    const at::ScalarType types[] = {at::kBFloat16, at::kFloat, at::kHalf};
+    const at::Tensor out = at::empty({m, N}, x.options().dtype(types[type]));
+    const int status = unlocked([&] {
+      return g_gemm_fp8(static_cast<const uint8_t*>(xq), static_cast<const float*>(xs), rows,
+                        static_cast<const int32_t*>(index), static_cast<const uint8_t*>(wq),
+                        static_cast<const float*>(ws), static_cast<const int32_t*>(off), (int32_t)E, m, N, k,
+                        out.data_ptr(), (int)type, N, stream);
+    });
+    need(status == MOE_FP4_OK);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// dispatch(x, row_token, device, stream): a new output
+PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 4 && g_dispatch);
+    Device dev;
+    const Matrix x(a[0], dev, true);
+    const int64_t m = tensor(a[1]).numel();
+    void* map = exact(a[1], at::kInt, {m}, dev);
+    void* stream = stream_on(a[2], a[3], dev);
+    const at::Tensor out = at::empty({m, x.cols}, x.t.options());
+    const int status = unlocked([&] {
+      return g_dispatch(x.t.data_ptr(), x.dtype, x.rows, x.cols, x.ld, ints(map), m, out.data_ptr(), x.cols, stream);
+    });
+    need(status == MOE_FP4_OK);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// dispatch_backward(dy, token_rows, device, stream): a new output
+PyObject* dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 4 && g_dispatch_backward);
+    Device dev;
+    const Matrix y(a[0], dev);
+    const at::Tensor& rows = tensor(a[1]);
+    need(rows.dim() == 2);
+    const int64_t T = rows.size(0), K = rows.size(1);
+    need(K >= 1 && K <= INT32_MAX);
+    void* map = exact(a[1], at::kInt, {T, K}, dev);
+    void* stream = stream_on(a[2], a[3], dev);
+    const at::Tensor out = at::empty({T, y.cols}, y.t.options());
+    const int status = unlocked([&] {
+      return g_dispatch_backward(y.t.data_ptr(), y.dtype, y.rows, y.cols, y.ld, ints(map), (int32_t)K, T,
+                                 out.data_ptr(), y.cols, stream);
+    });
+    need(status == MOE_FP4_OK);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// combine_backward(dout, rows, token_rows, token_weights, row_token, device, stream): new outputs
+PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 7 && g_combine_backward);
+    Device dev;
+    const Matrix g(a[0], dev), r(a[1], dev);
+    need(g.dtype != MOE_FP4_IN_FP16 && r.dtype == MOE_FP4_IN_BF16 && r.cols == g.cols);
+    const at::Tensor& map = tensor(a[2]);
+    need(map.dim() == 2 && map.size(0) == g.rows);
+    const int64_t K = map.size(1);
+    need(K >= 1 && K <= INT32_MAX);
+    void* rows = exact(a[2], at::kInt, {g.rows, K}, dev);
+    const void* weights = exact(a[3], at::kFloat, {g.rows, K}, dev);
+    void* row_token = exact(a[4], at::kInt, {r.rows}, dev);
+    void* stream = stream_on(a[5], a[6], dev);
+    const at::Tensor drows = at::empty({r.rows, r.cols}, r.t.options());
+    const at::Tensor dweights = at::empty({g.rows, K}, g.t.options().dtype(at::kFloat));
+    const int status = unlocked([&] {
+      return g_combine_backward(g.t.data_ptr(), g.dtype == MOE_FP4_IN_FP32 ? MOE_FP4_OUT_FP32 : MOE_FP4_OUT_BF16,
+                                g.rows, g.cols, g.ld, static_cast<const uint16_t*>(r.t.data_ptr()), r.ld, r.rows,
+                                ints(rows), static_cast<const float*>(weights), (int32_t)K, ints(row_token),
+                                static_cast<uint16_t*>(drows.data_ptr()), r.cols,
+                                static_cast<float*>(dweights.data_ptr()), stream);
+    });
+    need(status == MOE_FP4_OK);
+    return pair(drows, dweights);
+  });
+}
+
+// route_backward(logits, ids, dweights, score, renormalize, device, stream): a new output
+PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 7 && g_route_backward);
+    Device dev;
+    const Matrix x(a[0], dev);
+    const at::Tensor& idt = tensor(a[1]);
+    need(idt.dim() == 2 && idt.size(0) == x.rows && x.cols <= INT32_MAX);
+    const int64_t K = idt.size(1);
+    need(K >= 1 && K <= INT32_MAX);
+    void* ids = exact(a[1], at::kInt, {x.rows, K}, dev);
+    const void* d = exact(a[2], at::kFloat, {x.rows, K}, dev);
+    const int64_t score = integer(a[3]);
+    const int renormalize = PyObject_IsTrue(a[4]);
+    need(renormalize >= 0);
+    void* stream = stream_on(a[5], a[6], dev);
+    const at::Tensor out = at::empty({x.rows, x.cols}, x.t.options());
+    const int status = unlocked([&] {
+      return g_route_backward(x.t.data_ptr(), x.dtype, x.rows, (int32_t)x.cols, x.ld, ints(ids),
+                              static_cast<const float*>(d), (int32_t)K, (int)score, renormalize, out.data_ptr(),
+                              x.cols, stream);
+    });
+    need(status == MOE_FP4_OK);
+    return THPVariable_Wrap(out);
+  });
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction method() {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F));
+}
+
 PyMethodDef kMethods[] = {
+    {"quantize_fp8", method<quantize_fp8>(), METH_FASTCALL, nullptr},
+    {"gemm_fp8", method<gemm_fp8>(), METH_FASTCALL, nullptr},
+    {"dispatch", method<dispatch>(), METH_FASTCALL, nullptr},
+    {"dispatch_backward", method<dispatch_backward>(), METH_FASTCALL, nullptr},
+    {"combine_backward", method<combine_backward>(), METH_FASTCALL, nullptr},
+    {"route_backward", method<route_backward>(), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
     {"ffn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(ffn)), METH_FASTCALL, nullptr},

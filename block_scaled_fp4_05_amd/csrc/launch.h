@@ -336,8 +336,7 @@ struct RouteBackwardArgs {
   void* dlogits;          // [tokens][ld_out] of dtype
   int64_t ld_out, tokens;
   int32_t experts, topk, dtype, sigmoid, renormalize;
-  // Set by the launcher: lanes of a token's slots, tokens of a wavefront.
-  int32_t slot_lanes = 0, group_tokens = 0;
+  int32_t wide = 0;  // set by the launcher: rows can be read and written in 16-byte pieces
 };
 hipError_t launch_route_backward(const RouteBackwardArgs& args, hipStream_t stream);
 

@@ -50,7 +50,9 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
   return m;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 1 / (1 + e^-x) with the reciprocal instruction (a step of its own, where a division would round
+// once; the instructions of two divisions an element bound the SwiGLU modes).
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + expf(-x)); }
 
 enum { kPlain = 0, kSwiglu = 1, kSwigluGrad = 2 };
 
@@ -70,14 +72,14 @@ __device__ __forceinline__ void values8(const Fp8QuantArgs& a, int64_t row, int3
   if (MODE == kSwiglu) {
     load8<DT>(a.x, row * a.ld_x + half + h, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = silu(g[i]) * u[i];
+    for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
     return;
   }
   float d[8];
   load8<DT>(a.grad, row * a.ld_grad + h, d);
   if (up_half) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = d[i] * silu(g[i]);
+    for (int i = 0; i < 8; ++i) v[i] = d[i] * (g[i] * sigmoid(g[i]));
   } else {
     load8<DT>(a.x, row * a.ld_x + half + h, u);
 #pragma unroll
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void k_quantize_fp8_weights(Fp8WeightArgs
 
 template <int DT, int MODE>
 hipError_t rows(const Fp8QuantArgs& a, hipStream_t stream) {
-  constexpr int B = MODE == kSwigluGrad ? 1 : DT == kInF32 ? 2 : 4;
+  constexpr int B = MODE == kSwigluGrad || DT == kInF32 ? 2 : 4;
   constexpr uint32_t per_group = kThreads / 16 * B;
   const uint32_t grid = (a.blocks + per_group - 1) / per_group;
   hipLaunchKernelGGL((k_quantize_fp8<DT, MODE, B>), dim3(grid), dim3(kThreads), 0, stream, a);

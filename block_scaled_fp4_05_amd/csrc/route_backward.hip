@@ -10,12 +10,16 @@
 // complement the same of -x, so neither loses its small end, and the quotients of w are
 // taken with the largest e^min(x,0) divided out, so that tiny scores keep their proportions.
 //
-// A wavefront takes G tokens: first its lanes are (token, slot) pairs, which compute the
-// slots' terms; then all 64 lanes write each token's row of the dense result, every element
-// once, adding the slots that name its expert in slot order.  Bound: the logits (softmax only)
-// and the result, 2 to 8 bytes an expert, and for short calls the launch.
+// A token takes 16 lanes (up to 256 experts and 16 slots) or 64, each with 16 consecutive
+// experts.  Its first lanes are its slots, which compute the slots' terms; then every lane adds
+// the terms that name its experts, in slot order, so each element of the dense result is written
+// once.  Four tokens a wavefront share every instruction, and a reduction over 16 lanes needs no
+// LDS.  Bound: the logits (softmax only) and the result, 2 to 8 bytes an expert, and for short
+// calls the launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "few_token_device.h"
 #include "gemm_common.h"
@@ -25,136 +29,165 @@ namespace moe_fp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
-constexpr int kPerLane = 16;  // experts of a lane: 1024 / 64
+constexpr int kPer = 16;  // experts of a lane
 
-__device__ __forceinline__ float load_in(const void* p, int64_t i, int32_t dtype) {
-  if (dtype == kInF32) return static_cast<const float*>(p)[i];
-  if (dtype == kInF16) return (float)static_cast<const _Float16*>(p)[i];
-  return (float)static_cast<const __bf16*>(p)[i];
+// 16 consecutive elements, whole (from a 16-byte aligned address) or those below `have`.
+template <typename T>
+__device__ __forceinline__ void load16(const void* p, int64_t at, int32_t have, bool wide, float (&v)[kPer]) {
+  constexpr int N = 16 / sizeof(T);
+  typedef T vec_t __attribute__((ext_vector_type(N)));
+  const T* q = static_cast<const T*>(p) + at;
+  if (wide && have >= kPer) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += N) {
+      const vec_t x = *reinterpret_cast<const vec_t*>(q + i);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i + j] = (float)x[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = i < have ? (float)q[i] : -INFINITY;
+  }
 }
 
-__device__ __forceinline__ void store_in(void* p, int64_t i, float v, int32_t dtype) {
-  if (dtype == kInF32) static_cast<float*>(p)[i] = v;
-  else if (dtype == kInF16) static_cast<_Float16*>(p)[i] = (_Float16)v;
-  else static_cast<__bf16*>(p)[i] = (__bf16)v;
+template <typename T>
+__device__ __forceinline__ void store16(void* p, int64_t at, int32_t have, bool wide, const float (&v)[kPer]) {
+  constexpr int N = 16 / sizeof(T);
+  typedef T vec_t __attribute__((ext_vector_type(N)));
+  T* q = static_cast<T*>(p) + at;
+  if (wide && have >= kPer) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += N) {
+      vec_t x;
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = (T)v[i + j];
+      *reinterpret_cast<vec_t*>(q + i) = x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < have) q[i] = (T)v[i];
+  }
 }
 
-template <typename F>
-__device__ __forceinline__ float reduce(float v, int width, F f) {
-  for (int d = 1; d < width; d <<= 1) v = f(v, __shfl_xor(v, d, 64));
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+// The larger one, or NaN if one is.
+__device__ __forceinline__ float larger(float a, float b) { return a != a ? a : (b != b || b > a) ? b : a; }
+
+// Over the L lanes of a token, the same bits in each: rotations within 16 lanes give every lane
+// the same pairs in some order, and a sum or maximum of two does not depend on theirs.
+template <int L, typename F>
+__device__ __forceinline__ float reduce(float v, F f) {
+  auto turned = [](float x, auto n) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + decltype(n)::value, 0xf, 0xf, false));
+  };
+  v = f(v, turned(v, std::integral_constant<int, 8>{}));  // row_ror
+  v = f(v, turned(v, std::integral_constant<int, 4>{}));
+  v = f(v, turned(v, std::integral_constant<int, 2>{}));
+  v = f(v, turned(v, std::integral_constant<int, 1>{}));
+  if constexpr (L == 64) {
+    v = f(v, __shfl_xor(v, 16, 64));
+    v = f(v, __shfl_xor(v, 32, 64));
+  }
   return v;
 }
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
-// The larger one, or NaN if one is.
-__device__ __forceinline__ float larger_nan(float a, float b) { return a != a ? a : (b != b || b > a) ? b : a; }
 
+template <int L, typename T, bool DENSE>
 __global__ __launch_bounds__(kThreads) void k_route_backward(RouteBackwardArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int width = a.slot_lanes;  // lanes of one token in the first part, a power of two
-  const int64_t group = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6);
-  const int64_t t0 = group * a.group_tokens;
-  if (t0 >= a.tokens) return;
-  const bool dense = a.sigmoid == 0 && a.renormalize == 0;
+  const int lane = threadIdx.x & 63, me = lane & (L - 1);
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  const bool here = t < a.tokens;
+  const int64_t row = here ? t : 0;
+  const int32_t first = kPer * me, have = here ? a.experts - first : 0;
+  float x[kPer];
+  if (DENSE) load16<T>(a.logits, row * a.ld + first, have, a.wide != 0, x);
 
-  // (token, slot) pairs.
-  const int64_t t = t0 + lane / width;
-  const int s = lane & (width - 1);
-  const bool pair = lane / width < a.group_tokens && t < a.tokens && s < a.topk;
-  const int32_t e = pair ? a.ids[t * a.topk + s] : -1;
+  // Lane `me` of a token is its slot `me`.
+  const int32_t e = here && me < a.topk ? a.ids[row * a.topk + me] : -1;
   const bool valid = e >= 0 && e < a.experts;
-  const float d = valid ? a.dweights[t * a.topk + s] : 0.0f;
+  const float d = valid ? a.dweights[row * a.topk + me] : 0.0f;
   float term = d;
-  if (!dense) {
-    const float x = valid ? load_in(a.logits, t * a.ld + e, a.dtype) : -INFINITY;
+  if (!DENSE) {
+    const float l = valid ? (float)static_cast<const T*>(a.logits)[row * a.ld + e] : -INFINITY;
     if (a.sigmoid) {
-      const float low = fminf(x, 0.0f), left = expf(fminf(-x, 0.0f)) / (1.0f + expf(-fabsf(x)));
+      const float low = fminf(l, 0.0f), small = expf(-fabsf(l)), whole = 1.0f + small;
+      // 1 - p = e^min(-x,0) / (1 + e^-|x|): one of the two exponents is 0.
+      const float left = (l > 0.0f ? small : 1.0f) / whole;
       if (a.renormalize) {
-        const float m = reduce(valid ? low : -INFINITY, width, larger_nan);
-        const float p = valid ? expf(low - m) / (1.0f + expf(-fabsf(x))) : 0.0f;
-        const float sum = reduce(p, width, add);
-        const float w = p / sum;
-        const float mean = reduce(valid ? w * d : 0.0f, width, add);
-        term = w * left * (d - mean);
+        const float m = reduce<L>(valid ? low : -INFINITY, larger);
+        const float p = valid ? expf(low - m) / whole : 0.0f;
+        const float w = p / reduce<L>(p, add);
+        term = w * left * (d - reduce<L>(valid ? w * d : 0.0f, add));
       } else {
-        term = expf(low) / (1.0f + expf(-fabsf(x))) * left * d;
+        term = (l > 0.0f ? 1.0f : small) / whole * left * d;
+        if (l != l) term = l;
       }
     } else {
-      const float m = reduce(x, width, larger_nan);
-      const float p = valid ? expf(x - m) : 0.0f;
-      const float sum = reduce(p, width, add);
-      const float w = p / sum;
-      const float mean = reduce(valid ? w * d : 0.0f, width, add);
-      term = w * (d - mean);
+      const float m = reduce<L>(l, larger);
+      const float p = valid ? expf(l - m) : 0.0f;
+      const float w = p / reduce<L>(p, add);
+      term = w * (d - reduce<L>(valid ? w * d : 0.0f, add));
     }
-    if (!valid) term = 0.0f;
   }
+  if (!valid) term = 0.0f;
 
-  // Rows of the result.
-  for (int g = 0; g < a.group_tokens && t0 + g < a.tokens; ++g) {
-    const int64_t row = t0 + g;
-    float v[kPerLane];
+  float v[kPer];
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) v[j] = 0.0f;
-    for (int k = 0; k < a.topk; ++k) {
-      const int at = g * width + k;
-      const int32_t ek = uniform(__shfl(e, at, 64));
-      const float tk = __shfl(term, at, 64);
+  for (int j = 0; j < kPer; ++j) v[j] = 0.0f;
+  const int32_t mine = valid ? e : -1;
+  for (int k = 0; k < a.topk; ++k) {
+    const int32_t at = __shfl(mine, (lane & ~(L - 1)) + k, 64) - first;
+    const float tk = __shfl(term, (lane & ~(L - 1)) + k, 64);
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
-        if (64 * j < a.experts && 64 * j + lane == ek) v[j] += tk;
-    }
-    if (dense) {
-      float x[kPerLane];
-      float m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j) {
-        x[j] = -INFINITY;
-        if (64 * j + lane < a.experts) x[j] = load_in(a.logits, row * a.ld + 64 * j + lane, a.dtype);
-        if (64 * j < a.experts) m = larger_nan(m, x[j]);
-      }
-      m = reduce(m, 64, larger_nan);
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
-        if (64 * j < a.experts) {
-          x[j] = 64 * j + lane < a.experts ? expf(x[j] - m) : 0.0f;
-          sum += x[j];
-        }
-      sum = reduce(sum, 64, add);
-      float mean = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
-        if (64 * j < a.experts) {
-          x[j] = x[j] / sum;
-          mean += 64 * j + lane < a.experts ? x[j] * v[j] : 0.0f;
-        }
-      mean = reduce(mean, 64, add);
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j) v[j] = x[j] * (v[j] - mean);
-    }
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j)
-      if (64 * j + lane < a.experts) store_in(a.dlogits, row * a.ld_out + 64 * j + lane, v[j], a.dtype);
+    for (int j = 0; j < kPer; ++j) v[j] += at == j ? tk : 0.0f;
   }
+  if (DENSE) {
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) m = larger(m, x[j]);
+    if (have <= 0) m = -INFINITY;
+    m = reduce<L>(m, larger);
+    float sum = 0.0f, mean = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      x[j] = j < have ? expf(x[j] - m) : 0.0f;
+      sum += x[j];
+    }
+    sum = reduce<L>(sum, add);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      x[j] = j < have ? x[j] / sum : 0.0f;
+      mean += x[j] * v[j];
+    }
+    mean = reduce<L>(mean, add);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] = x[j] * (v[j] - mean);
+  }
+  store16<T>(a.dlogits, row * a.ld_out + first, have, a.wide != 0, v);
+}
+
+template <int L, typename T>
+hipError_t launch(const RouteBackwardArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.tokens + kThreads / L - 1) / (kThreads / L)));
+  if (!a.sigmoid && !a.renormalize)
+    hipLaunchKernelGGL((k_route_backward<L, T, true>), grid, dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_route_backward<L, T, false>), grid, dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_typed(RouteBackwardArgs a, hipStream_t stream) {
+  a.wide = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(a.dlogits) % 16 == 0 &&
+           a.ld * sizeof(T) % 16 == 0 && a.ld_out * sizeof(T) % 16 == 0;
+  return a.experts <= 256 && a.topk <= 16 ? launch<16, T>(a, stream) : launch<64, T>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_route_backward(const RouteBackwardArgs& args, hipStream_t stream) {
-  RouteBackwardArgs a = args;
-  a.slot_lanes = 1;
-  while (a.slot_lanes < a.topk) a.slot_lanes *= 2;
-  // Tokens of a wavefront: as many as its lanes hold slots for, once there are several
-  // wavefronts for every SIMD (1024 of them).
-  a.group_tokens = 1;
-  while (a.group_tokens * 2 * a.slot_lanes <= 64 && a.tokens >= (int64_t)a.group_tokens * 2 * 4096)
-    a.group_tokens *= 2;
-  const int64_t groups = (a.tokens + a.group_tokens - 1) / a.group_tokens;
-  hipLaunchKernelGGL(k_route_backward, dim3((unsigned)((groups + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                     stream, a);
-  return hipGetLastError();
+hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t stream) {
+  if (a.dtype == kInF32) return launch_typed<float>(a, stream);
+  return a.dtype == kInF16 ? launch_typed<_Float16>(a, stream) : launch_typed<__bf16>(a, stream);
 }
 
 }  // namespace moe_fp4

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(RowsArgs a) {
     for (int u = 0; u < U; ++u) {
       const int64_t c = p.piece + 64 * u;
       if (c < whole) {
-        *reinterpret_cast<piece_t*>(dst + c * V) = v[u];
+        __builtin_nontemporal_store(v[u], reinterpret_cast<piece_t*>(dst + c * V));
       } else if (c < all) {
         if (a.esize == 4)
           for (int64_t b = c * V; b < a.row_bytes; b += 4)

@@ -127,7 +127,7 @@ def lib() -> ctypes.CDLL:
     return L
 
 
-# The few-token calls' short host path (csrc/calls.cpp), or None where it was not built for
+# The short host path (csrc/calls.cpp) of the few-token, FP8 and gradient calls, or None where it was not built for
 # this torch: the Python code below does the same, only slower.
 _calls = None
 
@@ -143,7 +143,9 @@ def _load_calls(L) -> None:
         return
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                   for f in (L.moe_fp4_linear, L.moe_fp4_ffn, L.moe_fp4_ffn_workspace_size,
-                            L.moe_fp4_route, L.moe_fp4_route_workspace_size)))
+                            L.moe_fp4_route, L.moe_fp4_route_workspace_size, L.moe_fp8_quantize,
+                            L.moe_grouped_gemm_fp8, L.moe_fp4_dispatch, L.moe_fp4_dispatch_backward,
+                            L.moe_fp4_combine_backward, L.moe_fp4_route_backward)))
     _calls = module
 
 
@@ -744,6 +746,13 @@ def _typed(t, name, dims, types=_IN_TYPES):
     return t.shape
 
 
+def _short(x):
+    """The current device where the short host path may take a call whose first tensor is x, or None."""
+    if (_calls or lib() and _calls) and isinstance(x, torch.Tensor) and x.is_cuda:
+        return _current_device()
+    return None
+
+
 def _new(stream, like, shape, dtype):
     with _on(stream):
         return like.new_empty(shape, dtype=dtype)
@@ -762,6 +771,10 @@ def quantize_fp8(x, swiglu: bool = False, grad=None, power_of_two: bool = False,
     that with respect to x, [rows][2k].  power_of_two: scales rounded up to powers of two.
     Returns (q float8_e4m3fn [rows][columns], sf float32 [rows][ceil(columns / 128)]);
     new ones belong to the launch stream."""
+    if stream is None and q is None and sf is None and (dev := _short(x)) is not None:
+        got = _calls.quantize_fp8(x, swiglu, grad, power_of_two, dev, _raw_stream(dev))
+        if got is not None:
+            return got
     rows, width = _typed(x, "x", 2)
     k = width // 2 if swiglu else width
     if swiglu and width % 2:
@@ -860,6 +873,12 @@ def grouped_gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index=None, out=None, 
     int32 [m_total] or None.  m_total defaults to a_row_index's length, else a_rows.  Returns
     out [m_total][n] of out_dtype (or the given out's type); a new one belongs to the launch
     stream.  Rows outside the offsets are not written."""
+    if stream is None and out is None and m_total is None and offsets is not None and \
+            (dev := _short(a_q)) is not None:
+        got = _calls.gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index, _OUT_TYPES.get(out_dtype, 3), dev,
+                              _raw_stream(dev))
+        if got is not None:
+            return got
     E, n, k = _typed(w_q, "w_q", 3, (FP8,))
     if isinstance(a_q, torch.Tensor) and a_q.dim() == 2 and a_q.shape[1] != k:
         raise ValueError(f"w_q: shape {tuple(w_q.shape)}, expected {a_q.shape[1]} columns")
@@ -873,6 +892,10 @@ def grouped_gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index=None, out=None, 
 def linear_fp8(a_q, a_sf, w_q, w_sf, out=None, out_dtype=torch.bfloat16, stream=None):
     """Dense product of FP8 rows [m][k] with FP8 weights [n][k] in blocks of 128, scales as for
     grouped_gemm_fp8.  Returns out [m][n]; a new one belongs to the launch stream."""
+    if stream is None and out is None and (dev := _short(a_q)) is not None:
+        got = _calls.gemm_fp8(a_q, a_sf, w_q, w_sf, None, None, _OUT_TYPES.get(out_dtype, 3), dev, _raw_stream(dev))
+        if got is not None:
+            return got
     n, k = _typed(w_q, "w_q", 2, (FP8,))
     if isinstance(a_q, torch.Tensor) and a_q.dim() == 2 and a_q.shape[1] != k:
         raise ValueError(f"w_q: shape {tuple(w_q.shape)}, expected {a_q.shape[1]} columns")
@@ -894,6 +917,10 @@ def dispatch(x, row_token, out=None, stream=None):
     no such token.  x: CUDA tensor [tokens][n] (bfloat16, float16, float32 or float8_e4m3fn),
     unit column stride; row_token int32 [rows].  Returns out [rows][n] of x's type; a new one
     belongs to the launch stream."""
+    if stream is None and out is None and (dev := _short(x)) is not None:
+        got = _calls.dispatch(x, row_token, dev, _raw_stream(dev))
+        if got is not None:
+            return got
     T, n = _typed(x, "x", 2, _ROW_TYPES)
     ld = _pitch(x, "x", x.dtype, (T, n))
     _need(row_token, "row_token", torch.int32, (None,))
@@ -919,6 +946,10 @@ def dispatch_backward(dy, token_rows, out=None, stream=None):
     in dy passed over.  dy: bfloat16, float16 or float32 CUDA tensor [rows][n], unit column
     stride; token_rows int32 [tokens][topk] (Routing.token_rows).  Returns out [tokens][n] of
     dy's type; a new one belongs to the launch stream."""
+    if stream is None and out is None and (dev := _short(dy)) is not None:
+        got = _calls.dispatch_backward(dy, token_rows, dev, _raw_stream(dev))
+        if got is not None:
+            return got
     m, n = _typed(dy, "dy", 2)
     ld = _pitch(dy, "dy", dy.dtype, (m, n))
     _need(token_rows, "token_rows", torch.int32, (None, None))
@@ -947,6 +978,11 @@ def combine_backward(dout, rows, token_rows, token_weights, row_token=None, drow
     [tokens][topk]); the residual's gradient is dout itself.  Rows that no slot names: with
     row_token (Routing.row_token) they are zeroed; without it a new drows is zeroed as a whole
     first, and a given one keeps them.  New results belong to the launch stream."""
+    if stream is None and drows is None and dweights is None and row_token is not None and \
+            (dev := _short(dout)) is not None:
+        got = _calls.combine_backward(dout, rows, token_rows, token_weights, row_token, dev, _raw_stream(dev))
+        if got is not None:
+            return got
     T, n = _typed(dout, "dout", 2, (torch.bfloat16, torch.float32))
     ld = _pitch(dout, "dout", dout.dtype, (T, n))
     _typed(rows, "rows", 2, (torch.bfloat16,))
@@ -988,6 +1024,10 @@ def route_backward(logits, ids, dweights, score: str = "softmax", renormalize: b
     logits, score and renormalize as route took them, ids int32 [tokens][topk] as it gave them
     (Routing.ids); dweights float32 [tokens][topk], the gradient of Routing.weights.  Returns out
     [tokens][E] of the logits' type; a new one belongs to the launch stream."""
+    if stream is None and out is None and score in _SCORES and (dev := _short(logits)) is not None:
+        got = _calls.route_backward(logits, ids, dweights, _SCORES[score], renormalize, dev, _raw_stream(dev))
+        if got is not None:
+            return got
     T, E = _typed(logits, "logits", 2)
     if score not in _SCORES:
         raise ValueError(f"score: {score!r}, expected 'softmax' or 'sigmoid'")
