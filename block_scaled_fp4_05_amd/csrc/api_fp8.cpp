@@ -79,6 +79,7 @@ int moe_fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t k, int64
   a.sf = sf;
   a.per_row = moe_fp4::FastDiv::of((uint32_t)blocks(cols));
   a.blocks = (uint32_t)(rows * blocks(cols));
+  a.rows = rows;
   a.k = (int32_t)cols;
   a.dtype = in_dtype;
   a.swiglu = swiglu;

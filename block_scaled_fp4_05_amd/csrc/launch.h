@@ -256,8 +256,12 @@ struct Fp8QuantArgs {
   float* sf;   // [rows][k in blocks]
   FastDiv per_row;  // by the blocks of a row
   uint32_t blocks;  // of all rows, below 2^31 - 2^16
+  int64_t rows;
   int32_t k;        // columns of q
   int32_t dtype, swiglu, pow2;
+  // Set by the launcher: rows of a workgroup that holds whole rows, eight columns a thread.
+  FastDiv per_piece;
+  int32_t group_rows = 0;
 };
 hipError_t launch_quantize_fp8(const Fp8QuantArgs& args, hipStream_t stream);
 

@@ -81,7 +81,7 @@ def test_pitches_given_outputs_and_no_rows():
 
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("rows,k", [(1, 16), (2, 256), (5, 144), (66, 1424)])
+@pytest.mark.parametrize("rows,k", [(1, 16), (301, 16), (2, 256), (5, 144), (66, 1424), (9, 2064), (3, 8192), (2, 8208)])
 def test_swiglu_and_its_gradient(rows, k, dtype, pow2):
     require_gpu()
     from block_scaled_fp4_05_amd import moe_fp4 as m
