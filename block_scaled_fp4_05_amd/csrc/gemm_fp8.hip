@@ -14,16 +14,12 @@
 namespace moe_fp4 {
 namespace {
 
-// 32 bytes of a row: the 16-byte pieces g and 4 + g of a block.
-__device__ __forceinline__ i32x8_t load32(rsrc_t rs, uint32_t off0, uint32_t off1, int32_t k, int hint) {
-  u32x4_t lo, hi;
-  if (hint) {
-    lo = __builtin_amdgcn_raw_buffer_load_b128(rs, off0, k, kLoadStreamOnce);
-    hi = __builtin_amdgcn_raw_buffer_load_b128(rs, off1, k, kLoadStreamOnce);
-  } else {
-    lo = __builtin_amdgcn_raw_buffer_load_b128(rs, off0, k, 0);
-    hi = __builtin_amdgcn_raw_buffer_load_b128(rs, off1, k, 0);
-  }
+// 32 bytes of a row: the 16-byte pieces g and 4 + g of a block.  (Two loads share a 128-byte
+// line: the hint that drops a line after its first use made dense 6144 x 6144 of one token 14.7
+// us instead of 10.9.)
+__device__ __forceinline__ i32x8_t load32(rsrc_t rs, uint32_t off0, uint32_t off1, int32_t k) {
+  const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(rs, off0, k, 0);
+  const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(rs, off1, k, 0);
   return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
@@ -83,10 +79,10 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
     const int32_t kk = uniform(b * kFp8Block);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      s.w[t] = load32(w_rs, ok0 ? w_off[t] : kOutOfRange, ok1 ? w_off[t] + 64 : kOutOfRange, kk, 1);
+      s.w[t] = load32(w_rs, ok0 ? w_off[t] : kOutOfRange, ok1 ? w_off[t] + 64 : kOutOfRange, kk);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      s.a[m] = load32(a_rs, ok0 ? a_off[m] : kOutOfRange, ok1 ? a_off[m] + 64 : kOutOfRange, kk, 0);
+      s.a[m] = load32(a_rs, ok0 ? a_off[m] : kOutOfRange, ok1 ? a_off[m] + 64 : kOutOfRange, kk);
       s.sa[m] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(s_rs, in ? s_off[m] : kOutOfRange, uniform(b * 4), 0));
     }
     s.sw = ((sconst_f32)w_sf)[in ? b : b1 - 1];
@@ -136,6 +132,9 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
   }
 }
 
+// Items of 16 x 16 a launch may have (fewer than 2^32 threads).
+constexpr int64_t kFewItems = 1 << 21;
+
 template <int NT, int MT, int W, int D>
 hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
   p.n_tiles = (p.n + 16 * NT - 1) / (16 * NT);
@@ -146,23 +145,28 @@ hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
 
 }  // namespace
 
-// The few-row kernel while a call has so few tiles of 32 x 128 that they would leave CUs
-// without work; its K split then keeps them loading.  256 experts of 512 x 6144, top-8, one token
-// (32 tiles): 10.9 us against 31 with tiles; four tokens (132): 24.8 against 32.5; eight (264): 45
-// against 36.5; dense 8192 x 6144, 64 rows (192): 28.8 against 30; 128 rows (320): 51 against 31.
+// The few-row kernel for fewer than four rows an expert, and while tiles of 64 x 128 would leave
+// CUs without work (its K split keeps them loading).  Both sides in us: 256 experts of 512 x 6144,
+// top-8, one token 9.3 against 31 with tiles, eight 36 and 53, 64 (two rows an expert) 109 and
+// 107, 512 (16 rows) 225 and 163; 64 experts of 2048 x 4096, three rows 82 and 113, 32 rows 145 and
+// 138; dense 8192 x 6144, 64 rows (128 tiles) 22.7 and 31, 128 rows (192 tiles) 32 and 31.
 hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts;
-  const int64_t tiles = (p.m_total / 32 + experts) * ((p.n + 127) / 128);
-  if (tiles >= 224) return launch_gemm_fp8_tiled(p, stream);
-  // Up to 16, 32 or 64 rows of an expert read its weights once (dense 8192 x 6144, 32 rows: 20.6 us
-  // with room for 32, 23.1 for 64, 27 for 16; 64 rows: 28.8 with room for 64, 35 for 32).  Of 16
-  // rows, items of 16 weight rows while there is about one for a CU, else of 32 (dense
-  // 6144 x 6144, 16 rows: 16.5 us against 20; one token above: 14 against 10.9).
   const int64_t rows = (p.m_total + p.experts - 1) / p.experts;
-  if (rows > 32) return launch<2, 4, 4, 2>(p, stream);
-  if (rows > 16) return launch<2, 2, 4, 2>(p, stream);
+  const int64_t tiles = (p.m_total / 64 + experts) * ((p.n + 127) / 128);
+  const bool few = p.m_total < 4 * (int64_t)p.experts || tiles < 96 || (rows <= 64 && tiles < 224);
   const int64_t items = (p.m_total / 16 + experts) * ((p.n + 15) / 16);
-  return items <= 320 ? launch<1, 1, 8, 3>(p, stream) : launch<2, 1, 8, 2>(p, stream);
+  if (!few || items > kFewItems) return launch_gemm_fp8_tiled(p, stream);
+  // Activation rows of a workgroup: 16, 32, or 64 above that (dense 8192 x 6144, 32 rows: 17.4 with
+  // room for 32, 19 for 16; 64 rows: 22.7 with 32, 26 with 64; 128 rows: 32 with 64, 42 with 32).
+  if (rows > 64) return launch<4, 4, 4, 1>(p, stream);
+  if (rows > 32) return launch<4, 2, 4, 1>(p, stream);
+  if (rows > 16) return launch<2, 2, 4, 2>(p, stream);
+  // Weight rows: 16 while that is about one item a CU, 32 up to twice that, else 64 (one token
+  // above: 9.3, 11.4 and 17; dense 6144 x 6144, 16 rows: 18, 13.4 and 18; four tokens above:
+  // 24, 20.4 and 19.2).
+  if (items <= 320) return launch<1, 1, 8, 3>(p, stream);
+  return items <= 640 ? launch<2, 1, 8, 2>(p, stream) : launch<4, 1, 4, 2>(p, stream);
 }
 
 }  // namespace moe_fp4

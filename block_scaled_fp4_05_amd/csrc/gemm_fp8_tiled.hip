@@ -27,7 +27,10 @@ __device__ __forceinline__ int tile_row(int t, int i) { return 32 * (t >> 1) + 4
 __device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swz_w(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 
-template <int WN, int WM, int MT, int R>
+// Stages in LDS.
+constexpr int kRing = 2;
+
+template <int WN, int WM, int MT>
 struct Tile {
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
   static constexpr int BN = 128 * WN, BM = 16 * MT * WM;
@@ -40,7 +43,6 @@ struct Tile {
   static constexpr int WD = MT >= 3 ? 2 : 4, AD = MT >= 3 ? 1 : 2;
   static constexpr int kScales = BM > 64 * kWaves ? BM : 64 * kWaves;
   static_assert(BN % kRound == 0 && BM % kRound == 0, "whole rounds");
-  static_assert(R == 2 || R == 3, "stages in LDS");
 };
 
 // 16 (or 4) bytes a lane from memory to LDS: lane l's to `to` + 16 l (4 l), `to` uniform.  In
@@ -71,12 +73,11 @@ __device__ __forceinline__ u32x4_t rsrc_words(const void* base, uint32_t bytes) 
                  (uint32_t)kRawBufferWord3};
 }
 
-// Everything this wavefront has read from LDS is in registers and all but its newest N vector memory
-// operations are complete (they complete in order); then all wavefronts meet.
-template <int N>
+// Everything this wavefront has read from LDS is in registers and what it copied there is complete;
+// then all wavefronts meet.
 __device__ __forceinline__ void stage_barrier() {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #endif
 }
 
@@ -117,13 +118,13 @@ struct Index {
   static constexpr int value = I;
 };
 
-template <int WN, int WM, int MT, int R, bool EXACT>
-__global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(WM * WN > 2 ? 2 : 1, MT >= 3 ? 2 : 4)))
+template <int WN, int WM, int MT, bool EXACT>
+__global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, MT >= 3 ? 2 : 4)))
 void k_gemm_fp8_tiled(Fp8GemmArgs p) {
-  typedef Tile<WN, WM, MT, R> T;
+  typedef Tile<WN, WM, MT> T;
   constexpr int WD = T::WD, AD = T::AD;
-  __shared__ __align__(1024) uint8_t stages[R][T::kStage];
-  __shared__ __align__(1024) float scales[R][T::kScales];  // of the stages' activation rows
+  __shared__ __align__(1024) uint8_t stages[kRing][T::kStage];
+  __shared__ __align__(1024) float scales[kRing][T::kScales];  // of the stages' activation rows
   __shared__ Fp8Item place[2];
   __shared__ int32_t sums[T::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -138,10 +139,9 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
 
   // ---- copies: this thread moves piece lane % 8 of rows tid / 8 + kRound * j, swizzled, and
   // wavefront w the scales of activation rows 64 w ...
-  // (swz_a has a period of 16 rows, swz_w of 32: with 16 rows a round, odd rounds differ.)
-  static_assert(T::kRound % 16 == 0, "rows of a round");
-  const int piece_a = (lane & 7) ^ swz_a(tid >> 3);
-  const int piece_w[2] = {(lane & 7) ^ swz_w(tid >> 3), (lane & 7) ^ swz_w((tid >> 3) + T::kRound)};
+  // (swz_a has a period of 16 rows, swz_w of 32: every round's rows have the same pieces.)
+  static_assert(T::kRound % 32 == 0, "rows of a round");
+  const int piece_a = (lane & 7) ^ swz_a(tid >> 3), piece_w = (lane & 7) ^ swz_w(tid >> 3);
   const uint8_t* const w_base = p.w_q + (int64_t)it.e * n * k;
   // Without a row index the tile's rows follow each other: offsets from its first row.
   const int64_t base = p.a_row_index ? 0 : it.row0, a_rows = p.a_row_index ? p.a_rows : (int64_t)it.rows;
@@ -149,7 +149,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
 #pragma unroll
   for (int j = 0; j < T::kWRounds; ++j) {
     const int32_t row = it.n0 + (tid >> 3) + T::kRound * j;
-    off[j] = (uint32_t)(row < n ? row : n - 1) * (uint32_t)k + 16u * piece_w[j & 1];
+    off[j] = (uint32_t)(row < n ? row : n - 1) * (uint32_t)k + 16u * piece_w;
   }
   {
     int32_t row[T::kARounds + 1];
@@ -174,17 +174,16 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   const u32x4_t a_rs = rsrc_words(p.a_q + base * k, (uint32_t)(a_rows * k));
   const u32x4_t s_rs = rsrc_words(p.a_sf + base * kbs, (uint32_t)(a_rows * kbs * 4));
   const uint32_t last_at = (uint32_t)(kbs - 1) * 128u;
-  const uint32_t last_w[2] = {last_at + 16u * piece_w[0] >= (uint32_t)k ? 0u - 16u * piece_w[0] : last_at,
-                              last_at + 16u * piece_w[1] >= (uint32_t)k ? 0u - 16u * piece_w[1] : last_at};
+  const uint32_t last_w = last_at + 16u * piece_w >= (uint32_t)k ? 0u - 16u * piece_w : last_at;
   const uint32_t last_a = last_at + 16u * piece_a >= (uint32_t)k ? 0u - 16u * piece_a : last_at;
   auto within = [&](const u32x4_t& rs, int32_t b) { return u32x4_t{rs[0], rs[1], b < kbs ? rs[2] : 0u, rs[3]}; };
   auto copy = [&](uint8_t* to, int32_t b, int from, int end) {
     const u32x4_t w_now = within(w_rs, b), a_now = within(a_rs, b);
-    const uint32_t here = (uint32_t)b * 128u, at_a = b == kbs - 1 ? last_a : here;
-    const uint32_t at_w[2] = {b == kbs - 1 ? last_w[0] : here, b == kbs - 1 ? last_w[1] : here};
+    const uint32_t here = (uint32_t)b * 128u;
+    const uint32_t at_w = b == kbs - 1 ? last_w : here, at_a = b == kbs - 1 ? last_a : here;
 #pragma unroll
     for (int j = from; j < end; ++j)
-      copy16(j < T::kWRounds ? w_now : a_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + (j < T::kWRounds ? at_w[j & 1] : at_a));
+      copy16(j < T::kWRounds ? w_now : a_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + (j < T::kWRounds ? at_w : at_a));
   };
   auto copy_scales = [&](float* to, int32_t b) { copy4(within(s_rs, b), to + 64 * wave, scale_off + (uint32_t)b * 4u); };
 
@@ -211,13 +210,13 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
 
   // One stage, tile by tile: a tile's products are issued while tiles ahead are read and the tile
   // before it is scaled and added.  The last two tiles wait in registers for the barrier, behind
-  // which the stage's place is filled anew, R stages ahead, and the next stage's first operands
+  // which the stage's place is filled anew, two stages ahead, and the next stage's first operands
   // are read while those tiles are multiplied.  The fences keep the compiler from reading all
   // tiles first, which spills.
   constexpr int kHalf = (T::kCopies + 1) / 2;
   auto step = [&](auto which, int32_t b) {
     constexpr int S = decltype(which)::value;
-    uint8_t *const cur = stages[S % R], *const nxt = stages[(S + 1) % R];
+    uint8_t *const cur = stages[S], *const nxt = stages[1 - S];
     i32x8_t(&now_a)[MT] = a[S % AD];
     i32x8_t(&next_a)[MT] = a[(S + 1) % AD];
     if (b == kbs - 1 && k % kFp8Block != 0) {
@@ -232,7 +231,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     }
     float scale[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) scale[m] = scales[S % R][16 * (MT * wm + m) + r] * next_w;
+    for (int m = 0; m < MT; ++m) scale[m] = scales[S][16 * (MT * wm + m) + r] * next_w;
     next_w = ((sconst_f32)w_sf)[b + 1 < kbs ? b + 1 : b];
     operand_t ao[MT];
 #pragma unroll
@@ -241,8 +240,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     for (int t = 0; t < 8; ++t) {
       __builtin_amdgcn_sched_barrier(0);
       if (t == 6) {
-        // Newer than the next stage's copies: those of R - 2 later stages.
-        stage_barrier<(R - 2) * (T::kCopies + 1)>();
+        stage_barrier();
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (AD == 2) {
 #pragma unroll
@@ -256,10 +254,10 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
         for (int j = 0; j < WD - 2; ++j) read_w(nxt, j);
       }
       if (t == 7) read_w(nxt, WD - 2);
-      if (t == 6) copy(cur, b + R, 0, kHalf);
+      if (t == 6) copy(cur, b + kRing, 0, kHalf);
       if (t == 7) {
-        copy(cur, b + R, kHalf, T::kCopies);
-        copy_scales(scales[S % R], b + R);
+        copy(cur, b + kRing, kHalf, T::kCopies);
+        copy_scales(scales[S], b + kRing);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -283,34 +281,21 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     for (int m = 0; m < MT; ++m) add_scaled(acc[7][m], d[m], scale[m]);
   };
 
-#pragma unroll
-  for (int s = 0; s < R; ++s) {
-    copy(stages[s], s, 0, T::kCopies);
-    copy_scales(scales[s], s);
-  }
-  stage_barrier<(R - 1) * (T::kCopies + 1)>();
+  copy(stages[0], 0, 0, T::kCopies);
+  copy_scales(scales[0], 0);
+  stage_barrier();
+  copy(stages[1], 1, 0, T::kCopies);
+  copy_scales(scales[1], 1);
 #pragma unroll
   for (int m = 0; m < MT; ++m) read_a(stages[0], a[0], m);
 #pragma unroll
   for (int t = 0; t < WD - 1; ++t) read_w(stages[0], t);
-  for (int32_t b = 0; b < kbs;) {
+  for (int32_t b = 0; b < kbs; b += 2) {
     step(Index<0>{}, b);
-    if (++b == kbs) break;
-    step(Index<1>{}, b);
-    if (++b == kbs) break;
-    if constexpr (R == 3) {
-      step(Index<2>{}, b);
-      if (++b == kbs) break;
-      step(Index<3>{}, b);
-      if (++b == kbs) break;
-      step(Index<4>{}, b);
-      if (++b == kbs) break;
-      step(Index<5>{}, b);
-      ++b;
-    }
+    if (b + 1 < kbs) step(Index<1>{}, b + 1);
   }
   // Nothing is on its way into LDS when the workgroup ends.
-  stage_barrier<0>();
+  stage_barrier();
 
   // Where there is no row or column a store is sent out of range.
   constexpr int es = EXACT ? 4 : 2;
@@ -356,22 +341,20 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   }
 }
 
-template <int WN, int WM, int MT, int R, bool EXACT>
+template <int WN, int WM, int MT, bool EXACT>
 hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
-  typedef Tile<WN, WM, MT, R> T;
+  typedef Tile<WN, WM, MT> T;
   p.n_tiles = (p.n + T::BN - 1) / T::BN;
   // Columns that can be stored together everywhere: 8 (16-bit results) or 4 of them in one piece.
   const uint64_t es = EXACT ? 4 : 2, where = reinterpret_cast<uintptr_t>(p.out) | (uint64_t)p.ldo * es;
   p.store_cols = where % 16 == 0 && p.n % 8 == 0 ? 8 : where % (4 * es) == 0 && p.n % 4 == 0 ? 4 : 1;
   const int64_t items = (fp8_most_items(p, T::BM) + 7) / 8 * 8, row = 1 << 16;
   const dim3 grid = items <= row ? dim3((unsigned)items) : dim3((unsigned)row, (unsigned)((items + row - 1) / row));
-  hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, R, EXACT>), grid, dim3(T::kThreads), 0, stream, p);
+  hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, EXACT>), grid, dim3(T::kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
-// The tile by the average rows of an expert; both sides measured in us:
-//   32 x 128 below 8 rows, three stages deep (256 experts of 512 x 6144, top-8, 16 tokens: 58,
-//     against 68 with 64 x 128);
+// The tile by the average rows of an expert; both sides in us:
 //   64 x 128 below 96 rows (the down projection, 6144 x 256, 32 rows: 136 against 176 with 128 x
 //     128), and while 128 x 128 would leave CUs without two workgroups (dense 8192 x 6144, 256
 //     rows: 33 against 39);
@@ -383,13 +366,12 @@ hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
 template <bool EXACT>
 hipError_t launch_sized(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts, avg = p.m_total / p.experts;
-  if (avg < 8) return launch<1, 2, 1, 3, EXACT>(p, stream);
-  const int64_t m2 = (p.m_total / 128 + experts) * ((p.n + 127) / 128);
-  if (avg < 96 || m2 < 512) return launch<1, 4, 1, 2, EXACT>(p, stream);
+  const int64_t middle = (p.m_total / 128 + experts) * ((p.n + 127) / 128);
+  if (avg < 96 || middle < 512) return launch<1, 4, 1, EXACT>(p, stream);
   const int64_t big = (p.m_total + 255) / 256 * ((p.n + 255) / 256), rest = big % 256;
   if (!EXACT && avg >= 384 && big >= 224 && (rest == 0 || rest >= 160 || big >= 1024))
-    return launch<2, 4, 4, 2, false>(p, stream);
-  return launch<1, 4, 2, 2, EXACT>(p, stream);
+    return launch<2, 4, 4, false>(p, stream);
+  return launch<1, 4, 2, EXACT>(p, stream);
 }
 
 }  // namespace

@@ -309,6 +309,7 @@ struct RowsArgs {
   int32_t esize, dtype;
   // Set by the launchers.
   int64_t items = 0, segments = 0;
+  FastDiv per_segment;
   int32_t lanes = 0;
 };
 hipError_t launch_dispatch(const RowsArgs& args, hipStream_t stream);

@@ -11,10 +11,10 @@
 // taken with the largest e^min(x,0) divided out, so that tiny scores keep their proportions.
 //
 // A token takes 16 lanes (up to 256 experts and 16 slots) or 64, each with 16 consecutive
-// experts.  Its first lanes are its slots, which compute the slots' terms; then every lane adds
-// the terms that name its experts, in slot order, so each element of the dense result is written
-// once.  Four tokens a wavefront share every instruction, and a reduction over 16 lanes needs no
-// LDS.  Bound: the logits (softmax only) and the result, 2 to 8 bytes an expert, and for short
+// experts.  Its first lanes are its slots, which compute the slots' terms and put them into a row
+// of LDS (slots that name the same expert add up there, in slot order); every lane takes its
+// experts' terms from it and writes each element of the dense result once.  Four tokens a
+// wavefront share every instruction, and a reduction over 16 lanes needs no LDS.  Bound: the logits (softmax only) and the result, 2 to 8 bytes an expert, and for short
 // calls the launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -131,15 +131,33 @@ __global__ __launch_bounds__(kThreads) void k_route_backward(RouteBackwardArgs a
   }
   if (!valid) term = 0.0f;
 
+  // The token's row of terms.  Whether two slots name one expert: then one of them does not find its
+  // own number where it wrote it.
+  __shared__ __align__(16) float rows[kThreads * kPer];
+  float* const mine = rows + (threadIdx.x - me) * kPer;
+  int32_t* const names = reinterpret_cast<int32_t*>(mine);
+  if (valid) names[e] = me;
+  __syncthreads();
+  const bool twice = valid && names[e] != me;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPer; j += 4) *reinterpret_cast<float4_t*>(mine + first + j) = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  __syncthreads();
+  if (__syncthreads_or(twice)) {
+    for (int k = 0; k < a.topk; ++k) {
+      if (valid && me == k) mine[e] += term;
+      __syncthreads();
+    }
+  } else if (valid) {
+    mine[e] = term;
+  }
+  __syncthreads();
   float v[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) v[j] = 0.0f;
-  const int32_t mine = valid ? e : -1;
-  for (int k = 0; k < a.topk; ++k) {
-    const int32_t at = __shfl(mine, (lane & ~(L - 1)) + k, 64) - first;
-    const float tk = __shfl(term, (lane & ~(L - 1)) + k, 64);
+  for (int j = 0; j < kPer; j += 4) {
+    const float4_t f = *reinterpret_cast<const float4_t*>(mine + first + j);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] += at == j ? tk : 0.0f;
+    for (int i = 0; i < 4; ++i) v[j + i] = f[i];
   }
   if (DENSE) {
     float m = x[0];
@@ -153,10 +171,10 @@ __global__ __launch_bounds__(kThreads) void k_route_backward(RouteBackwardArgs a
       x[j] = j < have ? expf(x[j] - m) : 0.0f;
       sum += x[j];
     }
-    sum = reduce<L>(sum, add);
+    sum = 1.0f / reduce<L>(sum, add);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      x[j] = j < have ? x[j] / sum : 0.0f;
+      x[j] = j < have ? x[j] * sum : 0.0f;
       mean += x[j] * v[j];
     }
     mean = reduce<L>(mean, add);
