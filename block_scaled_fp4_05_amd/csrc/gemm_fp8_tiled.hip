@@ -42,7 +42,7 @@ struct Tile {
   // with few products a tile has to be more.
   static constexpr int WD = MT >= 3 ? 2 : 4, AD = MT >= 3 ? 1 : 2;
   static constexpr int kScales = BM > 64 * kWaves ? BM : 64 * kWaves;
-  static_assert(BN % kRound == 0 && BM % kRound == 0, "whole rounds");
+  static_assert(BN % kRound == 0 && BM % kRound == 0 && kCopies % 2 == 0, "whole rounds, an even number");
 };
 
 // 16 (or 4) bytes a lane from memory to LDS: lane l's to `to` + 16 l (4 l), `to` uniform.  In
@@ -213,7 +213,11 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   // which the stage's place is filled anew, two stages ahead, and the next stage's first operands
   // are read while those tiles are multiplied.  The fences keep the compiler from reading all
   // tiles first, which spills.
-  constexpr int kHalf = (T::kCopies + 1) / 2;
+  // A stage's copies are issued in four parts.  256 x 256: behind the barrier (tiles 6 and 7) and in
+  // the next stage's tiles 0 and 1, so that a wavefront's products do not queue behind eight of
+  // them (8192^3: 486 us, with all behind the barrier 509); smaller tiles behind the barrier, since
+  // what they wait for is the copies (4096 tokens of 256 experts: 259 us, spread 277).
+  constexpr int kPart = MT >= 3 ? T::kCopies / 4 : T::kCopies / 2;
   auto step = [&](auto which, int32_t b) {
     constexpr int S = decltype(which)::value;
     uint8_t *const cur = stages[S], *const nxt = stages[1 - S];
@@ -254,11 +258,13 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
         for (int j = 0; j < WD - 2; ++j) read_w(nxt, j);
       }
       if (t == 7) read_w(nxt, WD - 2);
-      if (t == 6) copy(cur, b + kRing, 0, kHalf);
+      if (t == 6) copy(cur, b + kRing, 0, kPart);
       if (t == 7) {
-        copy(cur, b + kRing, kHalf, T::kCopies);
+        copy(cur, b + kRing, kPart, 2 * kPart);
         copy_scales(scales[S], b + kRing);
       }
+      if (t == 0) copy(nxt, b + 1, 2 * kPart, min(3 * kPart, T::kCopies));
+      if (t == 1) copy(nxt, b + 1, 3 * kPart, T::kCopies);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -284,7 +290,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   copy(stages[0], 0, 0, T::kCopies);
   copy_scales(scales[0], 0);
   stage_barrier();
-  copy(stages[1], 1, 0, T::kCopies);
+  copy(stages[1], 1, 0, 2 * kPart);
   copy_scales(scales[1], 1);
 #pragma unroll
   for (int m = 0; m < MT; ++m) read_a(stages[0], a[0], m);
