@@ -87,7 +87,8 @@ template <int NTHR>
 struct Fp8Locator {
   const Fp8GemmArgs& p;
   const int32_t bm, bn, band;
-  int32_t lo, hi, run, own, start;  // this thread's experts, the items before and of them, first row
+  int32_t lo, hi, run, own;         // this thread's experts, the items before them and of them
+  int32_t start, second;            // first rows of its first expert and of the next
   int32_t total, count;             // items of all workgroups, of this one
   int32_t blocks, full, last, rounds;
 
@@ -99,15 +100,19 @@ struct Fp8Locator {
     lo = tid;
     hi = tid == 0 ? 1 : tid;
     start = run = 0;
+    second = m_total;
     own = total = fp8_items(p, m_total, bm);
     if (p.offsets) {
       const int32_t E = p.experts, per = (E + NTHR - 1) / NTHR;
       lo = min(tid * per, E);
       hi = min(lo + per, E);
       own = 0;
-      int32_t at = lo < hi ? clamp_off(p.offsets[lo], m_total) : 0;
-      start = at;
-      for (int32_t e = lo; e < hi; ++e) {
+      const int32_t first = p.offsets[lo], next0 = p.offsets[min(lo + 1, E)];  // (both on their way at once)
+      start = clamp_off(first, m_total);
+      second = clamp_off(next0, m_total);
+      if (lo < hi) own = fp8_items(p, second - start, bm);
+      int32_t at = second;
+      for (int32_t e = lo + 1; e < hi; ++e) {
         const int32_t next = clamp_off(p.offsets[e + 1], m_total);
         own += fp8_items(p, next - at, bm);
         at = next;
@@ -148,7 +153,7 @@ struct Fp8Locator {
     int32_t at = start, first = run;
     int32_t j = j0;
     for (int32_t e = lo; e < hi; ++e) {
-      const int32_t next = p.offsets ? clamp_off(p.offsets[e + 1], m_total) : m_total;
+      const int32_t next = e == lo ? second : clamp_off(p.offsets[e + 1], m_total);
       const int32_t rows = next - at, items = fp8_items(p, rows, bm);
       for (; j < j0 + n && j < count; ++j) {
         const int32_t item = j * blocks + (j == rounds - 1 ? last : full);
@@ -173,13 +178,6 @@ struct Fp8Locator {
     __syncthreads();
   }
 };
-
-// The activation row that result row r reads.
-__device__ __forceinline__ int32_t fp8_source_row(const Fp8GemmArgs& p, int32_t r) {
-  if (!p.a_row_index) return r;
-  const int32_t s = p.a_row_index[r], last = (int32_t)p.a_rows - 1;
-  return s < 0 ? 0 : s > last ? last : s;
-}
 
 // Four consecutive columns of a result row, rounded to nearest even.
 __device__ __forceinline__ void fp8_store4(const Fp8GemmArgs& p, int64_t row, int32_t col, const float4_t& v) {

@@ -56,12 +56,11 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
     const int32_t row = it.n0 + 16 * t + r;
     w_off[t] = (uint32_t)(row < n ? row : n - 1) * (uint32_t)k + 16u * g;
   }
+  int32_t src[MT];  // on its way while the first weights are asked for
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int32_t row = 16 * m + r;
-    const int32_t src = fp8_source_row(p, it.row0 + (row < it.rows ? row : it.rows - 1)) - (int32_t)base;
-    a_off[m] = (uint32_t)src * (uint32_t)k + 16u * g;
-    s_off[m] = (uint32_t)src * (uint32_t)kbs * 4u;
+    const int32_t row = it.row0 + min(16 * m + r, it.rows - 1);
+    src[m] = p.a_row_index ? p.a_row_index[row] : row;
   }
 
   float4_t acc[NT][MT];
@@ -72,14 +71,19 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
 
   const int32_t b0 = uniform(wave * kbs / W), b1 = uniform((wave + 1) * kbs / W);
   Stage<NT, MT> st[D];
-  auto load = [&](Stage<NT, MT>& s, int32_t b) {
-    // Pieces past k (the last block's) and blocks past the share read zeros.
+  // Pieces past k (the last block's) and blocks past the share read zeros.
+  auto load_w = [&](Stage<NT, MT>& s, int32_t b) {
     const bool in = b < b1;
     const bool ok0 = in && b * kFp8Block + 16 * g < k, ok1 = in && b * kFp8Block + 64 + 16 * g < k;
     const int32_t kk = uniform(b * kFp8Block);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       s.w[t] = load32(w_rs, ok0 ? w_off[t] : kOutOfRange, ok1 ? w_off[t] + 64 : kOutOfRange, kk);
+  };
+  auto load_a = [&](Stage<NT, MT>& s, int32_t b) {
+    const bool in = b < b1;
+    const bool ok0 = in && b * kFp8Block + 16 * g < k, ok1 = in && b * kFp8Block + 64 + 16 * g < k;
+    const int32_t kk = uniform(b * kFp8Block);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       s.a[m] = load32(a_rs, ok0 ? a_off[m] : kOutOfRange, ok1 ? a_off[m] + 64 : kOutOfRange, kk);
@@ -105,12 +109,23 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
   };
   if (b0 < b1) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(st[d], b0 + d);
+    for (int d = 0; d < D; ++d) load_w(st[d], b0 + d);
+    __builtin_amdgcn_sched_barrier(0);
+    const int32_t last = (int32_t)p.a_rows - 1;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint32_t row = (uint32_t)(p.a_row_index ? min(max(src[m], 0), last) : src[m] - (int32_t)base);
+      a_off[m] = row * (uint32_t)k + 16u * g;
+      s_off[m] = row * (uint32_t)kbs * 4u;
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_a(st[d], b0 + d);
     for (int32_t b = b0; b < b1; b += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (b + d < b1) multiply(st[d]);
-        load(st[d], b + d + D);
+        load_w(st[d], b + d + D);
+        load_a(st[d], b + d + D);
       }
     }
   }
