@@ -310,7 +310,7 @@ struct RowsArgs {
   // Set by the launchers.
   int64_t items = 0, segments = 0;
   FastDiv per_segment;
-  int32_t lanes = 0;
+  int32_t lanes = 0, by_slice = 0;
 };
 hipError_t launch_dispatch(const RowsArgs& args, hipStream_t stream);
 hipError_t launch_dispatch_backward(const RowsArgs& args, hipStream_t stream);

@@ -20,75 +20,40 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
-// V bytes of a row.
-template <int V> struct Piece;
-template <> struct Piece<16> { typedef u32x4_t type; };
-template <> struct Piece<8> { typedef u32x2_t type; };
-template <> struct Piece<4> { typedef uint32_t type; };
-template <> struct Piece<2> { typedef uint16_t type; };
-template <> struct Piece<1> { typedef uint8_t type; };
+// A row is copied in pieces of 16 bytes wherever it starts (the memory takes any alignment of
+// whole bytes; 4096 x 8 rows of 12 282 bytes: 105 us, in pieces of two bytes 241), its last
+// piece ending with it; rows under 16 bytes go byte by byte.
+//
+// What the copies cost is the way of the tokens into the XCDs' L2s, as many bytes again as
+// the rows written: the slots of a token are far apart.  So a workgroup takes a slice of
+// a.lanes pieces of some rows, the XCDs (workgroup b runs on b % 8) have slices of their own,
+// and a slice of all tokens stays in an L2 while it is used: 4096 x 8 rows of 12 KB take 84
+// us, row by row 108.  With one row a token nothing is read twice, and rows go whole.
+typedef u32x4_t any16_t __attribute__((aligned(1)));
 
-// Where a lane works: a wavefront takes one segment of 64 * U pieces of one row or, where rows
-// have fewer than 33 pieces, 64 / lanes rows side by side (lanes a power of two).
-struct Place {
-  int64_t row;
-  int64_t piece;  // first piece; the next ones follow at distance 64
-  bool in;
-};
-
-template <int U>
-__device__ __forceinline__ Place place(int64_t item, const RowsArgs& a, int lane) {
-  Place p;
-  if (a.segments > 1) {
-    const int64_t r = a.items <= INT32_MAX ? a.per_segment.div((uint32_t)item) : item / a.segments;
-    p.row = r;
-    p.piece = (item - r * a.segments) * (64 * U) + lane;
-  } else {
-    p.row = item * (64 / a.lanes) + lane / a.lanes;
-    p.piece = lane & (a.lanes - 1);
-  }
-  p.in = p.row < a.rows;
-  return p;
-}
-
-// Pieces of a row that are V bytes whole; what is left (fewer than V bytes, only with V
-// above an element) is copied element by element by the lane whose piece it is.
-template <int V, int U>
 __global__ __launch_bounds__(kThreads) void k_dispatch(RowsArgs a) {
-  typedef typename Piece<V>::type piece_t;
-  const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * kWaves;
-  const int64_t whole = a.row_bytes / V, all = (a.row_bytes + V - 1) / V;
-  for (int64_t item = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6); item < a.items;
-       item += waves) {
-    const Place p = place<U>(item, a, lane);
-    if (!p.in) continue;
-    const int32_t t = a.map[p.row];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int side = 64 / a.lanes;  // rows side by side in a wavefront
+  const int64_t share = (a.items + kXcds - 1) / kXcds;
+  const int64_t first = (blockIdx.x % kXcds) * share, last = min(first + share, a.items);
+  for (int64_t item = first + blockIdx.x / kXcds; item < last; item += gridDim.x / kXcds) {
+    const int64_t q = a.items <= INT32_MAX ? a.per_segment.div((uint32_t)item) : item / a.segments;
+    const int64_t rest = item - q * a.segments;
+    const int64_t slice = a.by_slice ? q : rest;
+    const int64_t row = ((a.by_slice ? rest : q) * kWaves + wave) * side + lane / a.lanes;
+    int64_t c = (slice * a.lanes + (lane & (a.lanes - 1))) * 16;
+    if (row >= a.rows || c >= a.row_bytes) continue;
+    const int32_t t = a.map[row];
     const bool ok = t >= 0 && t < a.source_rows;
     const char* src = static_cast<const char*>(a.x) + (ok ? t * a.ld_x : 0);
-    char* dst = static_cast<char*>(a.out) + p.row * a.ld_out;
-    piece_t v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = p.piece + 64 * u;
-      v[u] = piece_t{};
-      if (ok && c < whole) v[u] = *reinterpret_cast<const piece_t*>(src + c * V);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = p.piece + 64 * u;
-      if (c < whole) {
-        __builtin_nontemporal_store(v[u], reinterpret_cast<piece_t*>(dst + c * V));
-      } else if (c < all) {
-        if (a.esize == 4)
-          for (int64_t b = c * V; b < a.row_bytes; b += 4)
-            *reinterpret_cast<uint32_t*>(dst + b) = ok ? *reinterpret_cast<const uint32_t*>(src + b) : 0u;
-        else if (a.esize == 2)
-          for (int64_t b = c * V; b < a.row_bytes; b += 2)
-            *reinterpret_cast<uint16_t*>(dst + b) = ok ? *reinterpret_cast<const uint16_t*>(src + b) : (uint16_t)0;
-        else
-          for (int64_t b = c * V; b < a.row_bytes; ++b) dst[b] = ok ? src[b] : (char)0;
-      }
+    char* dst = static_cast<char*>(a.out) + row * a.ld_out;
+    if (a.row_bytes >= 16) {
+      c = min(c, a.row_bytes - 16);
+      u32x4_t v = u32x4_t{0, 0, 0, 0};
+      if (ok) v = *reinterpret_cast<const any16_t*>(src + c);
+      __builtin_nontemporal_store(v, reinterpret_cast<any16_t*>(dst + c));
+    } else {
+      for (int64_t b = 0; b < a.row_bytes; ++b) dst[b] = ok ? src[b] : (char)0;
     }
   }
 }
@@ -108,71 +73,70 @@ template <> struct Element<kInF16> {
   typedef _Float16 type;
 };
 
-template <int DT, int V, int U>
+// A wavefront takes 64 pieces of 16 bytes of a row or, where rows have fewer than 33, 64 / lanes
+// rows side by side (lanes a power of two); up to kSlots rows of the token are in flight
+// together.  A row's last piece ends with it: what two lanes both have they write alike.
+template <int DT>
 __global__ __launch_bounds__(kThreads) void k_dispatch_backward(RowsArgs a) {
   typedef typename Element<DT>::type elem_t;
-  constexpr int N = V / Element<DT>::size;  // elements of a piece
+  constexpr int N = 16 / Element<DT>::size;  // elements of a piece
+  constexpr int kSlots = 8;
   typedef elem_t vec_t __attribute__((ext_vector_type(N)));
-  constexpr int S = 4;  // slots whose rows are in flight together
+  typedef vec_t any_t __attribute__((aligned(sizeof(elem_t))));
   const int lane = threadIdx.x & 63;
   const int64_t waves = (int64_t)gridDim.x * kWaves;
-  const int64_t whole = a.row_bytes / V, all = (a.row_bytes + V - 1) / V;
   for (int64_t item = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6); item < a.items;
        item += waves) {
-    const Place p = place<U>(item, a, lane);
-    if (!p.in) continue;
-    const int32_t* slots = a.map + p.row * a.topk;
-    float acc[U][N];
+    int64_t row, c;  // c: the piece's first element
+    if (a.segments > 1) {
+      row = a.items <= INT32_MAX ? a.per_segment.div((uint32_t)item) : item / a.segments;
+      c = ((item - row * a.segments) * 64 + lane) * N;
+    } else {
+      row = item * (64 / a.lanes) + lane / a.lanes;
+      c = (lane & (a.lanes - 1)) * N;
+    }
+    if (row >= a.rows || c >= a.cols) continue;
+    const bool whole = a.cols >= N;
+    if (whole) c = min(c, a.cols - N);
+    const int32_t* slots = a.map + row * a.topk;
+    float acc[N];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    for (int32_t s0 = 0; s0 < a.topk; s0 += kSlots) {
+      vec_t v[kSlots];
+      bool ok[kSlots];
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[u][i] = 0.0f;
-    for (int32_t s0 = 0; s0 < a.topk; s0 += S) {
-      vec_t v[S][U];
-      bool ok[S];
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
+      for (int s = 0; s < kSlots; ++s) {
         const int32_t r = s0 + s < a.topk ? slots[s0 + s] : -1;
         ok[s] = r >= 0 && r < a.source_rows;
-        const char* src = static_cast<const char*>(a.x) + (ok[s] ? r * a.ld_x : 0);
+        if (!ok[s]) continue;
+        const elem_t* src = reinterpret_cast<const elem_t*>(static_cast<const char*>(a.x) + r * a.ld_x);
+        if (whole) {
+          v[s] = *reinterpret_cast<const any_t*>(src + c);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t c = p.piece + 64 * u;
-          if (ok[s] && c < whole) v[s][u] = *reinterpret_cast<const vec_t*>(src + c * V);
-          else if (ok[s] && c < all) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              v[s][u][i] = c * N + i < a.cols ? reinterpret_cast<const elem_t*>(src)[c * N + i] : (elem_t)0.0f;
-          }
+          for (int i = 0; i < N; ++i) v[s][i] = i < a.cols ? src[i] : (elem_t)0.0f;
         }
       }
       // A slot without a row is passed over (not added as 0: -0 stays -0, and what another row
       // holds plays no part).
 #pragma unroll
-      for (int s = 0; s < S; ++s)
+      for (int s = 0; s < kSlots; ++s)
         if (ok[s]) {
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (p.piece + 64 * u < all) {
-#pragma unroll
-              for (int i = 0; i < N; ++i) acc[u][i] += (float)v[s][u][i];
-            }
+          for (int i = 0; i < N; ++i) acc[i] += (float)v[s][i];
         }
     }
-    char* dst = static_cast<char*>(a.out) + p.row * a.ld_out;
+    elem_t* dst = reinterpret_cast<elem_t*>(static_cast<char*>(a.out) + row * a.ld_out);
+    vec_t o;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = p.piece + 64 * u;
-      if (c < whole) {
-        vec_t o;
+    for (int i = 0; i < N; ++i) o[i] = (elem_t)acc[i];
+    if (whole) {
+      *reinterpret_cast<any_t*>(dst + c) = o;
+    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = (elem_t)acc[u][i];
-        *reinterpret_cast<vec_t*>(dst + c * V) = o;
-      } else if (c < all) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (c * N + i < a.cols) reinterpret_cast<elem_t*>(dst)[c * N + i] = (elem_t)acc[u][i];
-      }
+      for (int i = 0; i < N; ++i)
+        if (i < a.cols) dst[i] = o[i];
     }
   }
 }
@@ -277,52 +241,19 @@ __global__ __launch_bounds__(W * 64) void k_combine_backward(CombineBackwardArgs
   }
 }
 
-// The widest piece that every row of both matrices starts at a multiple of.
-int piece_bytes(const RowsArgs& a) {
-  const uint64_t all = (uint64_t)reinterpret_cast<uintptr_t>(a.x) | (uint64_t)reinterpret_cast<uintptr_t>(a.out) |
-                       (uint64_t)a.ld_x | (uint64_t)a.ld_out;
-  int v = 16;
-  while (v > a.esize && all % v != 0) v /= 2;
-  return v;
-}
-
-template <int U>
-unsigned lay_out(RowsArgs& a, int v) {
-  const int64_t pieces = (a.row_bytes + v - 1) / v;
+template <int DT>
+hipError_t dispatch_backward_dt(RowsArgs a, hipStream_t stream) {
+  const int64_t pieces = (a.row_bytes + 15) / 16;
   a.lanes = 64;
   while (a.lanes > 1 && a.lanes / 2 >= pieces) a.lanes /= 2;
-  a.segments = (pieces + 64 * U - 1) / (64 * U);
+  a.segments = (pieces + 63) / 64;
   if (a.segments <= INT32_MAX) a.per_segment = FastDiv::of((uint32_t)a.segments);
   const int64_t side = 64 / a.lanes;  // rows side by side in a wavefront
   a.items = a.segments > 1 ? a.rows * a.segments : (a.rows + side - 1) / side;
-  int64_t grid = (a.items + kWaves - 1) / kWaves;
-  return (unsigned)(grid < (1 << 20) ? grid : (1 << 20));
-}
-
-template <int V>
-hipError_t dispatch_v(RowsArgs a, hipStream_t stream) {
-  constexpr int U = V == 16 ? 1 : 4;  // 4096 x 8 rows of 12 KB: 108 us; with 2 110, with 4 113
-  const unsigned grid = lay_out<U>(a, V);
-  hipLaunchKernelGGL((k_dispatch<V, U>), dim3(grid), dim3(kThreads), 0, stream, a);
+  const int64_t grid = (a.items + kWaves - 1) / kWaves;
+  hipLaunchKernelGGL((k_dispatch_backward<DT>), dim3((unsigned)(grid < (1 << 20) ? grid : (1 << 20))),
+                     dim3(kThreads), 0, stream, a);
   return hipGetLastError();
-}
-
-template <int DT, int V>
-hipError_t backward_v(RowsArgs a, hipStream_t stream) {
-  constexpr int U = 2;
-  const unsigned grid = lay_out<U>(a, V);
-  hipLaunchKernelGGL((k_dispatch_backward<DT, V, U>), dim3(grid), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
-}
-
-template <int DT>
-hipError_t backward_dt(const RowsArgs& a, hipStream_t stream) {
-  switch (piece_bytes(a)) {
-    case 16: return backward_v<DT, 16>(a, stream);
-    case 8: return backward_v<DT, 8>(a, stream);
-    case 4: return backward_v<DT, 4>(a, stream);
-    default: return backward_v<DT, Element<DT>::size>(a, stream);
-  }
 }
 
 template <bool F32>
@@ -342,20 +273,36 @@ hipError_t combine_backward_dt(const CombineBackwardArgs& a, hipStream_t stream)
 
 }  // namespace
 
-hipError_t launch_dispatch(const RowsArgs& a, hipStream_t stream) {
-  switch (piece_bytes(a)) {
-    case 16: return dispatch_v<16>(a, stream);
-    case 8: return dispatch_v<8>(a, stream);
-    case 4: return dispatch_v<4>(a, stream);
-    case 2: return dispatch_v<2>(a, stream);
-    default: return dispatch_v<1>(a, stream);
-  }
+hipError_t launch_dispatch(const RowsArgs& args, hipStream_t stream) {
+  RowsArgs a = args;
+  const int64_t pieces = (a.row_bytes + 15) / 16;
+  a.lanes = 64;
+  while (a.lanes > 1 && a.lanes / 2 >= pieces) a.lanes /= 2;
+  // By slices where a token has four rows or more (with three, 8192 x 3 of 12 KB, 95 us instead
+  // of 93): slices of which all tokens take half an L2 (4096 x 8 of 12 KB: 84 us, with a whole
+  // L2 87), but of two lines at least (16384 x 8 of 2 KB: 55 to 59 us with one, two and four),
+  // and of 1 KB where rows start inside lines, whose halves are written apart (4096 x 8 of
+  // 12 282 bytes: 155 us in slices of 512 bytes, 107 of 1 KB).
+  a.by_slice = a.rows >= 4 * a.source_rows;
+  const uint64_t starts = (uint64_t)reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ld_out;
+  if (a.by_slice && starts % 128 == 0)
+    while (a.lanes > 16 && a.source_rows * a.lanes * 16 > 2 << 20) a.lanes /= 2;
+  const int64_t slices = (pieces + a.lanes - 1) / a.lanes;
+  const int64_t rows = (int64_t)kWaves * (64 / a.lanes);
+  const int64_t groups = (a.rows + rows - 1) / rows;
+  a.items = slices * groups;
+  a.segments = a.by_slice ? groups : slices;
+  if (a.items <= INT32_MAX) a.per_segment = FastDiv::of((uint32_t)a.segments);
+  const int64_t share = (a.items + kXcds - 1) / kXcds;
+  const unsigned grid = kXcds * (unsigned)(share < (1 << 17) ? share : (1 << 17));
+  hipLaunchKernelGGL(k_dispatch, dim3(grid), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_dispatch_backward(const RowsArgs& a, hipStream_t stream) {
-  if (a.dtype == kInF32) return backward_dt<kInF32>(a, stream);
-  if (a.dtype == kInF16) return backward_dt<kInF16>(a, stream);
-  return backward_dt<kInBF16>(a, stream);
+  if (a.dtype == kInF32) return dispatch_backward_dt<kInF32>(a, stream);
+  if (a.dtype == kInF16) return dispatch_backward_dt<kInF16>(a, stream);
+  return dispatch_backward_dt<kInBF16>(a, stream);
 }
 
 hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t stream) {

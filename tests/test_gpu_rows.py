@@ -192,3 +192,42 @@ def test_there_and_back_against_autograd(drop):
     # drows is rounded to BF16 (2^-9) before it is summed.
     size = ((w * here).double().sum(1)[:, None] * dout.double().abs())
     ref.check(dx, gx, size * (2.0 ** -8 * 1.01 + (K + 1) * ref.U))
+
+
+@pytest.mark.parametrize("T,K,n,gap", [
+    (4099, 4, 1024, 0), (9001, 5, 1096, 56), (2053, 8, 200, 56), (4099, 3, 1024, 0), (3001, 4, 1021, 0)])
+def test_dispatch_of_many_tokens_copies_slice_by_slice(T, K, n, gap):
+    """Narrower slices than a row, rows that no slice divides, rows that start inside a line."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"dispatch slices {T} x {n} top-{K} gap={gap}")
+    g = torch.Generator().manual_seed(T)
+    row_token = torch.randint(-1, T + 1, (K * T,), generator=g, dtype=torch.int32).cuda()
+    x = torch.randn(T, n, generator=g).bfloat16().cuda()
+    out = torch.full((K * T, n + gap), 3.0, dtype=torch.bfloat16, device="cuda")
+    m.dispatch(x, row_token, out=out[:, :n])
+    there = (row_token >= 0) & (row_token < T)
+    want = torch.where(there[:, None], x[row_token.long().clamp(0, T - 1)], torch.zeros((), dtype=x.dtype, device="cuda"))
+    assert torch.equal(out[:, :n].contiguous().view(torch.int16), want.view(torch.int16))
+    assert (out[:, n:] == 3).all()
+
+
+def test_rows_past_32_bit_offsets():
+    """4.4 GB of rows, more workgroups than one launch has: every row, and the gradient of rows
+    on both sides of the border."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    T, M, n = 1000, 4_300_000, 512
+    say(f"dispatch {M} x {n}")
+    g = torch.Generator().manual_seed(5)
+    row_token = torch.randint(0, T, (M,), generator=g, dtype=torch.int32).cuda()
+    x = torch.randn(T, n, generator=g).bfloat16().cuda()
+    out = m.dispatch(x, row_token)
+    for i in range(0, M, 1 << 20):
+        part = slice(i, min(M, i + (1 << 20)))
+        assert torch.equal(out[part].view(torch.int16), x[row_token[part].long()].view(torch.int16)), i
+    token_rows = torch.tensor([[M - 1, 0], [2_200_000, M], [-1, M - 2]], dtype=torch.int32)
+    got = m.dispatch_backward(out, token_rows.cuda()).cpu().float()
+    pick = lambda r: out[r].cpu().float()  # noqa: E731
+    want = torch.stack([(pick(M - 1) + pick(0)).bfloat16().float(), pick(2_200_000), pick(M - 2)])
+    assert torch.equal(got, want)
