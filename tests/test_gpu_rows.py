@@ -231,3 +231,27 @@ def test_rows_past_32_bit_offsets():
     pick = lambda r: out[r].cpu().float()  # noqa: E731
     want = torch.stack([(pick(M - 1) + pick(0)).bfloat16().float(), pick(2_200_000), pick(M - 2)])
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,K,n", [(1030, 3, 48), (258, 9, 1040), (300, 2, 13008), (8200, 4, 2048)])
+def test_combine_backward_of_many_tokens(T, K, n):
+    """Beyond the few tokens whose rows several groups share; the last with rows read past the cache."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"combine_backward {T} x {n} top-{K}")
+    g = torch.Generator().manual_seed(T)
+    M = T * K - 5
+    token_rows = torch.randperm(T * K, generator=g).to(torch.int32).view(T, K)  # five slots without a row
+    rows = torch.randn(M, n, generator=g).bfloat16()
+    dout = torch.randn(T, n, generator=g).bfloat16()
+    weights = torch.rand(T, K, generator=g)
+    drows, dw = m.combine_backward(dout.cuda(), rows.cuda(), token_rows.cuda(), weights.cuda())
+    r, here = token_rows.long().clamp(max=M - 1), (token_rows < M)
+    prod = rows[r.view(-1)].double() * dout.double().repeat_interleave(K, 0)
+    want = torch.where(here, prod.sum(1).view(T, K), 0.0)
+    # A sum of n products, each rounded once: at most n roundings of a partial sum each.
+    assert ((dw.cpu().double() - want).abs() <= (n + 1) * ref.U * prod.abs().sum(1).view(T, K)).all()
+    pair = here.view(-1)
+    got = drows.cpu()[r.view(-1)[pair]]
+    exact = (weights.view(-1, 1) * dout.float().repeat_interleave(K, 0))[pair].bfloat16()
+    assert torch.equal(got, exact)
