@@ -182,8 +182,13 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     const uint32_t here = (uint32_t)b * 128u;
     const uint32_t at_w = b == kbs - 1 ? last_w : here, at_a = b == kbs - 1 ? last_a : here;
 #pragma unroll
-    for (int j = from; j < end; ++j)
+    for (int j = from; j < end; ++j) {
+      // Eight activation rows that are not there stay what they were: they reach only results that
+      // are not stored.  (Ragged experts of 273 rows on average 105 -> 101 us; but tiles of 64
+      // rows copy their last row again, 512 tokens of 256 experts 165 us, left out 172.)
+      if (MT >= 2 && j >= T::kWRounds && T::kRound * (j - T::kWRounds) + 8 * wave >= it.rows) continue;
       copy16(j < T::kWRounds ? w_now : a_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + (j < T::kWRounds ? at_w : at_a));
+    }
   };
   auto copy_scales = [&](float* to, int32_t b) { copy4(within(s_rs, b), to + 64 * wave, scale_off + (uint32_t)b * 4u); };
 
@@ -296,9 +301,18 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   for (int m = 0; m < MT; ++m) read_a(stages[0], a[0], m);
 #pragma unroll
   for (int t = 0; t < WD - 1; ++t) read_w(stages[0], t);
-  for (int32_t b = 0; b < kbs; b += 2) {
-    step(Index<0>{}, b);
-    if (b + 1 < kbs) step(Index<1>{}, b + 1);
+  if (16 * MT * wm < it.rows) {
+    for (int32_t b = 0; b < kbs; b += 2) {
+      step(Index<0>{}, b);
+      if (b + 1 < kbs) step(Index<1>{}, b + 1);
+    }
+  } else {  // no rows here: its copies, and the matrix core is another workgroup's (4096 tokens of 256 experts 260 -> 255 us)
+    for (int32_t b = 0; b < kbs; ++b) {
+      copy(stages[(b + 1) & 1], b + 1, 2 * kPart, T::kCopies);
+      stage_barrier();
+      copy(stages[b & 1], b + kRing, 0, 2 * kPart);
+      copy_scales(scales[b & 1], b + kRing);
+    }
   }
   // Nothing is on its way into LDS when the workgroup ends.
   stage_barrier();
