@@ -27,10 +27,9 @@ __device__ __forceinline__ int tile_row(int t, int i) { return 32 * (t >> 1) + 4
 __device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swz_w(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 
-// Stages in LDS.
-constexpr int kRing = 2;
 
-template <int WN, int WM, int MT>
+// R: stages in LDS.
+template <int WN, int WM, int MT, int R>
 struct Tile {
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
   static constexpr int BN = 128 * WN, BM = 16 * MT * WM;
@@ -73,11 +72,12 @@ __device__ __forceinline__ u32x4_t rsrc_words(const void* base, uint32_t bytes) 
                  (uint32_t)kRawBufferWord3};
 }
 
-// Everything this wavefront has read from LDS is in registers and what it copied there is complete;
-// then all wavefronts meet.
+// Everything this wavefront has read from LDS is in registers and what it copied there is complete,
+// but for its last LEFT copies; then all wavefronts meet.
+template <int LEFT>
 __device__ __forceinline__ void stage_barrier() {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 #endif
 }
 
@@ -118,13 +118,14 @@ struct Index {
   static constexpr int value = I;
 };
 
-template <int WN, int WM, int MT, bool EXACT>
+template <int WN, int WM, int MT, bool EXACT, int R>
 __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, MT >= 3 ? 2 : 4)))
 void k_gemm_fp8_tiled(Fp8GemmArgs p) {
-  typedef Tile<WN, WM, MT> T;
+  typedef Tile<WN, WM, MT, R> T;
+  static_assert(R == 2 || (R == 3 && MT == 1), "with three stages the copies of one are counted");
   constexpr int WD = T::WD, AD = T::AD;
-  __shared__ __align__(1024) uint8_t stages[kRing][T::kStage];
-  __shared__ __align__(1024) float scales[kRing][T::kScales];  // of the stages' activation rows
+  __shared__ __align__(1024) uint8_t stages[R][T::kStage];
+  __shared__ __align__(1024) float scales[R][T::kScales];  // of the stages' activation rows
   __shared__ Fp8Item place[2];
   __shared__ int32_t sums[T::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -223,9 +224,13 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   // them (8192^3: 486 us, with all behind the barrier 509); smaller tiles behind the barrier, since
   // what they wait for is the copies (4096 tokens of 256 experts: 259 us, spread 277).
   constexpr int kPart = MT >= 3 ? T::kCopies / 4 : T::kCopies / 2;
+  constexpr int kLeft = (R - 2) * (T::kCopies + 1);  // copies that may still be on their way
+  int i = 0;  // the stage's place
+  auto after = [](int x) { return x + 1 == R ? 0 : x + 1; };
   auto step = [&](auto which, int32_t b) {
     constexpr int S = decltype(which)::value;
-    uint8_t *const cur = stages[S], *const nxt = stages[1 - S];
+    if (R == 2) i = S;
+    uint8_t *const cur = stages[i], *const nxt = stages[after(i)];
     i32x8_t(&now_a)[MT] = a[S % AD];
     i32x8_t(&next_a)[MT] = a[(S + 1) % AD];
     if (b == kbs - 1 && k % kFp8Block != 0) {
@@ -240,7 +245,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     }
     float scale[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) scale[m] = scales[S][16 * (MT * wm + m) + r] * next_w;
+    for (int m = 0; m < MT; ++m) scale[m] = scales[i][16 * (MT * wm + m) + r] * next_w;
     next_w = ((sconst_f32)w_sf)[b + 1 < kbs ? b + 1 : b];
     operand_t ao[MT];
 #pragma unroll
@@ -249,7 +254,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     for (int t = 0; t < 8; ++t) {
       __builtin_amdgcn_sched_barrier(0);
       if (t == 6) {
-        stage_barrier();
+        stage_barrier<kLeft>();
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (AD == 2) {
 #pragma unroll
@@ -263,10 +268,10 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
         for (int j = 0; j < WD - 2; ++j) read_w(nxt, j);
       }
       if (t == 7) read_w(nxt, WD - 2);
-      if (t == 6) copy(cur, b + kRing, 0, kPart);
+      if (t == 6) copy(cur, b + R, 0, kPart);
       if (t == 7) {
-        copy(cur, b + kRing, kPart, 2 * kPart);
-        copy_scales(scales[S], b + kRing);
+        copy(cur, b + R, kPart, 2 * kPart);
+        copy_scales(scales[i], b + R);
       }
       if (t == 0) copy(nxt, b + 1, 2 * kPart, min(3 * kPart, T::kCopies));
       if (t == 1) copy(nxt, b + 1, 3 * kPart, T::kCopies);
@@ -290,13 +295,22 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int m = 0; m < MT; ++m) add_scaled(acc[7][m], d[m], scale[m]);
+    i = after(i);
   };
 
   copy(stages[0], 0, 0, T::kCopies);
   copy_scales(scales[0], 0);
-  stage_barrier();
-  copy(stages[1], 1, 0, 2 * kPart);
-  copy_scales(scales[1], 1);
+  if constexpr (R == 3) {  // every stage's copies are kCopies and one: none is left out
+    copy(stages[1], 1, 0, T::kCopies);
+    copy_scales(scales[1], 1);
+    stage_barrier<T::kCopies + 1>();
+    copy(stages[2], 2, 0, T::kCopies);
+    copy_scales(scales[2], 2);
+  } else {
+    stage_barrier<0>();
+    copy(stages[1], 1, 0, 2 * kPart);
+    copy_scales(scales[1], 1);
+  }
 #pragma unroll
   for (int m = 0; m < MT; ++m) read_a(stages[0], a[0], m);
 #pragma unroll
@@ -308,14 +322,15 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     }
   } else {  // no rows here: its copies, and the matrix core is another workgroup's (4096 tokens of 256 experts 260 -> 255 us)
     for (int32_t b = 0; b < kbs; ++b) {
-      copy(stages[(b + 1) & 1], b + 1, 2 * kPart, T::kCopies);
-      stage_barrier();
-      copy(stages[b & 1], b + kRing, 0, 2 * kPart);
-      copy_scales(scales[b & 1], b + kRing);
+      copy(stages[after(i)], b + 1, 2 * kPart, T::kCopies);
+      stage_barrier<kLeft>();
+      copy(stages[i], b + R, 0, 2 * kPart);
+      copy_scales(scales[i], b + R);
+      i = after(i);
     }
   }
   // Nothing is on its way into LDS when the workgroup ends.
-  stage_barrier();
+  stage_barrier<0>();
 
   // Where there is no row or column a store is sent out of range.
   constexpr int es = EXACT ? 4 : 2;
@@ -361,23 +376,26 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   }
 }
 
-template <int WN, int WM, int MT, bool EXACT>
+template <int WN, int WM, int MT, bool EXACT, int R>
 hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
-  typedef Tile<WN, WM, MT> T;
+  typedef Tile<WN, WM, MT, R> T;
   p.n_tiles = (p.n + T::BN - 1) / T::BN;
   // Columns that can be stored together everywhere: 8 (16-bit results) or 4 of them in one piece.
   const uint64_t es = EXACT ? 4 : 2, where = reinterpret_cast<uintptr_t>(p.out) | (uint64_t)p.ldo * es;
   p.store_cols = where % 16 == 0 && p.n % 8 == 0 ? 8 : where % (4 * es) == 0 && p.n % 4 == 0 ? 4 : 1;
   const int64_t items = (fp8_most_items(p, T::BM) + 7) / 8 * 8, row = 1 << 16;
   const dim3 grid = items <= row ? dim3((unsigned)items) : dim3((unsigned)row, (unsigned)((items + row - 1) / row));
-  hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, EXACT>), grid, dim3(T::kThreads), 0, stream, p);
+  hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, EXACT, R>), grid, dim3(T::kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
 // The tile by the average rows of an expert; both sides in us:
 //   64 x 128 below 96 rows (the down projection, 6144 x 256, 32 rows: 136 against 176 with 128 x
 //     128), and while 128 x 128 would leave CUs without two workgroups (dense 8192 x 6144, 256
-//     rows: 33 against 39);
+//     rows: 33 against 39); with three stages in LDS, two workgroups a CU instead of three, from
+//     32 blocks (512 tokens of 256 experts, K = 6144: 154 against 165 with two stages; K = 4096:
+//     190 and 192; K = 1024: 113 and 111; the down projection's two blocks: 134 and 116; FP32
+//     results the same);
 //   256 x 256 from 384 rows (8 experts of 8192 x 4096, 512 rows: 208 against 223 with 128 x 128;
 //     1024 rows: 342 against 414; 64 experts of 2048 x 4096, 256 rows: 260 against 253) where they
 //     fill most of a round of 256 CUs (dense 8192^2, 2048 rows: 134 against 179; 8192 x 4096, 2500
@@ -387,11 +405,12 @@ template <bool EXACT>
 hipError_t launch_sized(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts, avg = p.m_total / p.experts;
   const int64_t middle = (p.m_total / 128 + experts) * ((p.n + 127) / 128);
-  if (avg < 96 || middle < 512) return launch<1, 4, 1, EXACT>(p, stream);
+  if (avg < 96 || middle < 512)
+    return !EXACT && p.k_blocks >= 32 ? launch<1, 4, 1, false, 3>(p, stream) : launch<1, 4, 1, EXACT, 2>(p, stream);
   const int64_t big = (p.m_total + 255) / 256 * ((p.n + 255) / 256), rest = big % 256;
   if (!EXACT && avg >= 384 && big >= 224 && (rest == 0 || rest >= 160 || big >= 1024))
-    return launch<2, 4, 4, false>(p, stream);
-  return launch<1, 4, 2, EXACT>(p, stream);
+    return launch<2, 4, 4, false, 2>(p, stream);
+  return launch<1, 4, 2, EXACT, 2>(p, stream);
 }
 
 }  // namespace

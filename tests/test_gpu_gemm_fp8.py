@@ -238,3 +238,20 @@ def test_replayed_graph_follows_its_inputs():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, m.grouped_gemm_fp8(*ops, off))
+
+
+@pytest.mark.parametrize("counts,n,k,gather", [
+    ([70, 0, 128, 33, 64, 65, 150, 1, 17, 200, 90, 22], 1156, 4112, False),
+    ([5, 16, 64, 0, 48, 31, 130, 12] * 2, 1160, 4096, True), ([60] * 12, 1032, 4240, True)])
+def test_long_products_of_small_experts(counts, n, k, gather):
+    """Tiles of 64 rows with three stages in LDS: counts of blocks of every remainder by three."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"grouped_gemm_fp8 {len(counts)} experts n={n} k={k} gather={gather}")
+    offsets = np.concatenate(([0], np.cumsum(counts)))
+    M = int(offsets[-1])
+    rows = 77 if gather else M
+    a, sa, w, sw = operands(n + k, rows, len(counts), n, k)
+    index = np.random.default_rng(k).integers(0, rows, M) if gather else None
+    out = m.grouped_gemm_fp8(*on_gpu(a, sa, w, sw), i32(offsets), a_row_index=i32(index) if gather else None)
+    ref.check(out, *expected(a, sa, w, sw, offsets, index, eight_bit=True), counts)
