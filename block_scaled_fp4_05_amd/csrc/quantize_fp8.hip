@@ -167,8 +167,9 @@ __global__ __launch_bounds__(kPairThreads) void k_quantize_fp8_swiglu_grad(Fp8Qu
   uint32_t* const low = top + r * kbs + c / kFp8Block;
   uint32_t* const high = top + r * kbs + (half + c) / kFp8Block;
   if (in) {
-    atomicMax(low, __builtin_bit_cast(uint32_t, amax8(dg)));
-    atomicMax(high, __builtin_bit_cast(uint32_t, amax8(du)));
+    // (Eight NaN have a NaN for their largest, above every number as an integer: it counts as 0.)
+    atomicMax(low, __builtin_bit_cast(uint32_t, fmaxf(amax8(dg), 0.0f)));
+    atomicMax(high, __builtin_bit_cast(uint32_t, fmaxf(amax8(du), 0.0f)));
   }
   __syncthreads();
   if (in) {

@@ -136,3 +136,22 @@ def test_weights_with_an_odd_number_of_rows():
     _same(*m.quantize_fp8_weights(w.cuda()), *ref.quantize(w.float().numpy(), 128))
     with pytest.raises(m.MoeFp4Error, match="sizes"):
         m.quantize_fp8_weights(w.cuda(), transposed=True)
+
+
+@pytest.mark.parametrize("k", [128, 1424, 8320])
+def test_a_run_of_nan_gradients_leaves_its_blocks_scales_alone(k):
+    """Eight NaN that one thread holds, in blocks with numbers, in both halves."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"quantize_fp8 swiglu gradient with NaN, k={k}")
+    g = torch.Generator().manual_seed(k)
+    x, d = torch.randn(3, 2 * k, generator=g), torch.randn(3, k, generator=g)
+    d[1, 16:24] = float("nan")
+    q, s = m.quantize_fp8(x.cuda(), swiglu=True, grad=d.cuda())
+    hole = torch.zeros(3, 2 * k, dtype=torch.bool)
+    hole[1, 16:24] = hole[1, k + 16:k + 24] = True
+    assert torch.equal(q.cpu().float().isnan(), hole)
+    # The scales are those of zeros in the NaN's place.
+    q0, s0 = m.quantize_fp8(x.cuda(), swiglu=True, grad=torch.nan_to_num(d, nan=0.0).cuda())
+    assert torch.equal(s, s0)
+    assert torch.equal(q.cpu().view(torch.uint8)[~hole], q0.cpu().view(torch.uint8)[~hole])
