@@ -67,7 +67,8 @@ int moe_fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t k, int64
   if (rows == 0) return MOE_FP4_OK;
   const int64_t xb = extent(rows, in_cols, ld_x, es), gb = grad ? extent(rows, k, ld_grad, es) : 0;
   if (xb < 0 || gb < 0) return MOE_FP4_ERR_SHAPE;
-  if (rows > ((int64_t)INT32_MAX - (1 << 17)) / blocks(cols)) return MOE_FP4_ERR_UNSUPPORTED;
+  // Eight threads or fewer a block, fewer than 2^32 in a launch.
+  if (rows > ((1 << 29) - (1 << 17)) / blocks(cols)) return MOE_FP4_ERR_UNSUPPORTED;
   const Range r[] = {{x, xb}, {grad, gb}, {q, rows * cols}, {sf, rows * blocks(cols) * 4}};
   if (clash(r, 2)) return MOE_FP4_ERR_ARG;
   moe_fp4::Fp8QuantArgs a;

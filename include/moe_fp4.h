@@ -501,7 +501,8 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
  * has an infinite scale and stands for NaN throughout.
  *   swiglu = 0               v = x, k columns.
  *   swiglu = 1, grad NULL    x has 2k columns, gate and up: v = silu(gate) * up, k columns, in
- *                            FP32, silu(g) = g / (1 + e^-g).
+ *                            FP32, silu(g) = g / (1 + e^-g), e^-g taken for g within +-88 (so
+ *                            an infinite gate, of either sign, stands for an infinity).
  *   swiglu = 1, grad         its gradient, 2k columns: v = [grad * up * s (1 + gate (1 - s)) |
  *                            grad * silu(gate)], s = 1 / (1 + e^-gate), in FP32; the blocks run
  *                            over all 2k columns.
@@ -512,7 +513,7 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
  * Deterministic.
  * Errors: NULL, SHAPE (rows < 0, k < 1, k % 16, a pitch below its row), ALIGN, ARG (in_dtype,
  * swiglu or power_of_two not 0 or 1, grad without swiglu, q or sf overlapping another buffer),
- * UNSUPPORTED (about 2^31 blocks or more, k > 2^29 - 1024), HIP.
+ * UNSUPPORTED (2^29 - 2^17 blocks or more, k > 2^29 - 1024), HIP.
  */
 int moe_fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t k, int64_t ld_x, int swiglu,
                      const void* grad, int64_t ld_grad, int power_of_two, uint8_t* q, float* sf,
@@ -542,8 +543,8 @@ int moe_fp8_quantize_weights(const void* w, int in_dtype, int32_t num_experts, i
  *     src(r) = a_row_index ? a_row_index[r] : r
  *
  * Blocks are summed in FP32 and the result is rounded once, to out_dtype, nearest even.  Inside a
- * block the products are exact and their sum FP32 for an FP32 out and for experts of few
- * rows; for a 16-bit out, experts of many rows use the FP8 matrix cores, which cut each of eight
+ * block the products are exact and their sum FP32 for an FP32 out and for small problems (few
+ * rows an expert, or few tiles); the others use the FP8 matrix cores, which cut each of eight
  * consecutive products 13 bits below the leading bit of the largest of them (about 1.5e-5 of a
  * result on Gaussian data, against a rounding of 2^-9 or 2^-12).  Deterministic.  Columns
  * >= n and rows outside [off[0], off[E]) are not written; an empty expert writes nothing.
@@ -574,7 +575,7 @@ int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
  * The grouped GEMMs gather their rows by themselves; this is for rows that travel (send
  * buffers of expert parallelism) or that other code reads.
  *   x, out     device, [tokens][ld_x] and [m_total][ldo] of dtype (MOE_FP4_IN_*), aligned to the
- *              element (widest accesses where both bases and pitches are multiples of 16 bytes).
+ *              element (fastest where out's rows start at multiples of 128 bytes).
  *   row_token  device, [m_total] int32, any values.
  * Columns >= n of out are not touched.  m_total == 0 is a no-op.
  * Errors: NULL, SHAPE (tokens or m_total < 0, n < 1, a pitch below n), ALIGN, ARG (dtype, out

@@ -199,3 +199,12 @@ def test_expanded_rows_are_refused():
     x = torch.zeros(1, 32, dtype=BF16).expand(4, 32)
     assert m._pitch(x, "x", BF16, (4, 32)) == 0
     assert m.quantize_fp8_raw(_at(0), 0, 4, 32, 0, 0, None, 0, 0, _at(1), _at(2), None) == SHAPE
+
+
+def test_quantize_refuses_more_blocks_than_a_launch_has_threads_for():
+    """2^29 - 2^17 blocks of 128 and fewer pass the checks (rows of one block at addresses that
+    overlap are refused behind that check)."""
+    one = dict(QUANT, k=16, ld_x=16, swiglu=0, grad=None, ld_grad=0)
+    most = 2 ** 29 - 2 ** 17
+    assert m.quantize_fp8_raw(*dict(one, rows=most + 1).values()) == UNSUPPORTED
+    assert m.quantize_fp8_raw(*dict(one, rows=most, q=one["x"]).values()) == ARG
