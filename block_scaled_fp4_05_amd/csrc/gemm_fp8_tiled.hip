@@ -133,10 +133,12 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, kbs = p.k_blocks, n = p.n;
 
+  if (threadIdx.x == 0) place[0] = Fp8Item{0, 0, 0, 0};
   const Fp8Locator<T::kThreads> locator(p, T::BM, T::BN, 4, sums);
   if (locator.count == 0) return;
   locator.batch(0, 1, place);
   const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0)};
+  if (it.rows <= 0) return;  // not found: offsets that decrease
 
   // ---- copies: this thread moves piece lane % 8 of rows tid / 8 + kRound * j, swizzled, and
   // wavefront w the scales of activation rows 64 w ...

@@ -255,3 +255,18 @@ def test_long_products_of_small_experts(counts, n, k, gather):
     index = np.random.default_rng(k).integers(0, rows, M) if gather else None
     out = m.grouped_gemm_fp8(*on_gpu(a, sa, w, sw), i32(offsets), a_row_index=i32(index) if gather else None)
     ref.check(out, *expected(a, sa, w, sw, offsets, index, eight_bit=True), counts)
+
+
+@pytest.mark.parametrize("E,M,n,k", [(8192, 700, 160, 16), (64, 400, 400, 272), (6, 900, 1160, 4112)])
+def test_offsets_that_go_back_and_forth_stay_inside(E, M, n, k):
+    """Far more rows in all than there are: which of them are computed is open, rows behind the last
+    one and columns past n stay."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"grouped_gemm_fp8 offsets back and forth, {E} experts")
+    off = np.zeros(E + 1, dtype=np.int32)
+    off[1::2] = M
+    ops = on_gpu(*operands(E, M, E, n, k))
+    out = torch.full((M + 300, n + 8), 7.0, device="cuda")
+    m.grouped_gemm_fp8(*ops, i32(off), out=out[:M, :n])
+    assert (out[M:] == 7).all() and (out[:, n:] == 7).all() and out.isfinite().all()
