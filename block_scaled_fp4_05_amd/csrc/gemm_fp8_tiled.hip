@@ -118,6 +118,55 @@ struct Index {
   static constexpr int value = I;
 };
 
+// A wavefront's 16 MT x 128 results into `out`, from row row0 (rows of which there are) and column
+// col0 on.  Where there is no row or column a store is sent out of range.
+template <int MT, bool EXACT>
+__device__ __forceinline__ void store_tile(const Fp8GemmArgs& p, const float4_t (&acc)[8][MT], int32_t row0, int32_t rows,
+                                           int32_t first, int32_t col0, int r, int g) {
+  const int32_t n = p.n;
+  constexpr int es = EXACT ? 4 : 2;
+  const rsrc_t o = make_rsrc(static_cast<char*>(p.out) + (int64_t)row0 * p.ldo * es, (uint32_t)rows * (uint32_t)p.ldo * es);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int32_t row = first + 16 * m + r;
+    const uint32_t row_at = (uint32_t)row * (uint32_t)p.ldo;
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) {
+      const int32_t col = col0 + tile_row(t, 4 * g);
+      const uint32_t to = row < rows && col < n ? (row_at + (uint32_t)col) * es : kOutOfRange;
+      const u32x4_t v = fp8_round8(acc[t][m], acc[t + 1][m], p.out_dtype);
+      if (p.store_cols == 8) {
+        if constexpr (EXACT) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][m]), o, to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t + 1][m]), o, to, 16, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128(v, o, to, 0, 0);
+        }
+      } else if (p.store_cols == 4) {
+        const uint32_t to_hi = col + 4 < n ? to + 4 * es : kOutOfRange;
+        if constexpr (EXACT) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][m]), o, to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t + 1][m]), o, to_hi, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{v[0], v[1]}, o, to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{v[2], v[3]}, o, to_hi, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t to_i = col + i < n ? to + i * es : kOutOfRange;
+          if constexpr (EXACT) {
+            const float f = i < 4 ? acc[t][m][i & 3] : acc[t + 1][m][i & 3];
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f), o, to_i, 0, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[i >> 1] >> (16 * (i & 1))), o, to_i, 0, 0);
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int WN, int WM, int MT, bool EXACT, int R>
 __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, MT >= 3 ? 2 : 4)))
 void k_gemm_fp8_tiled(Fp8GemmArgs p) {
@@ -334,80 +383,220 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   // Nothing is on its way into LDS when the workgroup ends.
   stage_barrier<0>();
 
-  // Where there is no row or column a store is sent out of range.
-  constexpr int es = EXACT ? 4 : 2;
-  const rsrc_t o = make_rsrc(static_cast<char*>(p.out) + (int64_t)it.row0 * p.ldo * es, (uint32_t)it.rows * (uint32_t)p.ldo * es);
+  store_tile<MT, EXACT>(p, acc, it.row0, it.rows, 16 * MT * wm, it.n0 + 128 * wn, r, g);
+}
+
+// Products of KB blocks, up to four: a workgroup keeps its 64 MT activation rows in registers and
+// runs along `span` tiles of 128 weight rows, a stage in LDS being one block of a tile.
+// Rows are found, read and scaled once and the copies never stop, where the kernel above spends
+// most of a short item on its start and its end.
+constexpr int kShortRing = 3;
+
+template <int KB, int MT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 3)))
+void k_gemm_fp8_short(Fp8GemmArgs p) {
+  constexpr int R = kShortRing, kCopies = 4, WD = 4;
+  __shared__ __align__(1024) uint8_t stages[R][128 * 128];
+  __shared__ Fp8Item place[2];
+  __shared__ int32_t sums[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int32_t k = p.k, n = p.n;
+
+  if (threadIdx.x == 0) place[0] = Fp8Item{0, 0, 0, 0};
+  const Fp8Locator<256> locator(p, 64 * MT, 128 * p.span, 4, sums);
+  if (locator.count == 0) return;
+  locator.batch(0, 1, place);
+  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0)};
+  if (it.rows <= 0) return;  // not found: offsets that decrease
+  const int32_t tiles = min(p.span, (n - it.n0 + 127) / 128), all = tiles * KB;
+
+  // ---- copies of weights, as in the kernel above
+  const int piece = (lane & 7) ^ swz_w(tid >> 3);
+  const u32x4_t w_rs = rsrc_words(p.w_q + (int64_t)it.e * n * k, (uint32_t)n * (uint32_t)k);
+  // Block b's (static) piece; one past k is copied from the row's start (its products are zero).
+  auto copy = [&](uint8_t* to, int b, int32_t tile) {
+    const u32x4_t now = u32x4_t{w_rs[0], w_rs[1], tile < tiles ? w_rs[2] : 0u, w_rs[3]};
+    const int32_t at = b * 128 + 16 * piece;
+    const uint32_t in_row = at < k ? (uint32_t)at : 0u;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int32_t row = 16 * (MT * wm + m) + r;
-    const uint32_t row_at = (uint32_t)row * (uint32_t)p.ldo;
+    for (int j = 0; j < kCopies; ++j) {
+      const int32_t row = min(it.n0 + 128 * tile + (tid >> 3) + 32 * j, n - 1);
+      copy16(now, to + (32 * j + 8 * wave) * 128, (uint32_t)row * (uint32_t)k + in_row);
+    }
+  };
 #pragma unroll
-    for (int t = 0; t < 8; t += 2) {
-      const int32_t col = it.n0 + 128 * wn + tile_row(t, 4 * g);
-      const uint32_t to = row < it.rows && col < n ? (row_at + (uint32_t)col) * es : kOutOfRange;
-      const u32x4_t v = fp8_round8(acc[t][m], acc[t + 1][m], p.out_dtype);
-      if (p.store_cols == 8) {
-        if constexpr (EXACT) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][m]), o, to, 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t + 1][m]), o, to, 16, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b128(v, o, to, 0, 0);
-        }
-      } else if (p.store_cols == 4) {
-        const uint32_t to_hi = col + 4 < n ? to + 4 * es : kOutOfRange;
-        if constexpr (EXACT) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t][m]), o, to, 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[t + 1][m]), o, to_hi, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{v[0], v[1]}, o, to, 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{v[2], v[3]}, o, to_hi, 0, 0);
-        }
-      } else {
+  for (int s = 0; s < R; ++s) copy(stages[s], s % KB, s / KB);
+
+  // ---- this wavefront's rows; the pieces past k are zeros
+  const bool live = 16 * MT * wave < it.rows;
+  i32x8_t a[KB][MT];
+  float sa[KB][MT];
+  if (live) {
+    const int64_t base = p.a_row_index ? 0 : it.row0, a_rows = p.a_row_index ? p.a_rows : (int64_t)it.rows;
+    const rsrc_t a_rs = make_rsrc(p.a_q + base * k, (uint32_t)(a_rows * k));
+    const rsrc_t s_rs = make_rsrc(p.a_sf + base * KB, (uint32_t)(a_rows * KB * 4));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t to_i = col + i < n ? to + i * es : kOutOfRange;
-          if constexpr (EXACT) {
-            const float f = i < 4 ? acc[t][m][i & 3] : acc[t + 1][m][i & 3];
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f), o, to_i, 0, 0);
-          } else {
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[i >> 1] >> (16 * (i & 1))), o, to_i, 0, 0);
-          }
-        }
+    for (int m = 0; m < MT; ++m) {
+      int32_t row = min(16 * (MT * wave + m) + r, it.rows - 1);
+      if (p.a_row_index) row = min(max(p.a_row_index[it.row0 + row], 0), (int32_t)p.a_rows - 1);
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const int32_t at = 128 * b + 16 * g;
+        const uint32_t from = (uint32_t)row * (uint32_t)k + (uint32_t)at;
+        const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(a_rs, at < k ? from : kOutOfRange, 0, 0);
+        const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(a_rs, at + 64 < k ? from + 64 : kOutOfRange, 0, 0);
+        a[b][m] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        sa[b][m] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(s_rs, (uint32_t)(row * KB + b) * 4u, 0, 0));
       }
     }
   }
+
+  // ---- products
+  const float* const w_sf = p.w_sf + ((int64_t)it.e * p.n_blocks + it.n0 / kFp8Block) * KB;  // of stage s at s
+  const int at_w = tile_row(0, r) * 128 + 16 * (g ^ (r >> 1));
+  i32x8_t w[WD];
+  auto read_w = [&](const uint8_t* from, int t) {
+    const uint8_t* const row = from + tile_row(t, 0) * 128;
+    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(row + at_w);
+    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(row + (at_w ^ 64));
+    w[t % WD] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+  auto after = [](int x) { return x + 1 == R ? 0 : x + 1; };
+  float4_t acc[8][MT], d[MT];
+  float next_w = ((sconst_f32)w_sf)[0];
+  int i = 0;  // the stage's place
+  // (What a wavefront has loaded for itself is older than the copies that may still be on their way.)
+  auto step = [&](auto which, int32_t tile) {
+    constexpr int b = decltype(which)::value;
+    uint8_t *const cur = stages[i], *const nxt = stages[after(i)];
+    const int32_t s = tile * KB + b;
+    float scale[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) scale[m] = sa[b][m] * next_w;
+    next_w = ((sconst_f32)w_sf)[s + 1 < all ? s + 1 : s];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (t == 6) {
+        stage_barrier<(R - 2) * kCopies>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const i32x8_t wo = w[t % WD];
+      if (t + WD - 1 < 8) read_w(cur, t + WD - 1);
+      if (t == 6) {
+#pragma unroll
+        for (int j = 0; j < WD - 2; ++j) read_w(nxt, j);
+        copy(cur, (b + R) % KB, tile + (b + R) / KB);
+      }
+      if (t == 7) read_w(nxt, WD - 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float4_t now = fp8_block_product(wo, a[b][m]);
+        if (t > 0) add_scaled(acc[t - 1][m], d[m], scale[m]);
+        d[m] = now;
+      }
+      interleave<MT>();
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) add_scaled(acc[7][m], d[m], scale[m]);
+    i = after(i);
+  };
+  stage_barrier<0>();
+  if (live) {
+#pragma unroll
+    for (int t = 0; t < WD - 1; ++t) read_w(stages[0], t);
+    for (int32_t tile = 0; tile < tiles; ++tile) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      step(Index<0>{}, tile);
+      if constexpr (KB > 1) step(Index<1>{}, tile);
+      if constexpr (KB > 2) step(Index<2>{}, tile);
+      if constexpr (KB > 3) step(Index<3>{}, tile);
+      store_tile<MT, false>(p, acc, it.row0, it.rows, 16 * MT * wave, it.n0 + 128 * tile, r, g);
+    }
+  } else {
+    for (int32_t tile = 0; tile < tiles; ++tile)
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        stage_barrier<(R - 2) * kCopies>();
+        copy(stages[i], (b + R) % KB, tile + (b + R) / KB);
+        i = after(i);
+      }
+  }
+  // Nothing is on its way into LDS when the workgroup ends.
+  stage_barrier<0>();
+}
+
+// Sets how results are stored; workgroups for every tile of bm rows.
+dim3 fp8_grid(Fp8GemmArgs& p, int bm, uint64_t es) {
+  // Columns that can be stored together everywhere: 8 (16-bit results) or 4 of them in one piece.
+  const uint64_t where = reinterpret_cast<uintptr_t>(p.out) | (uint64_t)p.ldo * es;
+  p.store_cols = where % 16 == 0 && p.n % 8 == 0 ? 8 : where % (4 * es) == 0 && p.n % 4 == 0 ? 4 : 1;
+  const int64_t items = (fp8_most_items(p, bm) + 7) / 8 * 8, row = 1 << 16;
+  return items <= row ? dim3((unsigned)items) : dim3((unsigned)row, (unsigned)((items + row - 1) / row));
 }
 
 template <int WN, int WM, int MT, bool EXACT, int R>
 hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
   typedef Tile<WN, WM, MT, R> T;
   p.n_tiles = (p.n + T::BN - 1) / T::BN;
-  // Columns that can be stored together everywhere: 8 (16-bit results) or 4 of them in one piece.
-  const uint64_t es = EXACT ? 4 : 2, where = reinterpret_cast<uintptr_t>(p.out) | (uint64_t)p.ldo * es;
-  p.store_cols = where % 16 == 0 && p.n % 8 == 0 ? 8 : where % (4 * es) == 0 && p.n % 4 == 0 ? 4 : 1;
-  const int64_t items = (fp8_most_items(p, T::BM) + 7) / 8 * 8, row = 1 << 16;
-  const dim3 grid = items <= row ? dim3((unsigned)items) : dim3((unsigned)row, (unsigned)((items + row - 1) / row));
+  const dim3 grid = fp8_grid(p, T::BM, EXACT ? 4 : 2);
   hipLaunchKernelGGL((k_gemm_fp8_tiled<WN, WM, MT, EXACT, R>), grid, dim3(T::kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
+template <int KB, int MT>
+hipError_t launch_short(Fp8GemmArgs p, hipStream_t stream) {
+  p.n_tiles = (p.n + 128 * p.span - 1) / (128 * p.span);
+  const dim3 grid = fp8_grid(p, 64 * MT, 2);
+  hipLaunchKernelGGL((k_gemm_fp8_short<KB, MT>), grid, dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int MT>
+hipError_t launch_short_sized(const Fp8GemmArgs& p, hipStream_t stream) {
+  switch (p.k_blocks) {
+    case 1: return launch_short<1, MT>(p, stream);
+    case 2: return launch_short<2, MT>(p, stream);
+    case 3: return launch_short<3, MT>(p, stream);
+    default: return launch_short<4, MT>(p, stream);
+  }
+}
+
 // The tile by the average rows of an expert; both sides in us:
-//   64 x 128 below 96 rows (the down projection, 6144 x 256, 32 rows: 136 against 176 with 128 x
-//     128), and while 128 x 128 would leave CUs without two workgroups (dense 8192 x 6144, 256
+//   64 x 128 below 96 rows (6144 x 256, 32 rows: 136 against 176 with 128 x 128), and while 128 x 128 would leave CUs without two workgroups (dense 8192 x 6144, 256
 //     rows: 33 against 39); with three stages in LDS, two workgroups a CU instead of three, from
 //     32 blocks (512 tokens of 256 experts, K = 6144: 154 against 165 with two stages; K = 4096:
-//     190 and 192; K = 1024: 113 and 111; the down projection's two blocks: 134 and 116; FP32
-//     results the same);
+//     190 and 192; K = 1024: 113 and 111; FP32 results the same);
 //   256 x 256 from 384 rows (8 experts of 8192 x 4096, 512 rows: 208 against 223 with 128 x 128;
 //     1024 rows: 342 against 414; 64 experts of 2048 x 4096, 256 rows: 260 against 253) where they
 //     fill most of a round of 256 CUs (dense 8192^2, 2048 rows: 134 against 179; 8192 x 4096, 2500
 //     rows, 320 tiles: 123 against 106);
 //   128 x 128 else (4096 tokens of 256 experts: 269 against 276 with 64 x 128).
+//   Up to four blocks the workgroups that run along the weights' tiles, of 64 or 128 rows as above,
+//     four tiles each or, so that there are 512 at least, two or three (the down projection 92
+//     against 117, of 4096 tokens 171 against 274; K = 512: 170 against 187 and 249 against 349;
+//     dense 8192 x 8192 x 256 37 against 44; with eight tiles 96, 177, 175, 253 and 34); below 1024
+//     tiles those above (dense 4096 x 256, 512 rows: 6.7 against 8.4).
 template <bool EXACT>
 hipError_t launch_sized(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts, avg = p.m_total / p.experts;
   const int64_t middle = (p.m_total / 128 + experts) * ((p.n + 127) / 128);
-  if (avg < 96 || middle < 512)
+  const bool low = avg < 96 || middle < 512;
+  if (!EXACT && p.k_blocks <= 4) {
+    const int64_t tiles = (p.m_total / (low ? 64 : 128) + experts) * ((p.n + 127) / 128);
+    if (tiles >= 1024) {
+      Fp8GemmArgs a = p;
+      a.span = tiles < 2048 ? (int32_t)(tiles / 512) : 4;
+      return low ? launch_short_sized<1>(a, stream) : launch_short_sized<2>(a, stream);
+    }
+  }
+  if (low)
     return !EXACT && p.k_blocks >= 32 ? launch<1, 4, 1, false, 3>(p, stream) : launch<1, 4, 1, EXACT, 2>(p, stream);
   const int64_t big = (p.m_total + 255) / 256 * ((p.n + 255) / 256), rest = big % 256;
   if (!EXACT && avg >= 384 && big >= 224 && (rest == 0 || rest >= 160 || big >= 1024))

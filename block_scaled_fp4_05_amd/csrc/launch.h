@@ -292,6 +292,7 @@ struct Fp8GemmArgs {
   int32_t vec4;       // four consecutive columns may be stored together
   // Set by the launchers: N-tiles of an expert, and the columns that are stored together.
   int32_t n_tiles = 0, store_cols = 1;
+  int32_t span = 1;  // (short products) tiles of a workgroup
 };
 hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& args, hipStream_t stream);
 hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& p, hipStream_t stream);

@@ -270,3 +270,30 @@ def test_offsets_that_go_back_and_forth_stay_inside(E, M, n, k):
     out = torch.full((M + 300, n + 8), 7.0, device="cuda")
     m.grouped_gemm_fp8(*ops, i32(off), out=out[:M, :n])
     assert (out[M:] == 7).all() and (out[:, n:] == 7).all() and out.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("k", [16, 112, 128, 240, 384, 400, 512])
+@pytest.mark.parametrize("E,avg,n,gather", [(40, 30, 3000, True), (24, 150, 4004, False), (1, 700, 16400, False)])
+def test_short_products_with_many_tiles(E, avg, n, gather, k, dtype):
+    """Workgroups that run along the weights' tiles: one to four blocks, the last one whole or not,
+    uneven experts, spans that end inside the matrix; rows and columns outside are left."""
+    require_gpu()
+    from block_scaled_fp4_05_amd import moe_fp4 as m
+    say(f"grouped_gemm_fp8 short {E} experts of {avg} rows, {n} x {k} gather={gather} {dtype}")
+    rng = np.random.default_rng(E + k)
+    counts = rng.multinomial(E * avg, rng.dirichlet(np.full(E, 3.0)))
+    if E > 1:
+        counts[1] = 0
+    offsets = np.concatenate(([0], np.cumsum(counts)))
+    M = int(offsets[-1])
+    rows = 211 if gather else M
+    a, sa, w, sw = operands(E + k, rows, E, n, k)
+    sa, sw = sa * np.float32(2.0 ** -6), sw * np.float32(2.0 ** -6)
+    index = rng.integers(0, rows, M) if gather else None
+    out = torch.full((M + 3, n + 8), 7.0, dtype=ref.DT[dtype], device="cuda")
+    m.grouped_gemm_fp8(*on_gpu(a, sa, w, sw), i32(offsets), a_row_index=i32(index) if gather else None,
+                       out=out[:M, :n])
+    at = (lambda x: x[index]) if gather else (lambda x: x)
+    check_sampled(out[:M, :n], at(a), at(sa), w, sw, offsets, True, E + k)
+    assert (out[M:] == 7).all() and (out[:, n:] == 7).all()
