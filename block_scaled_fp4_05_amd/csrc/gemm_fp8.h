@@ -64,6 +64,7 @@ struct Fp8Item {
   int32_t row0;  // first result row
   int32_t rows;  // valid rows of the tile
   int32_t n0;    // first result column
+  int32_t once;  // whether these are all rows of the expert, so that its weights are read once
 };
 
 // Items of an expert of cnt rows (none for a decreasing pair of offsets).
@@ -170,7 +171,7 @@ struct Fp8Locator {
           nt = within / tall;
           mt = b * band + within - nt * tall;
         }
-        ring[j % (2 * n)] = Fp8Item{e, at + mt * bm, min(bm, rows - mt * bm), nt * bn};
+        ring[j % (2 * n)] = Fp8Item{e, at + mt * bm, min(bm, rows - mt * bm), nt * bn, mts == 1};
       }
       first += items;
       at = next;

@@ -2,7 +2,7 @@
 // (moe_grouped_gemm_fp8), tiles of BM activation rows x BN weight rows a workgroup.
 //
 // Bound: the matrix cores for large dense products (8192^3: 488-512 us, 2.2 PFLOP/s), the weight stream
-// for experts of some 16 rows (512 tokens of 256 experts of 512 x 6144: 150 us, 5.4 TB/s), the copies'
+// for experts of some 16 rows (512 tokens of 256 experts of 512 x 6144: 139 us, 5.9 TB/s), the copies'
 // requests between them (60 experts of 273 rows, 1444 x 1552: 99 us).  A stage is one block of 128
 // of every row of the tile, copied from memory straight into LDS (no registers) while the stage before
 // it is multiplied.
@@ -47,16 +47,21 @@ struct Tile {
   static_assert(BN % kRound == 0 && BM % kRound == 0 && kCopies % 2 == 0, "whole rounds, an even number");
 };
 
-// 16 (or 4) bytes a lane from memory to LDS: lane l's to `to` + 16 l (4 l), `to` uniform.  In
+// 16 (or 4) bytes a lane from memory to LDS: lane l's to `to` + 16 l (4 l), `to` uniform; ONCE:
+// with the hint that they are not read again.  In
 // assembly, because the compiler, which cannot tell the stages apart in a loop, otherwise waits
 // for copies of later stages before it reads an earlier one; all waits for copies are
 // stage_barrier's.  (The compiler sets M0 itself wherever it uses it.)  Five wait states: M0 before
 // its use, and a scalar register that a vector instruction may just have written.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(const u32x4_t& rs, uint8_t* to, uint32_t off) {
 #if defined(__HIP_DEVICE_COMPILE__)  // (the host pass has no such registers)
   typedef uint8_t __attribute__((address_space(3))) lds_byte;
   const uint32_t at = (uint32_t)(uintptr_t)(lds_byte*)to;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rs) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(at), "v"(off), "s"(rs) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rs) : "memory");
 #endif
 }
 __device__ __forceinline__ void copy4(const u32x4_t& rs, float* to, uint32_t off) {
@@ -185,11 +190,11 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, kbs = p.k_blocks, n = p.n;
 
-  if (threadIdx.x == 0) place[0] = Fp8Item{0, 0, 0, 0};
+  if (threadIdx.x == 0) place[0] = Fp8Item{};
   const Fp8Locator<T::kThreads> locator(p, T::BM, T::BN, 4, sums);
   if (locator.count == 0) return;
   locator.batch(0, 1, place);
-  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0)};
+  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0), uniform(place[0].once)};
   if (it.rows <= 0) return;  // not found: offsets that decrease
 
   // ---- copies: this thread moves piece lane % 8 of rows tid / 8 + kRound * j, swizzled, and
@@ -236,13 +241,24 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
     const u32x4_t w_now = within(w_rs, b), a_now = within(a_rs, b);
     const uint32_t here = (uint32_t)b * 128u;
     const uint32_t at_w = b == kbs - 1 ? last_w : here, at_a = b == kbs - 1 ? last_a : here;
+    const int w_end = end < T::kWRounds ? end : T::kWRounds;
+    // Weights that no other workgroup reads do not stay in the caches (512 tokens of 256 experts 139
+    // us instead of 154; experts of 64 rows, where a second tile often reads them too, 155 instead
+    // of 133 with the hint for all, 133 so.  Not in taller tiles: ragged experts 104 instead of 101.)
+    if (MT == 1 && it.once) {
 #pragma unroll
-    for (int j = from; j < end; ++j) {
+      for (int j = from; j < w_end; ++j) copy16<true>(w_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + at_w);
+    } else {
+#pragma unroll
+      for (int j = from; j < w_end; ++j) copy16(w_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + at_w);
+    }
+#pragma unroll
+    for (int j = from < T::kWRounds ? T::kWRounds : from; j < end; ++j) {
       // Eight activation rows that are not there stay what they were: they reach only results that
       // are not stored.  (Ragged experts of 273 rows on average 105 -> 101 us; but tiles of 64
       // rows copy their last row again, 512 tokens of 256 experts 165 us, left out 172.)
-      if (MT >= 2 && j >= T::kWRounds && T::kRound * (j - T::kWRounds) + 8 * wave >= it.rows) continue;
-      copy16(j < T::kWRounds ? w_now : a_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + (j < T::kWRounds ? at_w : at_a));
+      if (MT >= 2 && T::kRound * (j - T::kWRounds) + 8 * wave >= it.rows) continue;
+      copy16(a_now, to + (T::kRound * j + 8 * wave) * 128, off[j] + at_a);
     }
   };
   auto copy_scales = [&](float* to, int32_t b) { copy4(within(s_rs, b), to + 64 * wave, scale_off + (uint32_t)b * 4u); };
@@ -393,7 +409,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
 // runs along `span` tiles of 128 weight rows, a stage in LDS being one block of a tile.
 // Rows are found, read and scaled once and the copies never stop, where the kernel above spends
 // most of a short item on its start and its end.  Bound: the weights and results (6144 x 256,
-// 256 experts: 512 tokens 92 us, 4.9 TB/s; 4096 tokens 171 us, 4.7 TB/s).
+// 256 experts: 512 tokens 85 us, 5.3 TB/s; 4096 tokens 171 us, 4.7 TB/s).
 constexpr int kShortRing = 3;
 
 template <int KB, int MT>
@@ -407,11 +423,11 @@ void k_gemm_fp8_short(Fp8GemmArgs p) {
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, n = p.n;
 
-  if (threadIdx.x == 0) place[0] = Fp8Item{0, 0, 0, 0};
+  if (threadIdx.x == 0) place[0] = Fp8Item{};
   const Fp8Locator<256> locator(p, 64 * MT, 128 * p.span, 4, sums);
   if (locator.count == 0) return;
   locator.batch(0, 1, place);
-  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0)};
+  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0), uniform(place[0].once)};
   if (it.rows <= 0) return;  // not found: offsets that decrease
   const int32_t tiles = min(p.span, (n - it.n0 + 127) / 128), all = tiles * KB;
 
@@ -423,10 +439,16 @@ void k_gemm_fp8_short(Fp8GemmArgs p) {
     const u32x4_t now = u32x4_t{w_rs[0], w_rs[1], tile < tiles ? w_rs[2] : 0u, w_rs[3]};
     const int32_t at = b * 128 + 16 * piece;
     const uint32_t in_row = at < k ? (uint32_t)at : 0u;
+    uint32_t from[kCopies];
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) {
-      const int32_t row = min(it.n0 + 128 * tile + (tid >> 3) + 32 * j, n - 1);
-      copy16(now, to + (32 * j + 8 * wave) * 128, (uint32_t)row * (uint32_t)k + in_row);
+    for (int j = 0; j < kCopies; ++j)
+      from[j] = (uint32_t)min(it.n0 + 128 * tile + (tid >> 3) + 32 * j, n - 1) * (uint32_t)k + in_row;
+    if (it.once) {  // (6144 x 256: 85 us instead of 94; K = 512: 150 instead of 170)
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy16<true>(now, to + (32 * j + 8 * wave) * 128, from[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy16(now, to + (32 * j + 8 * wave) * 128, from[j]);
     }
   };
 #pragma unroll
@@ -583,6 +605,7 @@ hipError_t launch_short_sized(const Fp8GemmArgs& p, hipStream_t stream) {
 //     fill most of a round of 256 CUs (dense 8192^2, 2048 rows: 134 against 179; 8192 x 4096, 2500
 //     rows, 320 tiles: 123 against 106);
 //   128 x 128 else (4096 tokens of 256 experts: 269 against 276 with 64 x 128).
+//   (These without the hint for weights that are read once.)
 //   Up to four blocks the workgroups that run along the weights' tiles, of 64 or 128 rows as above,
 //     four tiles each or, so that there are 512 at least, two or three (the down projection 92
 //     against 117, of 4096 tokens 171 against 274; K = 512: 170 against 187 and 249 against 349;
