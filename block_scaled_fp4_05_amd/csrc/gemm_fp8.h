@@ -2,7 +2,8 @@
 // workgroup works, and how a result is stored.
 //
 // Products of two 16-row operands over one block of 128, which the block's two scales then
-// multiply: acc += d * (sa * sw), one multiply-add an element.  Weights are the first operand:
+// multiply: acc += d * (sa * sw), one multiply-add an element (rows whose sa * sw is no normal
+// number go another way, fp8_add_far).  Weights are the first operand:
 // lane l of the result then holds activation row l % 16, whose scale is one value a lane, and
 // weight rows 4 (l / 16) .. +3; the weight scale is uniform, since 16 rows at a multiple of
 // 16 lie in one block of 128.  Lane l gives 32 bytes of row l % 16 of each operand; which 32
@@ -56,6 +57,109 @@ __device__ __forceinline__ float4_t fp8_block_product(const Half32& w, const Hal
 #pragma unroll
   for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[i], a.v[i], d, 0, 0, 0);
   return d;
+}
+
+// What the matrix cores are given.
+template <bool EXACT>
+struct Operand {
+  typedef i32x8_t type;
+  static __device__ __forceinline__ const i32x8_t& of(const i32x8_t& x) { return x; }
+};
+template <>
+struct Operand<true> {
+  typedef Half32 type;
+  static __device__ __forceinline__ Half32 of(const i32x8_t& x) { return fp8_widen(x); }
+};
+
+// Where sa * sw is no normal FP32 number the result may be one all the same (blocks whose largest
+// magnitudes are near 2^-60 have scales near 2^-69 each).  Such "far" rows of a stage are added
+// apart, the scales' exponents with the block's products and only their mantissas multiplied, and
+// the usual way multiplies them with 0.  (For all rows it would make 8192^3 3% slower, 4096
+// tokens of 256 experts with an FP32 result 11%; a stage without far rows is checked for
+// them and no more.)
+
+// A scale as m 2^(e - 127): 1 <= |m| < 2 and 1 <= e <= 254, but for zeros, subnormal numbers,
+// infinities and NaN, which m keeps.
+struct Fp8Scale {
+  float m;
+  int32_t e;
+};
+
+__device__ __forceinline__ Fp8Scale fp8_split(float s) {
+  const uint32_t field = __builtin_bit_cast(uint32_t, s) >> 23 & 255u;
+  const int32_t e = (int32_t)min(max(field, 1u), 254u);
+  return Fp8Scale{__builtin_amdgcn_ldexpf(s, 127 - e), e};
+}
+
+__device__ __forceinline__ bool fp8_far(float scale) { return !__builtin_amdgcn_classf(scale, 0x108); }  // -, + normal
+
+// 2^(ea + ew - 254) times the block's products.  (The FP8 instruction takes an exponent for each row
+// of both operands, one for 32 elements, here all four of a row alike.)
+__device__ __forceinline__ float4_t fp8_far_product(const i32x8_t& w, const i32x8_t& a, int32_t ew, int32_t ea) {
+  const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, zero, 0, 0, 0, ew, 0, ea);
+}
+__device__ __forceinline__ float4_t fp8_far_product(const Half32& w, const Half32& a, int32_t ew, int32_t ea) {
+  float4_t d = fp8_block_product(w, a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_ldexpf(d[i], ea + ew - 254);
+  return d;
+}
+
+// Whether one of the 32 codes is not a zero.
+__device__ __forceinline__ bool fp8_any(const i32x8_t& x) {
+  int bits = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bits |= x[i];
+  return (bits & 0x7F7F7F7F) != 0;
+}
+
+// Adds a stage's far rows; scale: sa * sw, weights(t): the lane's 32 bytes of tile t.  Blocks of
+// zeros, whose scale is the least there is, and scales of zero give nothing and are passed over.
+// (No branch by lane: the matrix cores write the results of all lanes.)
+template <int NT, int MT, bool EXACT, bool PASS_ZEROS, typename W>
+__device__ __forceinline__ void fp8_add_far(float4_t (&acc)[NT][MT], const i32x8_t (&a)[MT], const float (&sa)[MT], float sw,
+                                            const float (&scale)[MT], W weights) {
+  bool small = false, large = false;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const bool far = fp8_far(scale[m]), below = fabsf(scale[m]) < 1.0f;
+    small |= far && below && sa[m] != 0.0f && sw != 0.0f && fp8_any(a[m]);
+    large |= far && !below;
+  }
+  const bool some_large = __builtin_amdgcn_ballot_w64(large) != 0;
+  if (!some_large && __builtin_amdgcn_ballot_w64(small) == 0) return;
+  const Fp8Scale by_w = fp8_split(sw);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const i32x8_t codes = weights(t);
+    if (PASS_ZEROS && !some_large && __builtin_amdgcn_ballot_w64(fp8_any(codes)) == 0) continue;
+    const auto w = Operand<EXACT>::of(codes);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const Fp8Scale by_a = fp8_far(scale[m]) ? fp8_split(sa[m]) : Fp8Scale{0.0f, 1};  // (keeps d finite)
+      const float4_t d = fp8_far_product(w, Operand<EXACT>::of(a[m]), by_w.e, by_a.e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][m][i] = __builtin_fmaf(d[i], by_a.m * by_w.m, acc[t][m][i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// 0 instead of the scales of far rows.
+template <int MT>
+__device__ __forceinline__ void fp8_drop_far(float (&scale)[MT]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m) scale[m] = fp8_far(scale[m]) ? 0.0f : scale[m];
+}
+
+// Whether the wavefront has far rows.
+template <int MT>
+__device__ __forceinline__ bool fp8_some_far(const float (&scale)[MT]) {
+  bool far = false;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) far |= fp8_far(scale[m]);
+  return __builtin_expect(__builtin_amdgcn_ballot_w64(far) != 0, 0);
 }
 
 // Where a workgroup works (uniform).

@@ -94,6 +94,10 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
     s.sw = ((sconst_f32)w_sf)[in ? b : b1 - 1];
   };
   auto multiply = [&](const Stage<NT, MT>& s) {
+    float scale[MT], by[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) by[m] = scale[m] = s.sa[m] * s.sw;
+    fp8_drop_far(by);
     Half32 a[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) a[m] = fp8_widen(s.a[m]);
@@ -103,11 +107,12 @@ __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const float4_t d = fp8_block_product(w, a[m]);
-        const float scale = s.sa[m] * s.sw;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][m][i] = __builtin_fmaf(d[i], scale, acc[t][m][i]);
+        for (int i = 0; i < 4; ++i) acc[t][m][i] = __builtin_fmaf(d[i], by[m], acc[t][m][i]);
       }
     }
+    if (fp8_some_far(scale))
+      fp8_add_far<NT, MT, true, false>(acc, s.a, s.sa, s.sw, scale, [&](int t) { return s.w[t]; });
   };
   if (b0 < b1) {
 #pragma unroll

@@ -89,18 +89,6 @@ __device__ __forceinline__ void stage_barrier() {
 #endif
 }
 
-// What the matrix cores are given.
-template <bool EXACT>
-struct Operand {
-  typedef i32x8_t type;
-  static __device__ __forceinline__ const i32x8_t& of(const i32x8_t& x) { return x; }
-};
-template <>
-struct Operand<true> {
-  typedef Half32 type;
-  static __device__ __forceinline__ Half32 of(const i32x8_t& x) { return fp8_widen(x); }
-};
-
 // Order of a tile's instructions: a product, then the additions of an earlier one.
 template <int MT>
 __device__ __forceinline__ void interleave() {
@@ -313,9 +301,17 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
           if (z1) now_a[m][4 + i] = 0;
         }
     }
-    float scale[MT];
+    float scale[MT], sa[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) scale[m] = scales[i][16 * (MT * wm + m) + r] * next_w;
+    for (int m = 0; m < MT; ++m) {
+      sa[m] = scales[i][16 * (MT * wm + m) + r];
+      scale[m] = sa[m] * next_w;
+    }
+    if (fp8_some_far(scale)) {
+      fp8_add_far<8, MT, EXACT, true>(acc, now_a, sa, next_w, scale,
+                                      [&](int t) { return fragment(cur, 128 * wn + tile_row(t, 0), at_w); });
+      fp8_drop_far(scale);
+    }
     next_w = ((sconst_f32)w_sf)[b + 1 < kbs ? b + 1 : b];
     operand_t ao[MT];
 #pragma unroll
@@ -413,7 +409,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
 constexpr int kShortRing = 3;
 
 template <int KB, int MT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 3)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(KB * MT <= 4 ? 3 : 2, 3)))
 void k_gemm_fp8_short(Fp8GemmArgs p) {
   constexpr int R = kShortRing, kCopies = 4, WD = 4;
   __shared__ __align__(1024) uint8_t stages[R][128 * 128];
@@ -482,12 +478,13 @@ void k_gemm_fp8_short(Fp8GemmArgs p) {
   const float* const w_sf = p.w_sf + ((int64_t)it.e * p.n_blocks + it.n0 / kFp8Block) * KB;  // of stage s at s
   const int at_w = tile_row(0, r) * 128 + 16 * (g ^ (r >> 1));
   i32x8_t w[WD];
-  auto read_w = [&](const uint8_t* from, int t) {
+  auto fragment = [&](const uint8_t* from, int t) {
     const uint8_t* const row = from + tile_row(t, 0) * 128;
     const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(row + at_w);
     const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(row + (at_w ^ 64));
-    w[t % WD] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
+  auto read_w = [&](const uint8_t* from, int t) { w[t % WD] = fragment(from, t); };
   auto after = [](int x) { return x + 1 == R ? 0 : x + 1; };
   float4_t acc[8][MT], d[MT];
   float next_w = ((sconst_f32)w_sf)[0];
@@ -500,6 +497,10 @@ void k_gemm_fp8_short(Fp8GemmArgs p) {
     float scale[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) scale[m] = sa[b][m] * next_w;
+    if (fp8_some_far(scale)) {
+      fp8_add_far<8, MT, false, true>(acc, a[b], sa[b], next_w, scale, [&](int t) { return fragment(cur, t); });
+      fp8_drop_far(scale);
+    }
     next_w = ((sconst_f32)w_sf)[s + 1 < all ? s + 1 : s];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
