@@ -55,8 +55,8 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // take thirty, and these modes are bound by instructions: the gradient of 5003 rows of 2 x 1424
 // took 24 us).  e^-x = 2^t (1 + r ln 2) with t = RN(-x log2 e) and r what t lost: the
 // product's rounding and the constant's.  x is kept within +-88, where 2^t neither overflows nor
-// vanishes; beyond, the sigmoid is within 6e-39 of 0 or 1.  A NaN is the caller's to keep: its
-// other factor is x.
+// vanishes; beyond, the sigmoid is within 6e-39 of 0 or 1, and the reciprocal instruction gives 0
+// for one below 2^-126.  A NaN is the caller's to keep: its other factor is x.
 __device__ __forceinline__ float sigmoid(float x) {
   const float c = __builtin_amdgcn_fmed3f(x, -88.0f, 88.0f);
   const float t = c * -0x1.715476p+0f;

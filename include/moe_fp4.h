@@ -501,8 +501,8 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
  * has an infinite scale and stands for NaN throughout.
  *   swiglu = 0               v = x, k columns.
  *   swiglu = 1, grad NULL    x has 2k columns, gate and up: v = silu(gate) * up, k columns, in
- *                            FP32, silu(g) = g / (1 + e^-g), e^-g taken for g within +-88 (so
- *                            an infinite gate, of either sign, stands for an infinity).
+ *                            FP32, silu(g) = g / (1 + e^-g); 1 / (1 + e^-g) counts as 0 below
+ *                            2^-126 (g < -87.3), so that a gate of -inf stands for a NaN.
  *   swiglu = 1, grad         its gradient, 2k columns: v = [grad * up * s (1 + gate (1 - s)) |
  *                            grad * silu(gate)], s = 1 / (1 + e^-gate), in FP32; the blocks run
  *                            over all 2k columns.
