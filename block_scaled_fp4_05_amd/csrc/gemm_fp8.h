@@ -183,106 +183,82 @@ inline int64_t fp8_most_items(const Fp8GemmArgs& p, int64_t bm) {
   return most * p.n_tiles;
 }
 
-// Finds a workgroup's items.  Every thread counts the items of a run of experts; the one whose run
-// holds an item names it.  In rounds of gridDim workgroups (a multiple of 8), items are numbered
-// so that an XCD (workgroup b runs on b % 8) gets consecutive ones, which share weight tiles
-// (M-tiles first) or activation rows.  band: M-tiles that are walked together with all N-tiles.
-// Every thread of the workgroup constructs it and calls batch (barriers inside).
+// A workgroup's item, one of no rows if it has none.  Every thread counts the items of a run of
+// experts; the one whose run holds the item names it.  Items are numbered so that an XCD
+// (workgroup b runs on b % 8) gets consecutive ones, which share weight tiles (M-tiles first) or
+// activation rows.  band: M-tiles that are walked together with all N-tiles.  Every thread of the
+// workgroup calls it (barriers inside), on a grid of at least as many workgroups as there can be
+// items, a multiple of 8.  (Offsets that go back and forth can make more: those are left out.)
 template <int NTHR>
-struct Fp8Locator {
-  const Fp8GemmArgs& p;
-  const int32_t bm, bn, band;
-  int32_t lo, hi, run, own;         // this thread's experts, the items before them and of them
-  int32_t start, second;            // first rows of its first expert and of the next
-  int32_t total, count;             // items of all workgroups, of this one
-  int32_t blocks, full, last, rounds;
-
-  __device__ __forceinline__ Fp8Locator(const Fp8GemmArgs& args, int32_t bm_, int32_t bn_, int32_t band_, int32_t* sums)
-      : p(args), bm(bm_), bn(bn_), band(band_) {
-    constexpr int WAVES = NTHR / 64;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int32_t m_total = (int32_t)p.m_total;
-    lo = tid;
-    hi = tid == 0 ? 1 : tid;
-    start = run = 0;
-    second = m_total;
-    own = total = fp8_items(p, m_total, bm);
-    if (p.offsets) {
-      const int32_t E = p.experts, per = (E + NTHR - 1) / NTHR;
-      lo = min(tid * per, E);
-      hi = min(lo + per, E);
-      own = 0;
-      const int32_t first = p.offsets[lo], next0 = p.offsets[min(lo + 1, E)];  // (both on their way at once)
-      start = clamp_off(first, m_total);
-      second = clamp_off(next0, m_total);
-      if (lo < hi) own = fp8_items(p, second - start, bm);
-      int32_t at = second;
-      for (int32_t e = lo + 1; e < hi; ++e) {
-        const int32_t next = clamp_off(p.offsets[e + 1], m_total);
-        own += fp8_items(p, next - at, bm);
-        at = next;
-      }
-      int32_t incl = own;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int32_t t = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += t;
-      }
-      if (lane == 63) sums[wave] = incl;
-      __syncthreads();
-      total = 0;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        if (w < wave) run += sums[w];
-        total += sums[w];
-      }
-      run += incl - own;
-      total = uniform(total);
-    }
-    // (Two axes, since one holds fewer than 2^32 threads.)
-    const int32_t block = blockIdx.y * gridDim.x + blockIdx.x;
-    blocks = gridDim.x * gridDim.y;
-    rounds = (total + blocks - 1) / blocks;
-    count = full = last = 0;
-    if (rounds > 0) {
-      const int32_t rest = total - (rounds - 1) * blocks;
-      full = logical_block(block, blocks, blocks);
-      last = logical_block(block, blocks, rest);
-      count = rounds - 1 + (last < rest ? 1 : 0);
-    }
-  }
-
-  // Items j0 .. j0 + n - 1 of this workgroup into ring[j % (2 n)].
-  __device__ __forceinline__ void batch(int32_t j0, int32_t n, Fp8Item* ring) const {
-    const int32_t m_total = (int32_t)p.m_total;
-    int32_t at = start, first = run;
-    int32_t j = j0;
-    for (int32_t e = lo; e < hi; ++e) {
-      const int32_t next = e == lo ? second : clamp_off(p.offsets[e + 1], m_total);
-      const int32_t rows = next - at, items = fp8_items(p, rows, bm);
-      for (; j < j0 + n && j < count; ++j) {
-        const int32_t item = j * blocks + (j == rounds - 1 ? last : full);
-        if (item >= first + items) break;
-        if (item < first) continue;
-        const int32_t local = item - first, mts = (rows + bm - 1) / bm;
-        int32_t mt, nt;
-        if (mts <= band) {
-          nt = local / mts;
-          mt = local - nt * mts;
-        } else {
-          const int32_t per_band = band * p.n_tiles, b = local / per_band, within = local - b * per_band;
-          const int32_t tall = min(band, mts - b * band);
-          nt = within / tall;
-          mt = b * band + within - nt * tall;
-        }
-        ring[j % (2 * n)] = Fp8Item{e, at + mt * bm, min(bm, rows - mt * bm), nt * bn, mts == 1};
-      }
-      first += items;
+__device__ __forceinline__ Fp8Item fp8_item(const Fp8GemmArgs& p, int32_t bm, int32_t bn, int32_t band) {
+  constexpr int WAVES = NTHR / 64;
+  __shared__ int32_t sums[WAVES];
+  __shared__ Fp8Item place;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t m_total = (int32_t)p.m_total;
+  if (tid == 0) place = Fp8Item{};
+  int32_t lo = tid, hi = tid == 0 ? 1 : tid;  // this thread's experts
+  int32_t start = 0, second = m_total;        // first rows of its first expert and of the next
+  int32_t run = 0;                            // the items before them
+  int32_t total = fp8_items(p, m_total, bm);
+  if (p.offsets) {
+    const int32_t E = p.experts, per = (E + NTHR - 1) / NTHR;
+    lo = min(tid * per, E);
+    hi = min(lo + per, E);
+    const int32_t first = p.offsets[lo], next0 = p.offsets[min(lo + 1, E)];  // (both on their way at once)
+    start = clamp_off(first, m_total);
+    second = clamp_off(next0, m_total);
+    int32_t own = lo < hi ? fp8_items(p, second - start, bm) : 0;
+    int32_t at = second;
+    for (int32_t e = lo + 1; e < hi; ++e) {
+      const int32_t next = clamp_off(p.offsets[e + 1], m_total);
+      own += fp8_items(p, next - at, bm);
       at = next;
     }
+    int32_t incl = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t t = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += t;
+    }
+    if (lane == 63) sums[wave] = incl;
     __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      if (w < wave) run += sums[w];
+      total += sums[w];
+    }
+    run += incl - own;
+    total = uniform(total);
   }
-};
+  // (Two axes, since one holds fewer than 2^32 threads.)
+  const int32_t blocks = gridDim.x * gridDim.y;
+  const int32_t item = logical_block(blockIdx.y * gridDim.x + blockIdx.x, blocks, total);
+  if (item >= total) return Fp8Item{};
+  for (int32_t e = lo, at = start; e < hi; ++e) {
+    const int32_t next = e == lo ? second : clamp_off(p.offsets[e + 1], m_total);
+    const int32_t rows = next - at, local = item - run, items = fp8_items(p, rows, bm);
+    if (local >= 0 && local < items) {
+      const int32_t mts = (rows + bm - 1) / bm;
+      int32_t mt, nt;
+      if (mts <= band) {
+        nt = local / mts;
+        mt = local - nt * mts;
+      } else {
+        const int32_t per_band = band * p.n_tiles, b = local / per_band, within = local - b * per_band;
+        const int32_t tall = min(band, mts - b * band);
+        nt = within / tall;
+        mt = b * band + within - nt * tall;
+      }
+      place = Fp8Item{e, at + mt * bm, min(bm, rows - mt * bm), nt * bn, mts == 1};
+    }
+    run += items;
+    at = next;
+  }
+  __syncthreads();
+  return Fp8Item{uniform(place.e), uniform(place.row0), uniform(place.rows), uniform(place.n0), uniform(place.once)};
+}
 
 // Four consecutive columns of a result row, rounded to nearest even.
 __device__ __forceinline__ void fp8_store4(const Fp8GemmArgs& p, int64_t row, int32_t col, const float4_t& v) {

@@ -33,14 +33,8 @@ struct Stage {
 template <int NT, int MT, int W, int D>
 __global__ __launch_bounds__(W * 64) void k_gemm_fp8_stream(Fp8GemmArgs p) {
   extern __shared__ __align__(16) char smem[];
-  __shared__ int32_t counts[W];
-  __shared__ Fp8Item place[2];
-  if (threadIdx.x == 0) place[0] = Fp8Item{};
-  const Fp8Locator<W * 64> locator(p, 16 * MT, 16 * NT, INT32_MAX, counts);
-  if (locator.count == 0) return;
-  locator.batch(0, 1, place);
-  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0), uniform(place[0].once)};
-  if (it.rows <= 0) return;  // not found: offsets that decrease
+  const Fp8Item it = fp8_item<W * 64>(p, 16 * MT, 16 * NT, INT32_MAX);
+  if (it.rows <= 0) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, kbs = p.k_blocks, n = p.n;

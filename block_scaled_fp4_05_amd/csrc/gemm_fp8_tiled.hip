@@ -171,19 +171,13 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   constexpr int WD = T::WD, AD = T::AD;
   __shared__ __align__(1024) uint8_t stages[R][T::kStage];
   __shared__ __align__(1024) float scales[R][T::kScales];  // of the stages' activation rows
-  __shared__ Fp8Item place[2];
-  __shared__ int32_t sums[T::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int wn = wave % WN, wm = wave / WN;
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, kbs = p.k_blocks, n = p.n;
 
-  if (threadIdx.x == 0) place[0] = Fp8Item{};
-  const Fp8Locator<T::kThreads> locator(p, T::BM, T::BN, 4, sums);
-  if (locator.count == 0) return;
-  locator.batch(0, 1, place);
-  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0), uniform(place[0].once)};
-  if (it.rows <= 0) return;  // not found: offsets that decrease
+  const Fp8Item it = fp8_item<T::kThreads>(p, T::BM, T::BN, 4);
+  if (it.rows <= 0) return;
 
   // ---- copies: this thread moves piece lane % 8 of rows tid / 8 + kRound * j, swizzled, and
   // wavefront w the scales of activation rows 64 w ...
@@ -413,18 +407,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(KB * MT <= 
 void k_gemm_fp8_short(Fp8GemmArgs p) {
   constexpr int R = kShortRing, kCopies = 4, WD = 4;
   __shared__ __align__(1024) uint8_t stages[R][128 * 128];
-  __shared__ Fp8Item place[2];
-  __shared__ int32_t sums[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int32_t k = p.k, n = p.n;
 
-  if (threadIdx.x == 0) place[0] = Fp8Item{};
-  const Fp8Locator<256> locator(p, 64 * MT, 128 * p.span, 4, sums);
-  if (locator.count == 0) return;
-  locator.batch(0, 1, place);
-  const Fp8Item it = {uniform(place[0].e), uniform(place[0].row0), uniform(place[0].rows), uniform(place[0].n0), uniform(place[0].once)};
-  if (it.rows <= 0) return;  // not found: offsets that decrease
+  const Fp8Item it = fp8_item<256>(p, 64 * MT, 128 * p.span, 4);
+  if (it.rows <= 0) return;
   const int32_t tiles = min(p.span, (n - it.n0 + 127) / 128), all = tiles * KB;
 
   // ---- copies of weights, as in the kernel above
