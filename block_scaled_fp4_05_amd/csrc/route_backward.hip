@@ -121,7 +121,6 @@ __global__ __launch_bounds__(kThreads) void k_route_backward(RouteBackwardArgs a
         term = w * left * (d - reduce<L>(valid ? w * d : 0.0f, add));
       } else {
         term = (l > 0.0f ? 1.0f : small) / whole * left * d;
-        if (l != l) term = l;
       }
     } else {
       const float m = reduce<L>(l, larger);

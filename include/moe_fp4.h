@@ -636,7 +636,9 @@ int moe_fp4_combine_backward(const void* dout, int dout_dtype, int64_t num_token
  *
  * and 0 for the other experts, in FP32, rounded once to dtype.  A slot whose id is outside [0,
  * num_experts) plays no part.  A token whose chosen logits (SOFTMAX without renormalize: all its
- * logits) are all -inf has the formula's NaN.  Deterministic.
+ * logits) are all -inf has the formula's NaN (SIGMOID without renormalize: 0).  A NaN, or with
+ * SOFTMAX a +inf, among the logits that a token's formula reads makes NaN of what depends on it;
+ * with SIGMOID an infinite logit has gradient 0.  Deterministic.
  *   logits     device, [tokens][ld] of dtype (BF16, FP32 or FP16), aligned to its element.
  *   ids, dweights device, [tokens][topk] int32 / float, topk 1 .. 32.
  *   dlogits    device, [tokens][ld_out] of dtype; columns >= num_experts are not touched.
