@@ -255,7 +255,7 @@ struct Fp8QuantArgs {
   uint8_t* q;  // [rows][k]
   float* sf;   // [rows][k in blocks]
   FastDiv per_row;  // by the blocks of a row
-  uint32_t blocks;  // of all rows, below 2^31 - 2^16
+  uint32_t blocks;  // of all rows, at most 2^29 - 2^17
   int64_t rows;
   int32_t k;        // columns of q
   int32_t dtype, swiglu, pow2;

@@ -513,7 +513,7 @@ int moe_fp4_route(const void* logits, int dtype, int64_t tokens, int32_t num_exp
  * Deterministic.
  * Errors: NULL, SHAPE (rows < 0, k < 1, k % 16, a pitch below its row), ALIGN, ARG (in_dtype,
  * swiglu or power_of_two not 0 or 1, grad without swiglu, q or sf overlapping another buffer),
- * UNSUPPORTED (2^29 - 2^17 blocks or more, k > 2^29 - 1024), HIP.
+ * UNSUPPORTED (more than 2^29 - 2^17 blocks, k >= 2^29 - 1024), HIP.
  */
 int moe_fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t k, int64_t ld_x, int swiglu,
                      const void* grad, int64_t ld_grad, int power_of_two, uint8_t* q, float* sf,
@@ -560,7 +560,7 @@ int moe_fp8_quantize_weights(const void* w, int in_dtype, int32_t num_experts, i
  *                  element, ldo >= n (stores are widest with 16-byte aligned rows).
  * Errors: NULL, SHAPE (num_experts, n or k < 1, m_total < 0, ldo < n, too few a_rows), ALIGN, ARG
  * (out_dtype, out overlapping an operand), UNSUPPORTED (k % 16, k > 2^22, num_experts > 8192,
- * n * k >= 2^31 - 4096, a_rows * k too with a row index, ldo > 2^20, m_total above about 2^29, or
+ * n * k >= 2^31 - 4096, a_rows * k too with a row index, ldo > 2^20, m_total >= 2^29 - 1024, or
  * (m_total / 16 + E) * n / 16 above 2^31), HIP.
  */
 int moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_sf, int64_t a_rows,
@@ -616,7 +616,7 @@ int moe_fp4_dispatch_backward(const void* dy, int dtype, int64_t m_total, int64_
  * Deterministic.
  * Errors: NULL, SHAPE (sizes < 0, topk or n < 1, a pitch below n), ALIGN, ARG (dout_dtype, drows
  * or dweights overlapping another buffer), UNSUPPORTED (n % 16, topk > 1024, num_tokens > 2^23,
- * m_total above 2^27), HIP.
+ * m_total > 2^27 - 257), HIP.
  */
 int moe_fp4_combine_backward(const void* dout, int dout_dtype, int64_t num_tokens, int64_t n, int64_t ld_dout,
                              const uint16_t* rows, int64_t ld_rows, int64_t m_total,
