@@ -3,7 +3,9 @@
 //   out[r][j] = sum_b sa[src(r)][b] sw[e][j / 128][b] sum_{k in block b} A[src(r)][k] W[e][j][k]
 //
 // Bound: the weight stream, one byte an element (up to some 64 rows give few operations a
-// byte; one token of 256 experts of 512 x 6144, top-8: 8.2 us, most of it latency).  A workgroup owns 16 NT weight rows and up to 16 MT activation rows of one expert;
+// byte; one token of 256 experts of 512 x 6144, top-8: 8.2 to 8.4 us, most of it latency: the offsets,
+// then two rounds of weights, since a wavefront has three of its six blocks in flight).  A
+// workgroup owns 16 NT weight rows and up to 16 MT activation rows of one expert;
 // its W wavefronts split K, each with D blocks of 128 in flight in registers, and their sums
 // meet in LDS in wavefront order (no atomics: the same inputs give the same bits).
 #include <hip/hip_runtime.h>
@@ -15,8 +17,8 @@ namespace moe_fp4 {
 namespace {
 
 // 32 bytes of a row: the 16-byte pieces g and 4 + g of a block.  (Two loads share a 128-byte
-// line: the hint that drops a line after its first use made dense 6144 x 6144 of one token 14.7
-// us instead of 10.9.)
+// line: the hint that drops a line after its first use made dense 6144 x 6144 of one token four
+// microseconds slower, 14.7 to 10.9 then.)
 __device__ __forceinline__ i32x8_t load32(rsrc_t rs, uint32_t off0, uint32_t off1, int32_t k) {
   const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(rs, off0, k, 0);
   const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(rs, off1, k, 0);
@@ -163,9 +165,11 @@ hipError_t launch(Fp8GemmArgs p, hipStream_t stream) {
 
 // The few-row kernel for fewer than four rows an expert, and while tiles of 64 x 128 would leave
 // CUs without work (its K split keeps them loading).  Both sides in us: 256 experts of 512 x 6144,
-// top-8, one token 9.3 against 31 with tiles, eight 36 and 53, 64 (two rows an expert) 109 and
-// 107, 512 (16 rows) 225 and 163; 64 experts of 2048 x 4096, three rows 82 and 113, 32 rows 145 and
-// 138; dense 8192 x 6144, 64 rows (128 tiles) 22.7 and 31, 128 rows (192 tiles) 32 and 31.
+// top-8, one token 8.4 against 30 with tiles, four 20 and 30, eight 36 and 33, 32 (one row an
+// expert) 80 and 77, 64 107 and 93, 96 (three rows) 120 and 112, 512 (16 rows) 199 and 141; 64 experts
+// of 2048 x 4096, one row 60 and 77, three 85 and 97, four 90 and 99, 16 134 and 108; dense
+// 8192 x 6144, 64 rows (128 tiles) 23.4 and 33, 128 rows (192 tiles) 31.6 and 31.5.  (Where the
+// tiles are ahead below four rows, the few-row kernel's exact sums are kept.)
 hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts;
   const int64_t rows = (p.m_total + p.experts - 1) / p.experts;
@@ -173,14 +177,14 @@ hipError_t launch_grouped_gemm_fp8(const Fp8GemmArgs& p, hipStream_t stream) {
   const bool few = p.m_total < 4 * (int64_t)p.experts || tiles < 96 || (rows <= 64 && tiles < 224);
   const int64_t items = (p.m_total / 16 + experts) * ((p.n + 15) / 16);
   if (!few || items > kFewItems) return launch_gemm_fp8_tiled(p, stream);
-  // Activation rows of a workgroup: 16, 32, or 64 above that (dense 8192 x 6144, 32 rows: 17.4 with
-  // room for 32, 19 for 16; 64 rows: 22.7 with 32, 26 with 64; 128 rows: 32 with 64, 42 with 32).
+  // Activation rows of a workgroup: 16, 32, or 64 above that (dense 8192 x 6144, 32 rows: 17.8 with
+  // room for 32, 18.7 for 16; 64 rows: 23.4 with 32, 31.6 with 64; 128 rows: 31.6 with 64, 41 with 32).
   if (rows > 64) return launch<4, 4, 4, 1>(p, stream);
   if (rows > 32) return launch<4, 2, 4, 1>(p, stream);
   if (rows > 16) return launch<2, 2, 4, 2>(p, stream);
   // Weight rows: 16 while that is about one item a CU, 32 up to twice that, else 64 (one token
-  // above: 9.3, 11.4 and 17; dense 6144 x 6144, 16 rows: 18, 13.4 and 18; four tokens above:
-  // 24, 20.4 and 19.2).
+  // above: 8.4, 10.9 and 16; dense 6144 x 6144, 16 rows: 17.8, 13.4 and 18.4; four tokens above:
+  // 24.1, 20.3 and 19.9).
   if (items <= 320) return launch<1, 1, 8, 3>(p, stream);
   return items <= 640 ? launch<2, 1, 8, 2>(p, stream) : launch<4, 1, 4, 2>(p, stream);
 }

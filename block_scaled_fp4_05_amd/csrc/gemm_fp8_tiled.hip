@@ -1,9 +1,10 @@
 // FP8 block-scaled grouped product for experts of many rows and the dense case
 // (moe_grouped_gemm_fp8), tiles of BM activation rows x BN weight rows a workgroup.
 //
-// Bound: the matrix cores for large dense products (8192^3: 488-512 us, 2.2 PFLOP/s), the weight stream
-// for experts of some 16 rows (512 tokens of 256 experts of 512 x 6144: 139 us, 5.9 TB/s), the copies'
-// requests between them (60 experts of 273 rows, 1444 x 1552: 99 us).  A stage is one block of 128
+// Bound: the matrix cores for large dense products (8192^3: 480-512 us, 2.2 PFLOP/s), the weight stream
+// for experts of some 16 rows (512 tokens of 256 experts of 512 x 6144: 140 us, 5.8 TB/s), the copies
+// between them (4096 tokens of the same 253 us; 60 experts of 273 rows, 1444 x 1552: 99 us), with an
+// FP32 result the conversions (4096 tokens 316 us, 4096^3 135).  A stage is one block of 128
 // of every row of the tile, copied from memory straight into LDS (no registers) while the stage before
 // it is multiplied.
 // Each wavefront owns 128 weight rows x 16 MT activation rows, so a stage takes one weight scale
@@ -273,7 +274,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
   // tiles first, which spills.
   // A stage's copies are issued in four parts.  256 x 256: behind the barrier (tiles 6 and 7) and in
   // the next stage's tiles 0 and 1, so that a wavefront's products do not queue behind eight of
-  // them (8192^3: 486 us, with all behind the barrier 509); smaller tiles behind the barrier, since
+  // them (8192^3: 5% less than with all behind the barrier); smaller tiles behind the barrier, since
   // what they wait for is the copies (4096 tokens of 256 experts: 259 us, spread 277).
   constexpr int kPart = MT >= 3 ? T::kCopies / 4 : T::kCopies / 2;
   constexpr int kLeft = (R - 2) * (T::kCopies + 1);  // copies that may still be on their way
@@ -399,7 +400,7 @@ void k_gemm_fp8_tiled(Fp8GemmArgs p) {
 // runs along `span` tiles of 128 weight rows, a stage in LDS being one block of a tile.
 // Rows are found, read and scaled once and the copies never stop, where the kernel above spends
 // most of a short item on its start and its end.  Bound: the weights and results (6144 x 256,
-// 256 experts: 512 tokens 85 us, 5.3 TB/s; 4096 tokens 171 us, 4.7 TB/s).
+// 256 experts: 512 tokens 82 us, 5.5 TB/s; 4096 tokens 172 us, 4.7 TB/s).
 constexpr int kShortRing = 3;
 
 template <int KB, int MT>
@@ -584,22 +585,22 @@ hipError_t launch_short_sized(const Fp8GemmArgs& p, hipStream_t stream) {
 }
 
 // The tile by the average rows of an expert; both sides in us:
-//   64 x 128 below 96 rows (6144 x 256, 32 rows: 136 against 176 with 128 x 128), and while 128 x
-//     128 would leave CUs without two workgroups (dense 8192 x 6144, 256 rows: 33 against 39); with
+//   64 x 128 below 96 rows (6144 x 256, 32 rows: 123 against 153 with 128 x 128), and while 128 x
+//     128 would leave CUs without two workgroups (dense 8192 x 6144, 256 rows: 34 against 38); with
 //     three stages in LDS, two workgroups a CU instead of three, from
-//     32 blocks (512 tokens of 256 experts, K = 6144: 154 against 165 with two stages; K = 4096:
-//     190 and 192; K = 1024: 113 and 111; FP32 results the same);
-//   256 x 256 from 384 rows (8 experts of 8192 x 4096, 512 rows: 208 against 223 with 128 x 128;
-//     1024 rows: 342 against 414; 64 experts of 2048 x 4096, 256 rows: 260 against 253) where they
-//     fill most of a round of 256 CUs (dense 8192^2, 2048 rows: 134 against 179; 8192 x 4096, 2500
-//     rows, 320 tiles: 123 against 106);
-//   128 x 128 else (4096 tokens of 256 experts: 269 against 276 with 64 x 128).
-//   (These without the hint for weights that are read once.)
+//     32 blocks (512 tokens of 256 experts, 512 x 6144: 141 against 151 with two stages; 512 x 4096:
+//     114 and 131; 512 x 1024: 31 and 33; 6144 x 512: 187 and 173; FP32 results the same);
+//   256 x 256 from 384 rows (8 experts of 8192 x 4096, 512 rows: 147 against 200 with 128 x 128;
+//     1024 rows: 275 against 378; 64 experts of 2048 x 4096, 256 rows: 225 against 233, in another
+//     session 260 against 253) where they
+//     fill most of a round of 256 CUs (dense 8192^2, 2048 rows: 122 against 161; 8192 x 4096, 2500
+//     rows, 320 tiles: 110 against 101);
+//   128 x 128 else (4096 tokens of 256 experts, 512 x 6144: 253 against 266 with 64 x 128).
 //   Up to four blocks the workgroups that run along the weights' tiles, of 64 or 128 rows as above,
-//     four tiles each or, so that there are 512 at least, two or three (the down projection 92
-//     against 117, of 4096 tokens 171 against 274; K = 512: 170 against 187 and 249 against 349;
-//     dense 8192 x 8192 x 256 37 against 44; with eight tiles 96, 177, 175, 253 and 34); below 1024
-//     tiles those above (dense 4096 x 256, 512 rows: 6.7 against 8.4).
+//     four tiles each or, so that there are 512 at least, two or three (512 tokens of 256 experts,
+//     6144 x 256: 82 against 112, 4096 tokens 172 against 268; 6144 x 512: 153 against 173 and 252 against 347;
+//     dense 8192 x 8192 x 256 34 against 48; with eight tiles 84, 178, 156, 254 and 32); below 1024
+//     tiles those above (dense 4096 x 256, 512 rows: 7.1 both).
 template <bool EXACT>
 hipError_t launch_sized(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t experts = p.m_total < p.experts ? p.m_total : p.experts, avg = p.m_total / p.experts;

@@ -14,9 +14,10 @@
 // experts.  Its first lanes are its slots, which compute the slots' terms and put them into a row
 // of LDS (slots that name the same expert add up there, in slot order); every lane takes its
 // experts' terms from it and writes each element of the dense result once.  Four tokens a
-// wavefront share every instruction, and a reduction over 16 lanes needs no LDS.  Bound: the logits (softmax only) and the result, 2 to 8 bytes an expert, in
-// one pass of dependent steps (16384 tokens of 256 experts, softmax over all: 8 us; with 64 lanes a
-// token 32), and for short calls the launch.
+// wavefront share every instruction, and a reduction over 16 lanes needs no LDS.  Bound: the
+// logits (softmax only) and the result, 2 to 8 bytes an expert, in one pass of dependent steps
+// with five barriers of the workgroup around the terms (16384 tokens of 256 experts, softmax over
+// all: 8 us; with 64 lanes a token 32), and for short calls the launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -5,8 +5,8 @@
 //   moe_fp4_combine_backward   drows[token_rows[t][s]] = w[t][s] * dout[t]
 //                              dw[t][s] = sum_j rows[token_rows[t][s]][j] * dout[t][j]
 //
-// Bound: bytes (4096 tokens x 8 rows of 12 KB: dispatch 77 us, 5.9 TB/s; combine's gradient 172 us,
-// 5.0 TB/s).  Every result is written once by one thread in a fixed order (a token gathers
+// Bound: bytes (4096 tokens x 8 rows of 12 KB: dispatch 77 us, 5.9 TB/s, its gradient 89 us, 5.1 TB/s;
+// combine's gradient 172 us, 5.0 TB/s, into the same results pass after pass 157).  Every result is written once by one thread in a fixed order (a token gathers
 // its rows; nothing is scattered with atomics), so the same inputs give the same bits.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -28,8 +28,8 @@ constexpr int kWaves = kThreads / 64;
 // What the copies cost is the way of the tokens into the XCDs' L2s, as many bytes again as
 // the rows written: the slots of a token are far apart.  So a workgroup takes a slice of
 // a.lanes pieces of some rows, the XCDs (workgroup b runs on b % 8) have slices of their own,
-// and a slice of all tokens stays in an L2 while it is used: 4096 x 8 rows of 12 KB take 84
-// us, row by row 108.  With one row a token nothing is read twice, and rows go whole.
+// and a slice of all tokens stays in an L2 while it is used: 4096 x 8 rows of 12 KB take 77
+// us, row by row 106.  With one row a token nothing is read twice, and rows go whole.
 typedef u32x4_t any16_t __attribute__((aligned(1)));
 
 __global__ __launch_bounds__(kThreads) void k_dispatch(RowsArgs a) {
@@ -119,8 +119,8 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_backward(RowsArgs a) {
           for (int i = 0; i < N; ++i) v[s][i] = i < a.cols ? src[i] : (elem_t)0.0f;
         }
       }
-      // A slot without a row is passed over (not added as 0: -0 stays -0, and what another row
-      // holds plays no part).
+      // A slot without a row is passed over (no other row is read in its place, whose NaN would
+      // count).
 #pragma unroll
       for (int s = 0; s < kSlots; ++s)
         if (ok[s]) {
@@ -297,12 +297,12 @@ hipError_t combine_backward_dt(const CombineBackwardArgs& a, hipStream_t stream)
 template <bool F32>
 hipError_t combine_backward(const CombineBackwardArgs& a, hipStream_t stream) {
   // Four groups a token where one would leave SIMDs without a wavefront (4 tokens, 8 rows of
-  // 12 KB: 6.0 us instead of 9.0; 256: 12.6 instead of 13.6; 512: 21 instead of 19).
+  // 12 KB: 6.2 us instead of 9.0; 256: 12.4 instead of 13.3; 512: 20.4 instead of 18.5).
   if (a.num_tokens * (a.n <= 1024 ? 1 : 4) <= 1024) return combine_backward_dt<F32, 4, false>(a, stream);
   // Rows beyond half of the last-level cache's 256 MB are read past it: they are read once, and
   // what is written stays for its reader (pass after pass into the same results: 402 MB 157 us
-  // instead of 169, 268 MB 94 instead of 112; but 25 MB, still there when they are read, 17 us
-  // instead of 13.6).
+  // instead of 169, 268 MB 94 instead of 112; into new ones 172 and 116 both ways; but 25 MB,
+  // still there when they are read, 16.6 us instead of 13.4).
   return a.m_total * a.n * 2 >= 128 << 20 ? combine_backward_dt<F32, 1, true>(a, stream)
                                     : combine_backward_dt<F32, 1, false>(a, stream);
 }
@@ -315,10 +315,10 @@ hipError_t launch_dispatch(const RowsArgs& args, hipStream_t stream) {
   a.lanes = 64;
   while (a.lanes > 1 && a.lanes / 2 >= pieces) a.lanes /= 2;
   // By slices where a token has four rows or more (with three, 8192 x 3 of 12 KB, 95 us instead
-  // of 93): slices of which all tokens take half an L2 (4096 x 8 of 12 KB: 84 us, with a whole
-  // L2 87), but of two lines at least (16384 x 8 of 2 KB: 55 to 59 us with one, two and four),
-  // and of 1 KB where rows start inside lines, whose halves are written apart (4096 x 8 of
-  // 12 282 bytes: 155 us in slices of 512 bytes, 107 of 1 KB).
+  // of 93, in another session 95 of 102): slices of which all tokens take half an L2 (4096 x 8 of
+  // 12 KB: 77 us, with a whole L2 82), but of two lines at least (16384 x 8 of 2 KB: 57 us, 55
+  // with one, 72 with four), and of 1 KB where rows start inside lines, whose halves are written
+  // apart (4096 x 8 of 12 282 bytes: 152 us in slices of 512 bytes, 105 of 1 KB).
   a.by_slice = a.rows >= 4 * a.source_rows;
   const uint64_t starts = (uint64_t)reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.ld_out;
   if (a.by_slice && starts % 128 == 0)

@@ -870,7 +870,7 @@ def grouped_gemm_fp8(a_q, a_sf, w_q, w_sf, offsets, a_row_index=None, out=None, 
     """Grouped product of FP8 rows with FP8 weights in blocks of 128: a_q float8_e4m3fn
     [a_rows][k], a_sf float32 [a_rows][ceil(k / 128)] (quantize_fp8); w_q [E][n][k], w_sf
     [E][ceil(n / 128)][ceil(k / 128)] (quantize_fp8_weights); offsets int32 [E + 1]; a_row_index
-    int32 [m_total] or None.  m_total defaults to a_row_index's length, else a_rows.  Returns
+    int32 [m_total] or None; all contiguous.  m_total defaults to a_row_index's length, else a_rows.  Returns
     out [m_total][n] of out_dtype (or the given out's type); a new one belongs to the launch
     stream.  Rows outside the offsets are not written."""
     if stream is None and out is None and m_total is None and offsets is not None and \

@@ -547,7 +547,9 @@ int moe_fp8_quantize_weights(const void* w, int in_dtype, int32_t num_experts, i
  * block the products are exact and their sum FP32 for an FP32 out and for small problems (few
  * rows an expert, or few tiles); the others use the FP8 matrix cores, which cut each of eight
  * consecutive products 13 bits below the leading bit of the largest of them (about 1.5e-5 of a
- * result on Gaussian data, against a rounding of 2^-9 or 2^-12).  Deterministic.  Columns
+ * result on Gaussian data, against a rounding of 2^-9 or 2^-12; at most 7 * 2^-13 of the sum of
+ * each eight's largest magnitude).  So a row's 16-bit result may differ in its last bits
+ * between calls of few and of many rows.  Deterministic: the same call gives the same bits.  Columns
  * >= n and rows outside [off[0], off[E]) are not written; an empty expert writes nothing.
  *   a_q, a_sf      device, [a_rows][k] bytes, 16-byte aligned, and [a_rows][KB] floats.
  *   a_row_index    device, [m_total] int32 in [0, a_rows), or NULL for identity (then a_rows
